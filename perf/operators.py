@@ -40,10 +40,10 @@ def listed():
         _linear("linear tiny layer", 256, 512, 1024, "f32", "f32", "f32"),
         # odd sizes: rows that are not 16-byte aligned, blocks cut by both edges
         _linear("linear odd sizes", 333, 4999, 1111, "bf16", "bf16", "f32"),
-        # a 4096-token pass, down projection
-        _linear("linear 4096 tokens, down", 4096, 13824, 5120, "bf16", "bf16", "f32"),
-        # a 4096-token pass, up projection, power-of-two scales, fp32 out
-        _linear("linear 4096 tokens, up, e8m0", 4096, 5120, 13824, "bf16", "f32", "e8m0"),
+        # a 4096-token pass, down projection, power-of-two scales
+        _linear("linear 4096 tokens, down, e8m0", 4096, 13824, 5120, "bf16", "bf16", "e8m0"),
+        # a 4096-token pass, up projection, fp32 out
+        _linear("linear 4096 tokens, up", 4096, 5120, 13824, "bf16", "f32", "f32"),
         # the full token count of a video frame stack
         _linear("linear 57600 tokens, up", 57600, 5120, 13824, "bf16", "bf16", "f32"),
         # one token through a layer of many experts: eight of 64 are read
