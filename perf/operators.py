@@ -18,7 +18,7 @@ import torch
 own = False
 
 E4M3_MAX = 448.0
-TINY = 2.0 ** -126          # smallest scale: the smallest normal binary32 number
+TINY = 2.0 ** -60           # smallest scale: products of two scales stay normal binary32 numbers
 DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
@@ -91,10 +91,10 @@ def _gen(seed):
 
 
 def _pow2_code(amax):
-    """E8M0 code of the smallest power of two s with amax <= 448 s, s >= 2^-126."""
+    """E8M0 code of the smallest power of two s with amax <= 448 s, s >= 2^-60."""
     m, e = torch.frexp(amax)                 # amax = 2m * 2^(e-1), 448 = 1.75 * 2^8
     c = e - 9 + (m > 0.875).to(torch.int32) + 127
-    return torch.clamp(c, 1, 254).to(torch.uint8)
+    return torch.clamp(c, 127 - 60, 254).to(torch.uint8)
 
 
 def _quantized(n, rows, cols, std, scales, g):
@@ -276,10 +276,10 @@ def _linear64(st):
             b = x[:, j:j + 128]
             amax = b.abs().amax(dim=1, keepdim=True)
             if case["scales"] == "f32":     # binary32: amax / 448 rounded once
-                s = (amax / 448.0).float().double().clamp_min(2.0 ** -126)
+                s = (amax / 448.0).float().double().clamp_min(2.0 ** -60)
             else:
-                s = torch.exp2(torch.ceil(torch.log2((amax / 448.0).clamp_min(2.0 ** -126))))
-                s = torch.where(amax > 448.0 * s, 2 * s, torch.where((amax <= 224.0 * s) & (s > 2.0 ** -126), s / 2, s))
+                s = torch.exp2(torch.ceil(torch.log2((amax / 448.0).clamp_min(2.0 ** -60))))
+                s = torch.where(amax > 448.0 * s, 2 * s, torch.where((amax <= 224.0 * s) & (s > 2.0 ** -60), s / 2, s))
             x[:, j:j + 128] = _nearest64((b / s).float().double()) * s
         out[t0:t0 + 8192] = x @ w.t()
     return out
