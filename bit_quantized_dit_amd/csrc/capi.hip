@@ -10,20 +10,12 @@
 #include <numeric>
 #include <vector>
 
+#include "capi_util.h"
 #include "w4a4_internal.h"
 
 using namespace w4a4;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
-bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
-
-int dev_status(hipError_t e) { return e == hipSuccess ? W4A4_OK : W4A4_ERR_DEVICE; }
 
 int64_t weight_scale_bytes(int64_t d_out, int64_t k_pad, int layout) {
     if (layout == W4A4_WS_1X32) return d_out * (k_pad / 32);

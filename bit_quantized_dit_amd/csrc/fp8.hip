@@ -1,0 +1,225 @@
+// FP8 block quantization on gfx950: activations (one scale per token and 128 inputs) and
+// weights (one scale per 128 x 128 block) into E4M3 codes, in the order in which the
+// products of fp8gemm.hip and moe.hip read them.
+//
+//   s = max(fl32(amax / 448), 2^-60), or the smallest power of two >= 2^-60 with
+//   amax <= 448 s;  q = e4m3_rne(fl32(x / s)).
+//
+// fl32(x / s) is the double product x * RN64(1 / s) rounded to binary32: it lies within
+// 2^-52 (relative) of x / s, and a quotient of two binary32 numbers stays further than
+// that from every binary32 rounding midpoint, so the rounding lands on the same value
+// (quotients below the normal range become the code 0 either way).
+#include "w4a4_device.h"
+#include "w4a4_internal.h"
+
+namespace w4a4 {
+
+namespace {
+
+// Scale of a block from the bit pattern of its largest |x|.
+__device__ __forceinline__ float block_scale(uint32_t amax_bits, int kind) {
+    if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    if (kind == W4A4_FP8_SCALE_F32) return __builtin_fmaxf(__uint_as_float(amax_bits) / 448.0f, 0x1p-60f);
+    // amax = (1 + m / 2^23) 2^(e - 127), 448 = 1.75 * 2^8
+    const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)(e < 127 - 60 ? 127 - 60 : e) << 23);
+}
+
+// 16 values to 16 codes; a block whose scale is NaN has zero codes.
+__device__ __forceinline__ uint4 encode16(const float* x, float s) {
+    if (s != s) return make_uint4(0, 0, 0, 0);
+    const double rinv = 1.0 / (double)s;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = (float)((double)x[4 * i + j] * rinv);
+        int r = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], r, true);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Values p .. p + 15 of a row of `cols`, zero past its end; `vec`: the row starts on a
+// 16-byte boundary (p is a multiple of 16).
+__device__ __forceinline__ void load16(const float* row, int64_t p, int64_t cols, bool vec, float* x) {
+    if (vec && p + 16 <= cols) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(row + p + 4 * i);
+            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = p + i < cols ? row[p + i] : 0.0f;
+}
+__device__ __forceinline__ void load16(const uint16_t* row, int64_t p, int64_t cols, bool vec, float* x) {
+    if (vec && p + 16 <= cols) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + p + 8 * i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = p + i < cols ? bf16_to_f32(row[p + i]) : 0.0f;
+}
+
+// Activations.  A wavefront takes 8 tokens x one block of 128 inputs: lane l holds the 16
+// inputs 16 (l / 8) .. of token l % 8, whose codes are one 16-byte piece of the packed
+// order, and the pieces of 8 consecutive tokens are 128 contiguous bytes: every store
+// instruction writes whole cache lines.
+template <typename X>
+__global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__ x, int64_t T, int64_t d_in, int64_t nkb,
+                                                           int64_t items, int kind, int vec, uint8_t* __restrict__ aq,
+                                                           float* __restrict__ as, int64_t t_ld) {
+    const int lane = threadIdx.x & 63, tk = lane & 7, i = lane >> 3;
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (item >= items) return;
+    const int64_t tg = item / nkb, kb = item - tg * nkb;
+    const int64_t t = tg * 8 + tk;
+    const bool live = t < T;
+    float v[16];
+    load16(x + (live ? t : 0) * d_in, kb * 128 + i * 16, d_in, vec != 0, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[j]));
+#pragma unroll
+    for (int o = 8; o < 64; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    const float s = block_scale(m, kind);
+    const uint4 c = encode16(v, s);
+    if (!live) return;
+    uint8_t* dst = aq + ((t / 32) * (nkb * 2) + kb * 2 + (i >> 2)) * 2048 + (i & 1) * 1024 +
+                   ((((i >> 1) & 1) * 32) + (t & 31)) * 16;
+    *reinterpret_cast<uint4*>(dst) = c;
+    if (i == 0) as[kb * t_ld + t] = s;
+}
+
+// Weights: one workgroup per 128 x 128 block; thread = (row, half of the block's inputs).
+template <typename W>
+__global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, int64_t d_in, int64_t d_out, int64_t nkb,
+                                                       int64_t nnb, int64_t n_pad, int kind, int vec, uint8_t* __restrict__ codes,
+                                                       float* __restrict__ scales) {
+    __shared__ uint32_t wmax[4];
+    const int64_t b = blockIdx.x;
+    const int64_t mat = b / (nnb * nkb), nb = (b / nkb) % nnb, kb = b % nkb;
+    const int64_t row = nb * 128 + (threadIdx.x >> 1);
+    const int64_t p0 = kb * 128 + (threadIdx.x & 1) * 64;
+    float v[4][16];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (row < d_out) {
+            load16(w + (mat * d_out + row) * d_in, p0 + 16 * i, d_in, vec != 0, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[i][j]));
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
+    const float s = block_scale(m, kind);
+    if (threadIdx.x == 0) scales[b] = s;
+    if (row >= n_pad) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t p = p0 + 16 * i;
+        uint8_t* dst = codes + ((mat * (n_pad / 32) + row / 32) * (nkb * 2) + p / 64) * 2048 + ((p / 16) & 1) * 1024 +
+                       (((p / 32) & 1) * 32 + (row & 31)) * 16;
+        *reinterpret_cast<uint4*>(dst) = encode16(v[i], s);
+    }
+}
+
+// Codes of a checkpoint, row-major, into the packed order: one thread per 16-byte piece.
+__global__ __launch_bounds__(256) void fp8_reorder_kernel(const uint8_t* __restrict__ src, int64_t d_in, int64_t d_out,
+                                                          int64_t nkb, int64_t n_pad, int64_t pieces, int vec,
+                                                          uint8_t* __restrict__ codes) {
+    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (q >= pieces) return;
+    const int l = (int)(q & 63), h = (int)((q >> 6) & 1);
+    const int64_t run = q >> 7;                       // 32 rows x 64 inputs
+    const int64_t rb = run / (nkb * 2), kb = run - rb * (nkb * 2);
+    const int64_t mat = rb / (n_pad / 32), row = (rb - mat * (n_pad / 32)) * 32 + (l & 31);
+    const int64_t p = kb * 64 + (l >> 5) * 32 + h * 16;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < d_out) {
+        const uint8_t* s = src + (mat * d_out + row) * d_in + p;
+        if (vec && p + 16 <= d_in) {
+            v = *reinterpret_cast<const uint4*>(s);
+        } else {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i / 4] |= (p + i < d_in ? (uint32_t)s[i] : 0u) << (8 * (i & 3));
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    *reinterpret_cast<uint4*>(codes + q * 16) = v;
+}
+
+__global__ __launch_bounds__(256) void fp8_scales_kernel(const void* __restrict__ src, int64_t n, int kind,
+                                                         float* __restrict__ scales) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    if (kind == W4A4_FP8_SCALE_F32) {
+        scales[i] = reinterpret_cast<const float*>(src)[i];
+    } else {
+        const uint32_t c = reinterpret_cast<const uint8_t*>(src)[i];
+        scales[i] = __uint_as_float(c == 0xFFu ? 0x7FC00000u : c == 0 ? 0x00400000u : c << 23);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_in, int kind, uint8_t* aq, float* as,
+                               int64_t t_ld, hipStream_t st) {
+    const int64_t nkb = (d_in + 127) / 128, items = (T + 7) / 8 * nkb;
+    const dim3 grid((uint32_t)((items + 3) / 4));
+    if (x_dtype == W4A4_X_BF16)
+        hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, items,
+                           kind, d_in % 8 == 0 ? 1 : 0, aq, as, t_ld);
+    else
+        hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, items, kind,
+                           d_in % 4 == 0 ? 1 : 0, aq, as, t_ld);
+    return hipGetLastError();
+}
+
+hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d, uint8_t* codes, float* scales,
+                           hipStream_t st) {
+    const int64_t nkb = d.k_pad / 128, nnb = (d.d_out + 127) / 128;
+    const dim3 grid((uint32_t)(d.n_mat * nnb * nkb));
+    if (w_dtype == W4A4_X_BF16)
+        hipLaunchKernelGGL(fp8_pack_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)W, d.d_in, d.d_out, nkb, nnb,
+                           d.n_pad, d.scale_kind, d.d_in % 8 == 0 ? 1 : 0, codes, scales);
+    else
+        hipLaunchKernelGGL(fp8_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)W, d.d_in, d.d_out, nkb, nnb,
+                           d.n_pad, d.scale_kind, d.d_in % 4 == 0 ? 1 : 0, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_fp8_reorder(const uint8_t* src, const void* src_scales, const w4a4_fp8_packed& d, uint8_t* codes,
+                              float* scales, hipStream_t st) {
+    const int64_t nkb = d.k_pad / 128, pieces = d.n_mat * d.n_pad * d.k_pad / 16;
+    hipLaunchKernelGGL(fp8_reorder_kernel, dim3((uint32_t)((pieces + 255) / 256)), dim3(256), 0, st, src, d.d_in, d.d_out, nkb,
+                       d.n_pad, pieces, d.d_in % 16 == 0 ? 1 : 0, codes);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t n = d.n_mat * ((d.d_out + 127) / 128) * nkb;
+    hipLaunchKernelGGL(fp8_scales_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, src_scales, n, d.scale_kind,
+                       scales);
+    return hipGetLastError();
+}
+
+}  // namespace w4a4

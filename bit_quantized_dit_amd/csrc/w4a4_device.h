@@ -128,4 +128,14 @@ __device__ __forceinline__ uint32_t gelu_tanh_bf16x2_raw(float y0, float y1) {
 
 __device__ __forceinline__ uint16_t gelu_tanh_bf16(float y) { return (uint16_t)gelu_tanh_bf16x2(y, 0.0f); }
 
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+// 8 E4M3 codes (two words) widened to bf16, which is exact.
+__device__ __forceinline__ v8bf widen_e4m3(uint32_t lo, uint32_t hi) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 }  // namespace w4a4

@@ -70,4 +70,25 @@ hipError_t launch_dyn_gather(const uint16_t* W_t, const int32_t* O, int64_t d_in
 // W_t[j][n] = bf16_rne(W[n][j]), W fp32 [d_out][d_in]
 hipError_t launch_dyn_transpose(const float* W, int64_t d_in, int64_t d_out, uint16_t* W_t, hipStream_t st);
 
+// FP8 block-scaled layer (fp8.hip, fp8gemm.hip): activation codes and scales ([k_pad/128]
+// rows of t_ld scales), weight quantization, the reordering of a checkpoint's codes, the
+// product
+hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_in, int kind, uint8_t* aq, float* as,
+                               int64_t t_ld, hipStream_t st);
+hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d, uint8_t* codes, float* scales,
+                           hipStream_t st);
+hipError_t launch_fp8_reorder(const uint8_t* src, const void* src_scales, const w4a4_fp8_packed& d, uint8_t* codes,
+                              float* scales, hipStream_t st);
+hipError_t launch_fp8_gemm(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
+                           int y_dtype, hipStream_t st);
+
+// mixture of experts (moe.hip): the arrays of w4a4_moe_ws_layout
+struct MoeBuffers {
+    float *logits, *p;
+    uint16_t *xb, *h;
+    int32_t *ids, *count, *pairs;
+};
+hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, const MoeBuffers& b, void* Y, int y_dtype,
+                      hipStream_t st);
+
 }  // namespace w4a4

@@ -25,6 +25,13 @@ W4A4_WS_128X1_STRIPE = 2
 STATUS = {0: "W4A4_OK", 1: "W4A4_ERR_INVALID", 2: "W4A4_ERR_SHAPE", 3: "W4A4_ERR_ALIGN",
           4: "W4A4_ERR_DEVICE", 5: "W4A4_ERR_NONFINITE", 6: "W4A4_ERR_SCRATCH"}
 NOALLOC_SCRATCH_BYTES = 128 << 20    # W4A4_NOALLOC_SCRATCH_BYTES
+W4A4_FP8_SCALE_F32 = 0
+W4A4_FP8_SCALE_E8M0 = 1
+W4A4_Y_F32 = 0
+W4A4_Y_BF16 = 1
+W4A4_MOE_SILU_GATED = 0
+W4A4_MOE_GELU_TANH = 1
+MOE_MAX_T = 128                      # W4A4_MOE_MAX_T
 
 EXPORTS = ("w4a4_status_string", "w4a4_column_absmax", "w4a4_calibrate_scales", "w4a4_packed_size",
            "w4a4_pack_weights", "w4a4_workspace_layout", "w4a4_workspace_size",
@@ -33,7 +40,10 @@ EXPORTS = ("w4a4_status_string", "w4a4_column_absmax", "w4a4_calibrate_scales", 
            "w4a4_search_scratch_size", "w4a4_search_alpha_k", "w4a4_packed_dyn_size", "w4a4_pack_weights_dyn",
            "w4a4_workspace_dyn_layout", "w4a4_workspace_dyn_size", "w4a4_linear_dyn",
            "w4a4_ffn_workspace_layout", "w4a4_ffn_workspace_size", "w4a4_ffn_up_quantize", "w4a4_ffn_forward",
-           "w4a4_linear_noalloc")
+           "w4a4_linear_noalloc",
+           "w4a4_fp8_packed_size", "w4a4_fp8_pack_weights", "w4a4_fp8_pack_codes", "w4a4_fp8_workspace_layout",
+           "w4a4_fp8_workspace_size", "w4a4_fp8_quantize_activations", "w4a4_fp8_gemm_prequantized", "w4a4_fp8_linear",
+           "w4a4_moe_workspace_layout", "w4a4_moe_workspace_size", "w4a4_moe_forward")
 
 
 class W4A4Packed(ctypes.Structure):
@@ -63,6 +73,29 @@ class W4A4WsDynLayout(ctypes.Structure):
 class W4A4FfnWsLayout(ctypes.Structure):
     _fields_ = [("up", W4A4WsLayout), ("down", W4A4WsLayout), ("up_base", ctypes.c_size_t),
                 ("down_base", ctypes.c_size_t), ("rinv", ctypes.c_size_t), ("total", ctypes.c_size_t)]
+
+
+class W4A4Fp8Packed(ctypes.Structure):
+    _fields_ = [("n_mat", ctypes.c_int64), ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64),
+                ("k_pad", ctypes.c_int64), ("n_pad", ctypes.c_int64), ("scale_kind", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class W4A4Fp8WsLayout(ctypes.Structure):
+    _fields_ = [("a_q", ctypes.c_size_t), ("a_s", ctypes.c_size_t), ("partial", ctypes.c_size_t),
+                ("total", ctypes.c_size_t)]
+
+
+class W4A4Moe(ctypes.Structure):
+    _fields_ = [("gate", W4A4Fp8Packed), ("up", W4A4Fp8Packed), ("down", W4A4Fp8Packed),
+                ("router", ctypes.c_void_p), ("router_dtype", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class W4A4MoeWsLayout(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_size_t), ("xb", ctypes.c_size_t), ("ids", ctypes.c_size_t), ("p", ctypes.c_size_t),
+                ("count", ctypes.c_size_t), ("pairs", ctypes.c_size_t), ("h", ctypes.c_size_t),
+                ("total", ctypes.c_size_t)]
 
 
 class W4A4Error(RuntimeError):
@@ -111,6 +144,17 @@ def lib() -> ctypes.CDLL:
             "w4a4_ffn_up_quantize": (ci, [vp, ci, i64, P(W4A4Packed), P(W4A4Packed), vp, sz, vp]),
             "w4a4_ffn_forward": (ci, [vp, ci, i64, P(W4A4Packed), P(W4A4Packed), vp, vp, sz, vp]),
             "w4a4_linear_noalloc": (ci, [vp, ci, i64, P(W4A4Packed), vp, vp]),
+            "w4a4_fp8_packed_size": (ci, [i64, i64, i64, P(sz)]),
+            "w4a4_fp8_pack_weights": (ci, [vp, ci, i64, i64, i64, ci, vp, sz, P(W4A4Fp8Packed), vp]),
+            "w4a4_fp8_pack_codes": (ci, [vp, vp, i64, i64, i64, ci, vp, sz, P(W4A4Fp8Packed), vp]),
+            "w4a4_fp8_workspace_layout": (ci, [i64, P(W4A4Fp8Packed), P(W4A4Fp8WsLayout)]),
+            "w4a4_fp8_workspace_size": (ci, [i64, P(W4A4Fp8Packed), P(sz)]),
+            "w4a4_fp8_quantize_activations": (ci, [vp, ci, i64, P(W4A4Fp8Packed), vp, sz, vp]),
+            "w4a4_fp8_gemm_prequantized": (ci, [vp, sz, i64, P(W4A4Fp8Packed), vp, ci, vp]),
+            "w4a4_fp8_linear": (ci, [vp, ci, i64, P(W4A4Fp8Packed), vp, ci, vp, sz, vp]),
+            "w4a4_moe_workspace_layout": (ci, [i64, P(W4A4Moe), P(W4A4MoeWsLayout)]),
+            "w4a4_moe_workspace_size": (ci, [i64, P(W4A4Moe), P(sz)]),
+            "w4a4_moe_forward": (ci, [vp, ci, i64, P(W4A4Moe), vp, ci, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -568,3 +612,223 @@ def w4a4_ffn_forward(X: torch.Tensor, up: PackedLayer, down: PackedLayer, Y: tor
     st = lib().w4a4_ffn_forward(_ptr(X), _x_dtype(X), T, ctypes.byref(up.desc), ctypes.byref(down.desc), _ptr(Y),
                                 _ptr(ws), ws.numel(), _stream(stream))
     _check("w4a4_ffn_forward", st)
+
+
+# --------------------------------------------------------------------------- FP8 block-scaled layer
+
+class PackedFp8:
+    """FP8 weights with block scales: n_mat matrices of one shape (one for a linear
+    layer, one per expert).  Keeps the device blob alive."""
+
+    def __init__(self, blob: torch.Tensor, desc: W4A4Fp8Packed):
+        self.blob, self.desc = blob, desc
+
+    @property
+    def n_mat(self) -> int: return self.desc.n_mat
+    @property
+    def d_in(self) -> int: return self.desc.d_in
+    @property
+    def d_out(self) -> int: return self.desc.d_out
+    @property
+    def k_pad(self) -> int: return self.desc.k_pad
+    @property
+    def n_pad(self) -> int: return self.desc.n_pad
+    @property
+    def scale_kind(self) -> int: return self.desc.scale_kind
+
+    def views(self) -> dict:
+        """Copies of the packed arrays: codes uint8 [n_mat, d_out, d_in] (row-major) and
+        scales float32 [n_mat, ceil(d_out / 128), k_pad / 128]."""
+        d = self.desc
+        n = d.n_mat * d.n_pad * d.k_pad
+        off = d.scales - self.blob.data_ptr()
+        sshape = (d.n_mat, (d.d_out + 127) // 128, d.k_pad // 128)
+        codes = untile_fp8(self.blob[:n], d.n_mat * d.n_pad, d.k_pad).view(d.n_mat, d.n_pad, d.k_pad)
+        return {"codes": codes[:, :d.d_out, :d.d_in].contiguous(),
+                "scales": self.blob[off:off + 4 * sshape[0] * sshape[1] * sshape[2]].view(torch.float32).view(sshape).clone()}
+
+
+def untile_fp8(raw: torch.Tensor, rows: int, k_pad: int) -> torch.Tensor:
+    """[rows, k_pad] row-major copy of E4M3 codes stored in the packed order (runs of 32
+    rows x 64 inputs: two halves of 16 inputs, two 32-input chunks, 32 rows, 16 bytes)."""
+    t = raw.view(rows // 32, k_pad // 64, 2, 2, 32, 16)      # run row, run input, half, chunk, row, byte
+    return t.permute(0, 4, 1, 3, 2, 5).reshape(rows, k_pad)
+
+
+def w4a4_fp8_packed_size(n_mat: int, d_in: int, d_out: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("w4a4_fp8_packed_size", lib().w4a4_fp8_packed_size(n_mat, d_in, d_out, ctypes.byref(n)))
+    return n.value
+
+
+def w4a4_fp8_pack_weights(W: torch.Tensor, scale_kind: int = W4A4_FP8_SCALE_F32, stream=None) -> PackedFp8:
+    """W: float32 or bfloat16 [d_out, d_in], or [n_mat, d_out, d_in] for experts."""
+    _dev(W, "W")
+    dt = _x_dtype(W)
+    if W.dim() not in (2, 3):
+        raise ValueError(f"W must be [d_out, d_in] or [n_mat, d_out, d_in], got {tuple(W.shape)}")
+    n_mat, (d_out, d_in) = (W.shape[0] if W.dim() == 3 else 1), W.shape[-2:]
+    blob = torch.empty(w4a4_fp8_packed_size(n_mat, d_in, d_out), dtype=torch.uint8, device=W.device)
+    desc = W4A4Fp8Packed()
+    _check("w4a4_fp8_pack_weights",
+           lib().w4a4_fp8_pack_weights(_ptr(W), dt, n_mat, d_in, d_out, int(scale_kind), _ptr(blob), blob.numel(),
+                                       ctypes.byref(desc), _stream(stream)))
+    return PackedFp8(blob, desc)
+
+
+def w4a4_fp8_pack_codes(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> PackedFp8:
+    """Weights that are quantized already: codes uint8 or float8_e4m3fn [d_out, d_in] or
+    [n_mat, d_out, d_in]; scales [..., ceil(d_out / 128), ceil(d_in / 128)], float32, or
+    uint8 / float8_e8m0fnu for E8M0 scales."""
+    _dev(codes, "codes")
+    _dev(scales, "scales")
+    if codes.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError(f"codes must be uint8 or float8_e4m3fn, got {codes.dtype}")
+    e8m0 = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
+    if scales.dtype != torch.float32 and scales.dtype not in e8m0:
+        raise TypeError(f"scales must be float32, or uint8 E8M0 codes, got {scales.dtype}")
+    if codes.dim() not in (2, 3) or codes.dim() != scales.dim() or codes.device != scales.device:
+        raise ValueError("codes and scales must be [d_out, d_in] or [n_mat, d_out, d_in] on one device")
+    n_mat, (d_out, d_in) = (codes.shape[0] if codes.dim() == 3 else 1), codes.shape[-2:]
+    want = tuple(codes.shape[:-2]) + ((d_out + 127) // 128, (d_in + 127) // 128)
+    if tuple(scales.shape) != want:
+        raise ValueError(f"scales must be {want}, got {tuple(scales.shape)}")
+    kind = W4A4_FP8_SCALE_F32 if scales.dtype == torch.float32 else W4A4_FP8_SCALE_E8M0
+    blob = torch.empty(w4a4_fp8_packed_size(n_mat, d_in, d_out), dtype=torch.uint8, device=codes.device)
+    desc = W4A4Fp8Packed()
+    _check("w4a4_fp8_pack_codes",
+           lib().w4a4_fp8_pack_codes(_ptr(codes), _ptr(scales), n_mat, d_in, d_out, kind, _ptr(blob), blob.numel(),
+                                     ctypes.byref(desc), _stream(stream)))
+    return PackedFp8(blob, desc)
+
+
+def w4a4_fp8_workspace_layout(T: int, packed: PackedFp8) -> W4A4Fp8WsLayout:
+    out = W4A4Fp8WsLayout()
+    _check("w4a4_fp8_workspace_layout",
+           lib().w4a4_fp8_workspace_layout(T, ctypes.byref(packed.desc), ctypes.byref(out)))
+    return out
+
+
+def w4a4_fp8_workspace_size(T: int, packed: PackedFp8) -> int:
+    n = ctypes.c_size_t(0)
+    _check("w4a4_fp8_workspace_size", lib().w4a4_fp8_workspace_size(T, ctypes.byref(packed.desc), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_workspace_fp8(T: int, packed: PackedFp8, device="cuda") -> torch.Tensor:
+    return torch.empty(max(w4a4_fp8_workspace_size(T, packed), 256), dtype=torch.uint8, device=device)
+
+
+def workspace_fp8_views(ws: torch.Tensor, T: int, packed: PackedFp8) -> dict:
+    """Copies of the quantized activations inside ws: A_q uint8 [T, k_pad] (row-major) and
+    A_s float32 [T, k_pad / 128]."""
+    L = w4a4_fp8_workspace_layout(T, packed)
+    rows, nkb = (T + 31) // 32 * 32, packed.k_pad // 128
+    return {"A_q": untile_fp8(ws[L.a_q:L.a_q + rows * packed.k_pad], rows, packed.k_pad)[:T],
+            "A_s": ws[L.a_s:L.a_s + 4 * nkb * rows].view(torch.float32).view(nkb, rows)[:, :T].t().contiguous()}
+
+
+def _y_dtype(Y: torch.Tensor, T: int, d_out: int, like: torch.Tensor) -> int:
+    if Y.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"Y must be float32 or bfloat16, got {Y.dtype}")
+    _out(Y, T, d_out, Y.dtype, "Y", like)
+    return W4A4_Y_F32 if Y.dtype == torch.float32 else W4A4_Y_BF16
+
+
+def w4a4_fp8_quantize_activations(X: torch.Tensor, packed: PackedFp8, ws: torch.Tensor, stream=None) -> None:
+    T = _acts(X, packed.d_in)
+    _wsbuf(ws, X)
+    st = lib().w4a4_fp8_quantize_activations(_ptr(X), _x_dtype(X), T, ctypes.byref(packed.desc), _ptr(ws), ws.numel(),
+                                             _stream(stream))
+    _check("w4a4_fp8_quantize_activations", st)
+
+
+def w4a4_fp8_gemm_prequantized(ws: torch.Tensor, T: int, packed: PackedFp8, Y: torch.Tensor, stream=None) -> None:
+    _dev(Y, "Y")
+    dt = _y_dtype(Y, T, packed.d_out, Y)
+    _wsbuf(ws, Y)
+    st = lib().w4a4_fp8_gemm_prequantized(_ptr(ws), ws.numel(), T, ctypes.byref(packed.desc), _ptr(Y), dt, _stream(stream))
+    _check("w4a4_fp8_gemm_prequantized", st)
+
+
+def w4a4_fp8_linear(X: torch.Tensor, packed: PackedFp8, Y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    T = _acts(X, packed.d_in)
+    dt = _y_dtype(Y, T, packed.d_out, X)
+    _wsbuf(ws, X)
+    st = lib().w4a4_fp8_linear(_ptr(X), _x_dtype(X), T, ctypes.byref(packed.desc), _ptr(Y), dt, _ptr(ws), ws.numel(),
+                               _stream(stream))
+    _check("w4a4_fp8_linear", st)
+
+
+# --------------------------------------------------------------------------- mixture of experts
+
+class MoeLayer:
+    """A mixture-of-experts layer: descriptor, and the tensors it points to."""
+
+    def __init__(self, desc: W4A4Moe, keep: tuple):
+        self.desc, self.keep = desc, keep
+
+    @property
+    def n_experts(self) -> int: return self.desc.up.n_mat
+    @property
+    def d(self) -> int: return self.desc.up.d_in
+    @property
+    def f(self) -> int: return self.desc.up.d_out
+    @property
+    def top_k(self) -> int: return self.desc.top_k
+
+
+def moe_layer(router: torch.Tensor, gate: PackedFp8 | None, up: PackedFp8, down: PackedFp8, top_k: int,
+              renormalize: bool = True) -> MoeLayer:
+    """router: float32 or bfloat16 [E, d]; gate, up: E matrices [f, d]; down: E matrices
+    [d, f].  With a gate the activation is silu(gate) * up, without one gelu_tanh(up)."""
+    _dev(router, "router")
+    dt = _x_dtype(router)
+    if tuple(router.shape) != (up.n_mat, up.d_in):
+        raise ValueError(f"router must be [{up.n_mat}, {up.d_in}], got {tuple(router.shape)}")
+    desc = W4A4Moe()
+    if gate is not None:
+        desc.gate = gate.desc
+    desc.up, desc.down = up.desc, down.desc
+    desc.router, desc.router_dtype = router.data_ptr(), dt
+    desc.top_k, desc.renormalize = int(top_k), int(bool(renormalize))
+    desc.activation = W4A4_MOE_SILU_GATED if gate is not None else W4A4_MOE_GELU_TANH
+    layer = MoeLayer(desc, (router, gate, up, down))
+    w4a4_moe_workspace_size(0, layer)      # the library's checks of the descriptor
+    return layer
+
+
+def w4a4_moe_workspace_layout(T: int, layer: MoeLayer) -> W4A4MoeWsLayout:
+    out = W4A4MoeWsLayout()
+    _check("w4a4_moe_workspace_layout", lib().w4a4_moe_workspace_layout(T, ctypes.byref(layer.desc), ctypes.byref(out)))
+    return out
+
+
+def w4a4_moe_workspace_size(T: int, layer: MoeLayer) -> int:
+    n = ctypes.c_size_t(0)
+    _check("w4a4_moe_workspace_size", lib().w4a4_moe_workspace_size(T, ctypes.byref(layer.desc), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_workspace_moe(T: int, layer: MoeLayer, device="cuda") -> torch.Tensor:
+    return torch.empty(max(w4a4_moe_workspace_size(T, layer), 256), dtype=torch.uint8, device=device)
+
+
+def workspace_moe_views(ws: torch.Tensor, T: int, layer: MoeLayer) -> dict:
+    """Device views of what a call left in ws: logits [T, E], ids and p [T, top_k], h
+    [T, top_k, f]."""
+    L = w4a4_moe_workspace_layout(T, layer)
+    k, E, fp = layer.top_k, layer.n_experts, layer.desc.down.k_pad
+    return {"logits": ws[L.logits:L.logits + 4 * T * E].view(torch.float32).view(T, E),
+            "ids": ws[L.ids:L.ids + 4 * T * k].view(torch.int32).view(T, k),
+            "p": ws[L.p:L.p + 4 * T * k].view(torch.float32).view(T, k),
+            "h": ws[L.h:L.h + 2 * T * k * fp].view(torch.bfloat16).view(T, k, fp)[:, :, :layer.f]}
+
+
+def w4a4_moe_forward(X: torch.Tensor, layer: MoeLayer, Y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    T = _acts(X, layer.d)
+    dt = _y_dtype(Y, T, layer.d, X)
+    _wsbuf(ws, X)
+    st = lib().w4a4_moe_forward(_ptr(X), _x_dtype(X), T, ctypes.byref(layer.desc), _ptr(Y), dt, _ptr(ws), ws.numel(),
+                                _stream(stream))
+    _check("w4a4_moe_forward", st)

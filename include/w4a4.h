@@ -336,6 +336,155 @@ int w4a4_gelu_tanh_bf16(const float* Y, int64_t n, uint16_t* H, void* stream);
 int w4a4_linear_noalloc(const void* X, int x_dtype, int64_t T, const w4a4_packed* desc, float* Y,
                         void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * FP8 linear layer with block scales: the 8-bit layer for the projections that four bits
+ * cannot carry (the page keeps up to five blocks at a higher precision, sec. 2).
+ *
+ *     Y[t][n] = sum_b s_x[t][b] s_w[n / 128][b] sum_{p in block b} q_x[t][p] q_w[n][p]
+ *
+ *   - Codes are OCP E4M3 (largest value 448), blocks b are 128 inputs; activations have
+ *     one scale per token and block, weights one per 128 outputs x 128 inputs.
+ *   - Scale of a block with largest magnitude a:
+ *       W4A4_FP8_SCALE_F32:  s = max(fl32(a / 448), 2^-60)
+ *       W4A4_FP8_SCALE_E8M0: s = the smallest power of two >= 2^-60 with a <= 448 s
+ *     (the floor keeps products of two scales normal numbers; blocks below 448 * 2^-60
+ *     lose codes to it).  A NaN or Inf in the block gives s = NaN and zero codes (every
+ *     output that reads the block is NaN).  A zero block has s = 2^-60.
+ *   - Codes: e4m3_rne(fl32(x / s)), nearest, ties to the even mantissa, signs kept.
+ *   - Sums, and the products with the scales, are binary32, and fp32 outputs are those
+ *     sums.  For bf16 outputs of more than 64 tokens the matrix instructions take the codes
+ *     as FP8 and drop what is 13 bits below the largest product beside it: 1.4e-5 to 4e-5
+ *     of a sum, a fiftieth of the outputs' own rounding.  The product of two scales
+ *     s_x s_w is taken first: with scales of a checkpoint it has to be a normal number.
+ *   - The inputs are zero padded to k_pad = roundup(d_in, 128); 1 <= d_in <=
+ *     W4A4_FP8_MAX_D, 1 <= d_out <= W4A4_FP8_MAX_D, any number of tokens.
+ * The conventions at the top of this file hold: caller-owned buffers, 16-byte aligned
+ * device pointers, T = 0 a no-op, no allocation or synchronisation, graph capture.
+ * Calls are bit-reproducible for a given shape. */
+enum { W4A4_FP8_SCALE_F32 = 0, W4A4_FP8_SCALE_E8M0 = 1 };
+enum { W4A4_Y_F32 = 0, W4A4_Y_BF16 = 1 };
+#define W4A4_FP8_MAX_D 1048576
+
+/* n_mat weight matrices of one shape (one for a linear layer, one per expert for a
+ * mixture of experts).  Plain data that points into the caller's blob. */
+typedef struct w4a4_fp8_packed {
+    int64_t n_mat, d_in, d_out;
+    int64_t k_pad;           /* roundup(d_in, 128)                                          */
+    int64_t n_pad;           /* roundup(d_out, 32)                                          */
+    int32_t scale_kind;      /* W4A4_FP8_SCALE_*: also the kind of the activations' scales  */
+    int32_t reserved;
+    const uint8_t* codes;    /* device E4M3 [n_mat][n_pad/32][k_pad/64][2][64][16]: each run
+                                of 32 rows x 64 inputs is 2 KiB in the order the matrix
+                                instructions read it; the byte of row r, input p sits at
+                                  ((r/32)*(k_pad/64) + p/64)*2048 + ((p/16)%2)*1024
+                                  + (((p/32)%2)*32 + r%32)*16 + p%16;
+                                rows past d_out and inputs past d_in are zero              */
+    const float* scales;     /* device [n_mat][ceil(d_out/128)][k_pad/128], as binary32 for
+                                both kinds                                                 */
+} w4a4_fp8_packed;
+
+/* Bytes of the device blob of n_mat packed matrices. */
+int w4a4_fp8_packed_size(int64_t n_mat, int64_t d_in, int64_t d_out, size_t* bytes);
+
+/* Quantize W (device [n_mat][d_out][d_in], fp32 or bf16: w_dtype is W4A4_X_F32 or
+ * W4A4_X_BF16) into `blob` (device, blob_bytes >= w4a4_fp8_packed_size) and fill *desc.
+ * A 128 x 128 block that the matrix's edge cuts takes its scale from the part inside.
+ * Async on `stream`. */
+int w4a4_fp8_pack_weights(const void* W, int w_dtype, int64_t n_mat, int64_t d_in, int64_t d_out,
+                          int scale_kind, void* blob, size_t blob_bytes, w4a4_fp8_packed* desc,
+                          void* stream);
+
+/* The same from weights that are quantized already (a checkpoint): codes device uint8
+ * [n_mat][d_out][d_in] E4M3, scales device [n_mat][ceil(d_out/128)][ceil(d_in/128)], fp32
+ * for W4A4_FP8_SCALE_F32, uint8 E8M0 codes for W4A4_FP8_SCALE_E8M0 (value 2^(c-127); 0xFF
+ * is NaN).  Values are taken as they are.  Async on `stream`. */
+int w4a4_fp8_pack_codes(const uint8_t* codes, const void* scales, int64_t n_mat, int64_t d_in,
+                        int64_t d_out, int scale_kind, void* blob, size_t blob_bytes,
+                        w4a4_fp8_packed* desc, void* stream);
+
+/* Offsets (bytes) inside a workspace for T tokens. */
+typedef struct w4a4_fp8_ws_layout {
+    size_t a_q;       /* activation codes in the order of w4a4_fp8_packed.codes, tokens as
+                         rows: [ceil(T/32)][k_pad/64][2][64][16]; rows past T unwritten    */
+    size_t a_s;       /* fp32 [k_pad/128][roundup(T, 32)] activation scales; tokens past T
+                         unwritten                                                         */
+    size_t partial;   /* fp32 partial sums of K ranges (written and read back within a
+                         call; empty when the plan does not split)                         */
+    size_t total;
+} w4a4_fp8_ws_layout;
+int w4a4_fp8_workspace_layout(int64_t T, const w4a4_fp8_packed* desc, w4a4_fp8_ws_layout* out);
+int w4a4_fp8_workspace_size(int64_t T, const w4a4_fp8_packed* desc, size_t* bytes);
+
+/* Activation codes and scales of X (device [T][d_in] fp32 or bf16, row-major contiguous)
+ * into ws.  desc->n_mat must be 1, here and in the calls below.  Async. */
+int w4a4_fp8_quantize_activations(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc,
+                                  void* ws, size_t ws_bytes, void* stream);
+/* The product on quantized activations in ws.  Y device [T][d_out], fp32 or bf16 (the
+ * fp32 sums rounded once to nearest even): y_dtype is W4A4_Y_F32 or W4A4_Y_BF16.  Async. */
+int w4a4_fp8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_fp8_packed* desc,
+                               void* Y, int y_dtype, void* stream);
+/* Both.  Async.  (The codes and scales of X may stay out of ws where the product takes
+ * them as it computes them.) */
+int w4a4_fp8_linear(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc, void* Y,
+                    int y_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Mixture-of-experts layer for a few tokens (decoding), weights in the FP8 block format
+ * above.  For each token t of X [T][d], with E experts of width f:
+ *
+ *     l[e]  = sum_i X[t][i] router[e][i]                            (fp32 sums)
+ *     S     = the top_k experts by l: larger first, ties to the lower index, a NaN before
+ *             every number
+ *     p[e]  = exp(l[e] - max l) / sum of the same over S (renormalize != 0) or over all
+ *             experts (renormalize == 0)
+ *     g, u  = gate_e . x, up_e . x     with x = bf16_rne(X[t]),     (fp32 sums)
+ *     h     = bf16_rne(silu(g) u)      or, W4A4_MOE_GELU_TANH: h = bf16_rne(gelu_tanh(u))
+ *     Y[t]  = sum_{e in S} p[e] (down_e . h)                        (fp32 sums)
+ *
+ * The experts' products are bound by reading the codes of the chosen experts, so the
+ * activations stay bf16 (the matrix instructions take E4M3 weights widened to bf16, which
+ * is exact): no activation quantization error at no cost in time.
+ * Limits: 1 <= T <= W4A4_MOE_MAX_T tokens a call (W4A4_ERR_SHAPE above), E <=
+ * W4A4_MOE_MAX_E, top_k <= W4A4_MOE_MAX_K and <= E, d and f <= W4A4_MOE_MAX_D. */
+enum { W4A4_MOE_SILU_GATED = 0, W4A4_MOE_GELU_TANH = 1 };
+#define W4A4_MOE_MAX_T 128
+#define W4A4_MOE_MAX_E 1024
+#define W4A4_MOE_MAX_K 32
+#define W4A4_MOE_MAX_D 65536
+
+typedef struct w4a4_moe {
+    w4a4_fp8_packed gate;    /* n_mat = E, d -> f; not read for W4A4_MOE_GELU_TANH          */
+    w4a4_fp8_packed up;      /* n_mat = E, d -> f                                           */
+    w4a4_fp8_packed down;    /* n_mat = E, f -> d                                           */
+    const void* router;      /* device [E][d], row-major contiguous                         */
+    int32_t router_dtype;    /* W4A4_X_F32 or W4A4_X_BF16                                   */
+    int32_t top_k;
+    int32_t renormalize;
+    int32_t activation;      /* W4A4_MOE_*                                                  */
+} w4a4_moe;
+
+/* Offsets (bytes) inside a workspace for T tokens: what a call leaves there. */
+typedef struct w4a4_moe_ws_layout {
+    size_t logits;    /* fp32 [T][E]                                                        */
+    size_t xb;        /* bf16 [T][roundup(d, 128)], zero padded                             */
+    size_t ids;       /* int32 [T][top_k]: the chosen experts, largest logit first          */
+    size_t p;         /* fp32 [T][top_k]: exp(l - max), divided by the sum over all experts
+                         when renormalize == 0 (otherwise the down step divides by the sum
+                         over the row)                                                      */
+    size_t count;     /* int32 [E]: tokens of each expert                                   */
+    size_t pairs;     /* int32 [E][T]: their entries t * top_k + rank of ids, ascending     */
+    size_t h;         /* bf16 [T * top_k][roundup(f, 128)], zero padded                     */
+    size_t total;
+} w4a4_moe_ws_layout;
+int w4a4_moe_workspace_layout(int64_t T, const w4a4_moe* moe, w4a4_moe_ws_layout* out);
+int w4a4_moe_workspace_size(int64_t T, const w4a4_moe* moe, size_t* bytes);
+
+/* The whole layer: X device [T][d] fp32 or bf16, Y device [T][d] fp32 or bf16.  Async;
+ * never allocates.  Three launches: router logits, the chosen experts' up projections, their
+ * down projections with the weighted sum. */
+int w4a4_moe_forward(const void* X, int x_dtype, int64_t T, const w4a4_moe* moe, void* Y, int y_dtype,
+                     void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

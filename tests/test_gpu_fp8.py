@@ -1,0 +1,227 @@
+"""The FP8 block-scaled linear layer on the GPU against its 64-bit form: codes and scales bit
+for bit, outputs within the rounding bound of a binary32 evaluation, at the sizes and values
+where each path changes."""
+import numpy as np
+import pytest
+import torch
+
+from bit_quantized_dit_amd import w4a4 as B
+from tests import fp8_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _x(T, d, dtype, seed, heavy=True):
+    rng = np.random.default_rng(seed)
+    x = (rng.standard_normal((T, d)) * 0.3).astype(np.float32)
+    if heavy:
+        x[:, rng.integers(0, d, max(1, d // 80))] *= 20
+    if dtype == BF16:
+        x = R.bf16(x)
+    return x
+
+
+def _guarded(x, dtype, fill):
+    """x on the device, inside a larger buffer whose other values are `fill`."""
+    buf = torch.full((x.size + 512,), fill, dtype=dtype, device="cuda")
+    buf[256:256 + x.size] = torch.from_numpy(x.ravel()).to(dtype).cuda()
+    return buf, buf[256:256 + x.size].view(x.shape)
+
+
+def _run(x, xt, w, kind, yt, stream=None):
+    """(codes, scales, Y as float64, weight codes, weight scales) of one call; inputs sit among
+    NaNs, the workspace starts as 0xFF bytes, and writes outside Y are looked for."""
+    T, (n, d) = x.shape[0], w.shape
+    print(f"fp8 linear T={T} {d}->{n} x={xt} y={yt} kind={kind}", flush=True)
+    _, X = _guarded(x, xt, float("nan"))
+    _, W = _guarded(w, F32, float("nan"))
+    layer = B.w4a4_fp8_pack_weights(W, kind)
+    ws = torch.full((max(B.w4a4_fp8_workspace_size(T, layer), 256) + 512,), 255, dtype=torch.uint8, device="cuda")
+    buf, Y = _guarded(np.zeros((T, n), np.float32), yt, 7.0)
+    B.w4a4_fp8_linear(X, layer, Y, ws[:-512])
+    torch.cuda.synchronize()
+    assert bool((ws[-512:] == 255).all()) and bool((buf[:256] == 7).all()) and bool((buf[256 + T * n:] == 7).all())
+    v, p = B.workspace_fp8_views(ws, T, layer), layer.views()
+    return v["A_q"].cpu().numpy(), v["A_s"].cpu().numpy(), Y.double().cpu().numpy(), p["codes"][0].cpu().numpy(), p["scales"][0].cpu().numpy()
+
+
+def _check(x, xt, w, kind, yt):
+    aq, as_, y, wc, wsc = _run(x, xt, w, kind, yt)
+    rq, rs = R.quantize_rows(x, kind)
+    cq, cs = R.quantize_blocks(w, kind)
+    assert np.array_equal(as_.view(np.uint32)[~np.isnan(rs)], rs.view(np.uint32)[~np.isnan(rs)]) and np.array_equal(np.isnan(as_), np.isnan(rs))
+    assert np.array_equal(aq, rq), f"{int((aq != rq).sum())} activation codes differ"
+    assert np.array_equal(wsc.view(np.uint32)[~np.isnan(cs)], cs.view(np.uint32)[~np.isnan(cs)]) and np.array_equal(np.isnan(wsc), np.isnan(cs))
+    assert np.array_equal(wc, cq), f"{int((wc != cq).sum())} weight codes differ"
+    d = w.shape[1]
+    ref, tol = R.product(R.dequant_rows(rq, rs)[:, :d], R.dequant_blocks(cq, cs), yt == BF16 and x.shape[0] > 64)
+    if yt == BF16:
+        tol = tol + R.BF16_U * (np.abs(ref) + tol)
+    R.close(y, ref, tol, "Y")
+    return y
+
+
+SHAPES = [(1, 1, 1), (1, 128, 16), (2, 127, 17), (5, 129, 33), (16, 256, 128), (17, 300, 257), (31, 1100, 40),
+          (33, 640, 96), (64, 2176, 130), (65, 384, 129), (100, 1000, 300), (129, 128, 128), (257, 512, 1024),
+          (300, 333, 1111)]
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("T,d,n", SHAPES)
+def test_shapes(T, d, n, kind):
+    rng = np.random.default_rng(T * 7 + d)
+    w = (rng.standard_normal((n, d)) * 0.02).astype(np.float32)
+    _check(_x(T, d, BF16, 1), BF16, w, kind, F32)
+    _check(_x(T, d, F32, 2), F32, w, kind, BF16)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("T,d,n,yt", [(4001, 200, 3211, F32), (4001, 200, 3211, BF16), (2048, 256, 6144, BF16)])
+def test_large_tiles(T, d, n, yt, kind):
+    rng = np.random.default_rng(5)
+    _check(_x(T, d, BF16, 3), BF16, (rng.standard_normal((n, d)) * 0.02).astype(np.float32), kind, yt)
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_special_values(T, kind):
+    """Zero blocks, blocks whose scale sits at its floor, the largest finite values, ties of
+    the code grid; a NaN or an infinity makes its own token's row NaN and no other."""
+    d, n = 400, 144
+    x = _x(T, d, F32, 11)
+    w = (np.random.default_rng(12).standard_normal((n, d)) * 0.02).astype(np.float32)
+    x[0, :128] = 0
+    x[0, 128:256] = 1e-42
+    x[1, :] = 0
+    x[1, 7] = 448.0
+    x[1, 8:24] = [1.0625, 1.1875, 17, 19, 2.0 ** -10, 3 * 2.0 ** -10, 0.0, -0.0, 2.0 ** -9, -1.0625, 432, 416, 256, 240, 464 / 2, 1]
+    x[2, :] = np.float32(2.0 ** -130)
+    y = _check(x, F32, w, kind, F32)
+    assert np.isfinite(y).all()
+    for bad in (np.nan, np.inf, -np.inf):
+        z = x.copy()
+        z[T // 2, 300] = bad
+        y2 = _check(z, F32, w, kind, F32)
+        assert np.isnan(y2[T // 2]).all()
+        keep = np.arange(T) != T // 2
+        assert np.array_equal(y2[keep], y[keep])
+    big = x.copy()
+    big[0, 5] = 3.0e38
+    _check(big, F32, w, kind, F32)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("T", [4, 70])
+def test_weights_with_nan_and_zero_blocks(T, kind):
+    d, n = 300, 300
+    w = (np.random.default_rng(13).standard_normal((n, d)) * 0.02).astype(np.float32)
+    w[:128, :128] = 0
+    w[200, 140] = np.nan
+    y = _check(_x(T, d, BF16, 14), BF16, w, kind, F32)
+    assert np.isnan(y[:, 128:256]).all() and np.isfinite(y[:, :128]).all() and np.isfinite(y[:, 256:]).all()
+
+
+@pytest.mark.parametrize("T", [1, 64, 65, 130])
+def test_every_activation_code(T):
+    """All bf16 magnitudes of one binade range through the quantizer: exact division and
+    rounding on each."""
+    rng = np.random.default_rng(20)
+    x = rng.integers(0, 1 << 16, (T, 1024)).astype(np.uint16)
+    x = np.where((x & 0x7F80) == 0x7F80, 0x3F80, x).astype(np.uint32)      # finite
+    x = (((x & 0x807F) | (np.uint32(100 + T % 20) << 7)) + ((x >> 7) % 24 << 7)).astype(np.uint32)
+    v = (x << 16).view(np.float32)
+    assert np.isfinite(v).all()
+    for kind in (0, 1):
+        _check(v, BF16, (rng.standard_normal((32, 1024)) * 0.02).astype(np.float32), kind, F32)
+
+
+def test_checkpoint_codes():
+    """pack_codes keeps a checkpoint's codes and scales, in either scale format and for several
+    matrices at once, and the layer computes with them; bf16 weights quantize as their values."""
+    rng = np.random.default_rng(30)
+    for n_mat, n, d in [(1, 70, 130), (3, 33, 128), (2, 257, 300)]:
+        codes = rng.integers(0, 256, (n_mat, n, d)).astype(np.uint8)
+        codes[(codes & 0x7F) == 0x7F] = 0x38
+        sc = np.exp(rng.standard_normal((n_mat, -(-n // 128), -(-d // 128)))).astype(np.float32)
+        e8 = rng.integers(110, 140, sc.shape).astype(np.uint8)
+        p = B.w4a4_fp8_pack_codes(torch.from_numpy(codes).cuda(), torch.from_numpy(sc).cuda())
+        assert np.array_equal(p.views()["codes"].cpu().numpy(), codes) and np.array_equal(p.views()["scales"].cpu().numpy(), sc)
+        q = B.w4a4_fp8_pack_codes(torch.from_numpy(codes).cuda(), torch.from_numpy(e8).cuda())
+        assert q.scale_kind == B.W4A4_FP8_SCALE_E8M0
+        assert np.array_equal(q.views()["scales"].cpu().numpy(), (2.0 ** (e8.astype(np.float64) - 127)).astype(np.float32))
+        if n_mat == 1:
+            x = _x(9, d, BF16, 31)
+            Y = torch.empty(9, n, device="cuda")
+            B.w4a4_fp8_linear(torch.from_numpy(x).to(BF16).cuda(), p, Y, B.alloc_workspace_fp8(9, p))
+            rq, rs = R.quantize_rows(x, 0)
+            ref, tol = R.product(R.dequant_rows(rq, rs)[:, :d], R.dequant_blocks(codes[0], sc[0]))
+            R.close(Y.cpu().numpy(), ref, tol, "Y")
+    w = R.bf16((rng.standard_normal((2, 130, 200)) * 0.02).astype(np.float32))
+    a = B.w4a4_fp8_pack_weights(torch.from_numpy(w).to(BF16).cuda()).views()
+    for m in range(2):
+        c, s = R.quantize_blocks(w[m], 0)
+        assert np.array_equal(a["codes"][m].cpu().numpy(), c) and np.array_equal(a["scales"][m].cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("T,d,n,kind", [(1, 640, 300, 0), (40, 1300, 200, 1), (300, 700, 520, 0), (300, 700, 520, 1), (4000, 384, 3300, 0)])
+def test_split_calls_streams_and_repeats(T, d, n, kind):
+    """quantize + product equals the one call; a call on another stream, a repeated call and a
+    captured graph's replays give the same bits."""
+    print(f"fp8 repeats T={T} {d}->{n} kind={kind}", flush=True)
+    X = torch.from_numpy(_x(T, d, BF16, 40)).to(BF16).cuda()
+    layer = B.w4a4_fp8_pack_weights(torch.randn(n, d, device="cuda") * 0.02, kind)
+    ws = B.alloc_workspace_fp8(T, layer)
+    Y = torch.empty(T, n, device="cuda")
+    B.w4a4_fp8_linear(X, layer, Y, ws)
+    ref = Y.clone()
+    B.w4a4_fp8_quantize_activations(X, layer, ws)
+    Y.fill_(float("nan"))
+    B.w4a4_fp8_gemm_prequantized(ws, T, layer, Y)
+    assert torch.equal(Y, ref)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    Y.fill_(float("nan"))
+    torch.cuda.synchronize()
+    B.w4a4_fp8_linear(X, layer, Y, ws, s)
+    s.synchronize()
+    assert torch.equal(Y, ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.w4a4_fp8_linear(X, layer, Y, ws)
+    for _ in range(4):
+        Y.fill_(float("nan"))
+        (X.float() @ torch.ones(d, 8, device="cuda")).sum().item()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, ref)
+
+
+def test_zero_tokens():
+    layer = B.w4a4_fp8_pack_weights(torch.randn(20, 40, device="cuda"))
+    X, Y = torch.empty(16, 40, device="cuda")[:0], torch.full((16, 20), 3.0, device="cuda")
+    B.w4a4_fp8_quantize_activations(torch.zeros(1, 40, device="cuda"), layer, B.alloc_workspace_fp8(1, layer))
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    st = B.lib().w4a4_fp8_linear(B._ptr(Y), 0, 0, layer.desc, B._ptr(Y), 0, B._ptr(ws), 256, None)
+    assert st == 0 and X.shape[0] == 0
+    torch.cuda.synchronize()
+    assert bool((Y == 3).all())
+
+
+def test_binding_refusals():
+    layer = B.w4a4_fp8_pack_weights(torch.randn(20, 40, device="cuda"))
+    two = B.w4a4_fp8_pack_weights(torch.randn(2, 20, 40, device="cuda"))
+    X, Y, ws = torch.zeros(3, 40, device="cuda"), torch.zeros(3, 20, device="cuda"), B.alloc_workspace_fp8(3, layer)
+    for args, exc in [((X.half(), layer, Y, ws), TypeError), ((X, layer, Y.half(), ws), TypeError), ((X[:, :39], layer, Y, ws), ValueError),
+                      ((X[:, :39].contiguous(), layer, Y, ws), ValueError), ((X, layer, Y[:2], ws), ValueError), ((X.cpu(), layer, Y, ws), ValueError),
+                      ((X, layer, Y, ws.float()), TypeError), ((X, layer, Y, ws[:64]), B.W4A4Error), ((X, layer, Y, ws[1:]), B.W4A4Error),
+                      ((X, two, Y, ws), B.W4A4Error)]:
+        with pytest.raises(exc):
+            B.w4a4_fp8_linear(*args)
+    with pytest.raises(ValueError):
+        B.w4a4_fp8_pack_codes(torch.zeros(20, 40, dtype=torch.uint8, device="cuda"), torch.zeros(2, 1, device="cuda"))
+    with pytest.raises(TypeError):
+        B.w4a4_fp8_pack_codes(torch.zeros(20, 40, dtype=torch.int8, device="cuda"), torch.zeros(1, 1, device="cuda"))
+    with pytest.raises(B.W4A4Error):
+        B.w4a4_fp8_pack_weights(torch.randn(20, 40, device="cuda"), 2)
