@@ -97,8 +97,7 @@ __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__
     const float s = block_scale(m, kind);
     const uint4 c = encode16(v, s);
     if (!live) return;
-    uint8_t* dst = aq + ((t / 32) * (nkb * 2) + kb * 2 + (i >> 2)) * 2048 + (i & 1) * 1024 +
-                   ((((i >> 1) & 1) * 32) + (t & 31)) * 16;
+    uint8_t* dst = aq + ((t / 16) * nkb + kb) * 2048 + (i & 1) * 1024 + (i >> 1) * 256 + (t & 15) * 16;
     *reinterpret_cast<uint4*>(dst) = c;
     if (i == 0) as[kb * t_ld + t] = s;
 }
@@ -137,8 +136,8 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t p = p0 + 16 * i;
-        uint8_t* dst = codes + ((mat * (n_pad / 32) + row / 32) * (nkb * 2) + p / 64) * 2048 + ((p / 16) & 1) * 1024 +
-                       (((p / 32) & 1) * 32 + (row & 31)) * 16;
+        uint8_t* dst = codes + ((mat * (n_pad / 16) + row / 16) * nkb + kb) * 2048 + ((p / 16) & 1) * 1024 + ((p / 32) & 3) * 256 +
+                       (row & 15) * 16;
         *reinterpret_cast<uint4*>(dst) = encode16(v[i], s);
     }
 }
@@ -150,10 +149,10 @@ __global__ __launch_bounds__(256) void fp8_reorder_kernel(const uint8_t* __restr
     const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (q >= pieces) return;
     const int l = (int)(q & 63), h = (int)((q >> 6) & 1);
-    const int64_t run = q >> 7;                       // 32 rows x 64 inputs
-    const int64_t rb = run / (nkb * 2), kb = run - rb * (nkb * 2);
-    const int64_t mat = rb / (n_pad / 32), row = (rb - mat * (n_pad / 32)) * 32 + (l & 31);
-    const int64_t p = kb * 64 + (l >> 5) * 32 + h * 16;
+    const int64_t run = q >> 7;                       // 16 rows x 128 inputs
+    const int64_t rb = run / nkb, kb = run - rb * nkb;
+    const int64_t mat = rb / (n_pad / 16), row = (rb - mat * (n_pad / 16)) * 16 + (l & 15);
+    const int64_t p = kb * 128 + (l >> 4) * 32 + h * 16;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (row < d_out) {
         const uint8_t* s = src + (mat * d_out + row) * d_in + p;

@@ -20,12 +20,12 @@ int check_dims(int64_t n_mat, int64_t d_in, int64_t d_out) {
     if (n_mat <= 0 || d_in <= 0 || d_out <= 0) return W4A4_ERR_INVALID;
     if (d_in > W4A4_FP8_MAX_D || d_out > W4A4_FP8_MAX_D || n_mat > 65535) return W4A4_ERR_SHAPE;
     // packing runs one workgroup per 4 KiB of codes or 128 x 128 block
-    if (n_mat * (round_up(d_out, 32) / 32) * (round_up(d_in, 128) / 128) > kMaxBlocks) return W4A4_ERR_SHAPE;
+    if (n_mat * (round_up(d_out, 16) / 16) * (round_up(d_in, 128) / 128) > kMaxBlocks) return W4A4_ERR_SHAPE;
     return W4A4_OK;
 }
 
 size_t codes_bytes(int64_t n_mat, int64_t d_in, int64_t d_out) {
-    return (size_t)n_mat * (size_t)round_up(d_out, 32) * (size_t)round_up(d_in, 128);
+    return (size_t)n_mat * (size_t)round_up(d_out, 16) * (size_t)round_up(d_in, 128);
 }
 size_t scales_bytes(int64_t n_mat, int64_t d_in, int64_t d_out) {
     return (size_t)n_mat * (size_t)((d_out + 127) / 128) * (size_t)((d_in + 127) / 128) * 4;
@@ -38,7 +38,7 @@ int check_packed(const w4a4_fp8_packed* d) {
     if (!d) return W4A4_ERR_INVALID;
     const int st = check_dims(d->n_mat, d->d_in, d->d_out);
     if (st) return st;
-    if (!valid_kind(d->scale_kind) || d->k_pad != round_up(d->d_in, 128) || d->n_pad != round_up(d->d_out, 32) || !d->codes ||
+    if (!valid_kind(d->scale_kind) || d->k_pad != round_up(d->d_in, 128) || d->n_pad != round_up(d->d_out, 16) || !d->codes ||
         !d->scales)
         return W4A4_ERR_INVALID;
     if (misaligned(d->codes) || misaligned(d->scales)) return W4A4_ERR_ALIGN;
@@ -62,7 +62,7 @@ int64_t t_ld_of(int64_t T) { return round_up(T, 32); }
 w4a4_fp8_ws_layout ws_layout(int64_t T, const w4a4_fp8_packed* d) {
     w4a4_fp8_ws_layout w;
     size_t off = 0;
-    w.a_q = off;     off = align_up(off + (size_t)(round_up(T, 32) * d->k_pad));
+    w.a_q = off;     off = align_up(off + (size_t)(round_up(T, 16) * d->k_pad));
     w.a_s = off;     off = align_up(off + (size_t)(d->k_pad / 128 * t_ld_of(T)) * 4);
     w.partial = off;
     w.total = off;
@@ -79,7 +79,7 @@ int describe(int64_t n_mat, int64_t d_in, int64_t d_out, int kind, void* blob, s
     out->d_in = d_in;
     out->d_out = d_out;
     out->k_pad = round_up(d_in, 128);
-    out->n_pad = round_up(d_out, 32);
+    out->n_pad = round_up(d_out, 16);
     out->scale_kind = kind;
     out->reserved = 0;
     out->codes = (const uint8_t*)blob;
@@ -109,14 +109,14 @@ int check_moe(int64_t T, const w4a4_moe* m) {
 w4a4_moe_ws_layout moe_layout(int64_t T, const w4a4_moe* m) {
     w4a4_moe_ws_layout w;
     const int64_t E = m->up.n_mat, pairs = T * m->top_k;
+    const int64_t h_tiles = (moe_by_slot(T, m->top_k, E) ? pairs : E) * ((T + 15) / 16);
     size_t off = 0;
-    w.logits = off; off = align_up(off + (size_t)(T * E) * 4);
+    w.logits = off; off = align_up(off + (size_t)(T * round_up(E, 4)) * 4);
     w.xb = off;     off = align_up(off + (size_t)(T * m->up.k_pad) * 2);
     w.ids = off;    off = align_up(off + (size_t)pairs * 4);
     w.p = off;      off = align_up(off + (size_t)pairs * 4);
-    w.count = off;  off = align_up(off + (size_t)E * 4);
-    w.pairs = off;  off = align_up(off + (size_t)(E * T) * 4);
-    w.h = off;      off = align_up(off + (size_t)(pairs * m->down.k_pad) * 2);
+    w.pos = off;    off = align_up(off + (size_t)pairs * 4);
+    w.h = off;      off = align_up(off + (size_t)(h_tiles * 16 * m->down.k_pad) * 2);
     w.total = off;
     return w;
 }
@@ -244,8 +244,7 @@ int w4a4_moe_forward(const void* X, int x_dtype, int64_t T, const w4a4_moe* moe,
     m.xb = (uint16_t*)(b + w.xb);
     m.h = (uint16_t*)(b + w.h);
     m.ids = (int32_t*)(b + w.ids);
-    m.count = (int32_t*)(b + w.count);
-    m.pairs = (int32_t*)(b + w.pairs);
+    m.pos = (int32_t*)(b + w.pos);
     return dev_status(launch_moe(X, x_dtype, T, *moe, m, Y, y_dtype, (hipStream_t)stream));
 }
 

@@ -6,10 +6,12 @@
 // src0 = weight rows, src1 = token rows, so a lane of the result holds one token and its
 // activation scale is one value per lane.
 //
-// Both operands lie in memory in the order in which a wavefront of
-// v_mfma_f32_32x32x64_f8f6f4 reads them (32 rows x 64 inputs = two KiB, lane l: row l % 32,
-// inputs 32 (l / 32) .. + 31, its two 16-byte halves 1 KiB apart), so copies to LDS are
-// linear and fragment reads are conflict-free without a swizzle.
+// Both operands lie in memory in runs of 16 rows x 128 inputs (2 KiB), in the order in which a
+// wavefront of a 16-row matrix instruction reads them: lane l takes row l % 16, inputs
+// 32 (l / 16) .. + 31, its two 16-byte halves at 16 l and 1024 + 16 l.  Runs of a row block
+// follow each other along the inputs, so that whoever streams 16 rows reads one contiguous
+// range; copies to LDS are linear; and a 32-row fragment takes 16 rows from each of two runs
+// in 256-byte pieces that no two of 16 neighbouring lanes' banks share.
 //
 // Precision.  The FP8 matrix instructions (all of them, whatever their shape) line the
 // products of a few inputs up with the largest one and drop what falls about 13 bits below
@@ -86,9 +88,9 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
     tile_at<4>(blockIdx.x, (uint32_t)((T + BT - 1) / BT), (uint32_t)((N + BF - 1) / BF), tm, tn);
     const int64_t t0 = (int64_t)tm * BT, f0 = (int64_t)tn * BF;
     const int64_t rows_a = T - t0 < BT ? T - t0 : BT, rows_b = N - f0 < BF ? N - f0 : BF;
-    const int64_t blk = nkb64 * 4096;                     // bytes of 32 rows
-    const v4i srd_a = make_srd(Aq + t0 / 32 * blk, (uint32_t)((rows_a + 31) / 32 * blk));
-    const v4i srd_b = make_srd(Bq + f0 / 32 * blk, (uint32_t)((rows_b + 31) / 32 * blk));
+    const int64_t blk = nkb64 * 2048;                     // bytes of 16 rows
+    const v4i srd_a = make_srd(Aq + t0 / 16 * blk, (uint32_t)((rows_a + 15) / 16 * blk));
+    const v4i srd_b = make_srd(Bq + f0 / 16 * blk, (uint32_t)((rows_b + 15) / 16 * blk));
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
     // copy the operands and scales of block kb into slot kb & 1
@@ -97,10 +99,10 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
 #pragma unroll
         for (int i = 0; i < PIECES / NW; ++i) {
             const int q = wave * (PIECES / NW) + i;       // wave-uniform
-            const int rb = q >> 2, sub = q & 3;
-            const bool is_a = rb < BT / 32;
-            const int r = is_a ? rb : rb - BT / 32;
-            dma16(is_a ? srd_a : srd_b, slot + q * 1024, (int)(r * blk) + sub * 1024 + lane * 16, kb * 4096);
+            const int rb = q >> 1, sub = q & 1;
+            const bool is_a = rb < BT / 16;
+            const int r = is_a ? rb : rb - BT / 16;
+            dma16(is_a ? srd_a : srd_b, slot + q * 1024, (int)(r * blk) + sub * 1024 + lane * 16, kb * 2048);
         }
         if (wave < BT / 64) {
             dma4(make_srd(As + (int64_t)kb * t_ld + t0, (uint32_t)(rows_a * 4)), slot + AS_OFF + wave * 256,
@@ -127,7 +129,7 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
         if (kb + 1 < nkb) issue(kb + 1);
         const uint8_t* slot = smem + (kb & 1) * SLOT;
         auto frag = [&](int off, int rb, int half) __attribute__((always_inline)) {
-            const uint8_t* p = slot + off + rb * 4096 + half * 2048 + lane * 16;
+            const uint8_t* p = slot + off + (rb * 2 + (l32 >> 4)) * 2048 + half * 512 + lh * 256 + (lane & 15) * 16;
             return join(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024));
         };
         v8i b[FF][2];
@@ -253,19 +255,18 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int64_t blk = nkb * 4096;
-    const int off = (g >> 1) * 2048 + ((g & 1) * 32 + r) * 16;
-    const uint8_t* const bp = Bq + n0 / 32 * blk + off + (int)(n0 & 16) * 16;
+    const int64_t blk = nkb * 2048;
+    const uint8_t* const bp = Bq + blockIdx.x * blk + lane * 16;
     const float* const sp = Bs + n0 / 128 * nkb;
     const uint8_t* ap[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) ap[i] = Aq + (i >> 1) * blk + off + (i & 1) * 256;
+    for (int i = 0; i < NT; ++i) ap[i] = Aq + (i * 16 < T ? i : 0) * blk + lane * 16;
 
     v4f acc[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = v4f{0, 0, 0, 0};
     for (int64_t kb = wave; kb < nkb; kb += 8) {
-        const uint8_t* const p = bp + kb * 4096;
+        const uint8_t* const p = bp + kb * 2048;
         const v8i b = join(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024));
         const float sb = sp[kb];
         v8bf wb[4];
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
         for (int q = 0; q < 4; ++q) wb[q] = widen_e4m3(b[2 * q], b[2 * q + 1]);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const uint8_t* const x = ap[i] + kb * 4096;
+            const uint8_t* const x = ap[i] + kb * 2048;
             const v8i a = join(*reinterpret_cast<const uint4*>(x), *reinterpret_cast<const uint4*>(x + 1024));
             const float s = As[kb * t_ld + i * 16 + r] * sb;
             v4f t = v4f{0, 0, 0, 0};

@@ -7,8 +7,8 @@
 //   3. per 16 output columns: every chosen expert's down product, weighted and summed.
 //
 // The layer is bound by reading the chosen experts' codes once.  Wavefronts read codes
-// straight from memory in the packed order (lane l of a 16-row half block: row l % 16,
-// inputs 32 (l / 16) .. + 31), widen them to bf16 (exact) and feed
+// straight from memory in the packed order (lane l of a run: row l % 16, inputs
+// 32 (l / 16) .. + 31), widen them to bf16 (exact) and feed
 // v_mfma_f32_16x16x32_bf16 with 16 tokens on the other side; a block's sum of 128 products
 // is scaled by the block's weight scale in fp32.
 //
@@ -25,7 +25,8 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int MAX_T = W4A4_MOE_MAX_T;
-constexpr int WAVES = 8;
+constexpr int SLOT_E = 256;   // experts that the up kernel's slot search holds in a wavefront's registers
+constexpr int WAVES = 4;   // of the up kernel: together a workgroup's rs x ks
 
 // Order of logits as integers: larger first, a NaN before every number, -0 = +0.
 __device__ __forceinline__ uint32_t rank_key(float l) {
@@ -54,95 +55,216 @@ __device__ __forceinline__ void load8(const uint16_t* p, float* v) {
 
 // ---------------------------------------------------------------- 1. router
 
-constexpr int LT = 4;   // tokens per wavefront
-// Wavefront: one expert x LT tokens.  The last column of workgroups writes the bf16 copy of
-// its tokens (zero padded to d_pad) and clears the experts' counts.
-template <typename X, typename R>
+__host__ __device__ constexpr int logits_ld(int E) { return (E + 3) / 4 * 4; }   // row stride of the logits
+
+constexpr int LE = 2;   // experts per workgroup
+// Workgroup: LE experts x LT tokens, the inputs dealt over its 256 lanes.  Workgroups past the
+// experts' write the bf16 copy of X (zero padded to d_pad), 2048 inputs of LT tokens each; there
+// are none where X itself is bf16 without padding.
+template <int LT, typename X, typename R>
 __global__ __launch_bounds__(256) void moe_logits_kernel(const X* __restrict__ x, const R* __restrict__ router, int T, int d,
                                                          int d_pad, int E, int vec, float* __restrict__ logits,
-                                                         uint16_t* __restrict__ xb, int32_t* __restrict__ count) {
-    const int lane = threadIdx.x & 63;
+                                                         uint16_t* __restrict__ xb) {
+    __shared__ float part[4][LE * LT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int t0 = blockIdx.y * LT;
-    if (blockIdx.x == gridDim.x - 1) {
-        for (int i = threadIdx.x; i < LT * d_pad; i += 256) {
-            const int t = t0 + i / d_pad, p = i % d_pad;
-            if (t < T) xb[(int64_t)t * d_pad + p] = p < d ? bf16_rne(load1(x + (int64_t)t * d + p)) : 0;
+    const int ne = (E + LE - 1) / LE;
+    if ((int)blockIdx.x >= ne) {
+        const int p = ((int)blockIdx.x - ne) * 2048 + tid * 8;
+        if (p >= d_pad) return;
+        for (int t = t0; t < t0 + LT && t < T; ++t) {
+            const X* const r = x + (int64_t)t * d;
+            float v[8];
+            if (vec && p + 8 <= d) {
+                load8(r + p, v);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = p + q < d ? load1(r + p + q) : 0.0f;
+            }
+            *reinterpret_cast<uint4*>(xb + (int64_t)t * d_pad + p) =
+                make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
         }
-        if (blockIdx.y == 0)
-            for (int e = threadIdx.x; e < E; e += 256) count[e] = 0;
         return;
     }
-    const int e = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (e >= E) return;
-    const R* const w = router + (int64_t)e * d;
-    float acc[LT];
+    const int e0 = blockIdx.x * LE;
+    float acc[LE][LT];
+    const R* wr[LE];
     const X* xr[LT];
 #pragma unroll
+    for (int j = 0; j < LE; ++j) wr[j] = router + (int64_t)(e0 + j < E ? e0 + j : E - 1) * d;
+#pragma unroll
     for (int i = 0; i < LT; ++i) {
-        acc[i] = 0.0f;
         xr[i] = x + (int64_t)(t0 + i < T ? t0 + i : T - 1) * d;
+#pragma unroll
+        for (int j = 0; j < LE; ++j) acc[j][i] = 0.0f;
     }
-    int p = 0;
     if (vec) {
-        for (p = lane * 8; p + 8 <= d; p += 512) {
-            float a[8], b[8];
-            load8(w + p, a);
+#pragma unroll 2
+        for (int p = tid * 8; p < d; p += 2048) {
+            float a[LE][8], b[8];
+#pragma unroll
+            for (int j = 0; j < LE; ++j) load8(wr[j] + p, a[j]);
 #pragma unroll
             for (int i = 0; i < LT; ++i) {
                 load8(xr[i] + p, b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i] = __builtin_fmaf(a[j], b[j], acc[i]);
+                for (int j = 0; j < LE; ++j)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) acc[j][i] = __builtin_fmaf(a[j][q], b[q], acc[j][i]);
             }
         }
     } else {
-        for (p = lane; p < d; p += 64) {
-            const float a = load1(w + p);
+        for (int p = tid; p < d; p += 256) {
 #pragma unroll
-            for (int i = 0; i < LT; ++i) acc[i] = __builtin_fmaf(a, load1(xr[i] + p), acc[i]);
+            for (int i = 0; i < LT; ++i) {
+                const float b = load1(xr[i] + p);
+#pragma unroll
+                for (int j = 0; j < LE; ++j) acc[j][i] = __builtin_fmaf(load1(wr[j] + p), b, acc[j][i]);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < LT; ++i) {
+    for (int j = 0; j < LE; ++j)
 #pragma unroll
-        for (int o = 32; o; o >>= 1) acc[i] += __shfl_xor(acc[i], o);
-        if (lane == 0 && t0 + i < T) logits[(int64_t)(t0 + i) * E + e] = acc[i];
+        for (int i = 0; i < LT; ++i) {
+#pragma unroll
+            for (int o = 32; o; o >>= 1) acc[j][i] += __shfl_xor(acc[j][i], o);
+            if (lane == 0) part[wave][j * LT + i] = acc[j][i];
+        }
+    __syncthreads();
+    if (tid < LE * LT) {
+        const int e = e0 + tid / LT, t = t0 + tid % LT;
+        if (e < E && t < T) logits[(int64_t)t * logits_ld(E) + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
     }
 }
 
 // ---------------------------------------------------------------- products
 
-// Byte offset of this lane's first 16 codes of the 16-row half block `half` of a 32-row run.
-__device__ __forceinline__ int lane_off(int half) {
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    return (g >> 1) * 2048 + ((g & 1) * 32 + half * 16 + r) * 16;
-}
-
 struct Codes {
     uint4 lo, hi;   // a lane's 32 codes of one block
 };
-__device__ __forceinline__ Codes load_codes(const uint8_t* p) {
-    return Codes{*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024)};
+// Buffer loads: a uniform descriptor, a lane offset that stays in one register for a whole stream
+// and a uniform offset that walks it (flat addresses cost two registers a load in flight).
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
-// acc += scale * (16 rows x 128 inputs of codes) . (128 inputs x 16 tokens); x: this lane's
-// 32 consecutive bf16 values of its token.
-__device__ __forceinline__ void block_mma(v4f& acc, const Codes& c, const uint4* x, float scale) {
+__device__ __forceinline__ uint4 load_at(Rsrc p, uint32_t lane_off, uint32_t off) {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(p, (int)lane_off, (int)off, 0));
+}
+// The same for codes, which a call reads once: marked non-temporal, they do not push what is read
+// again (tokens, h, routing) out of the L2 (up step of 64 tokens, 64 experts of 5120 x 1536: 190 to
+// 176 us).
+__device__ __forceinline__ uint4 load_once(Rsrc p, uint32_t lane_off, uint32_t off) {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(p, (int)lane_off, (int)off, 2));
+}
+// Scale of block b, the same address in every lane: a vector load, so that its wait is the codes'
+// (scalar loads return out of order and would each be waited for by themselves).
+__device__ __forceinline__ float load_scale(Rsrc p, uint32_t lane_off, uint32_t b) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(p, (int)lane_off, (int)b * 4, 0));
+}
+// Added to the lane offset of a load that nothing needs: past every descriptor's range (which is
+// at most 2^26 bytes), it reads zeros and no memory.
+constexpr uint32_t NO_LOAD = 0x80000000u;
+// (16 rows x 128 inputs of codes) . (128 inputs x 16 tokens); x: this lane's 32 consecutive
+// bf16 values of its token.
+__device__ __forceinline__ v4f block_mma(const Codes& c, const uint4* x) {
     const uint32_t w[8] = {c.lo.x, c.lo.y, c.lo.z, c.lo.w, c.hi.x, c.hi.y, c.hi.z, c.hi.w};
     v4f t = v4f{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_e4m3(w[2 * j], w[2 * j + 1]), __builtin_bit_cast(v8bf, x[j]), t, 0, 0, 0);
+    return t;
+}
+
+// acc[m][i] += the scaled blocks kb0, kb0 + step, ... (n of them) of NM row tiles (wp, sp: codes and
+// scales of the row tiles' nkb blocks, uniform) on NT token tiles, whose operand of block b starts
+// at x0 + b * 256 + xoff (the lane's 64 bytes).  A ring of D blocks per wavefront: a block's
+// registers are refilled as soon as they are used, so D - 1 blocks are always in flight.  The code
+// is kept short: these kernels run
+// for a few microseconds from a cold instruction cache.
+template <int D, int NM, int NT>
+__device__ __forceinline__ void stream_blocks(v4f (&acc)[NM][NT], const uint8_t* const (&wp)[NM], const float* const (&sp)[NM],
+                                              Rsrc x0, const uint32_t (&xoff)[NT], int nkb, int kb0, int n, int step) {
+    if (n <= 0) return;
+    const uint32_t woff = (threadIdx.x & 63) * 16;
+    Rsrc wr[NM], sr[NM];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(t[r], scale, acc[r]);
+    for (int m = 0; m < NM; ++m) {
+        wr[m] = rsrc(wp[m], (uint32_t)nkb * 2048u);
+        sr[m] = rsrc(sp[m], (uint32_t)nkb * 4u);
+    }
+    Codes w[D][NM];
+    float s[D][NM];
+    uint4 x[D][NT][4];
+    auto load = [&](int j, int i) __attribute__((always_inline)) {
+        const uint32_t b = (uint32_t)(kb0 + (i < n ? i : 0) * step), off = i < n ? 0 : NO_LOAD;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            w[j][m] = Codes{load_once(wr[m], woff + off, b * 2048), load_once(wr[m], woff + off + 1024, b * 2048)};
+            s[j][m] = load_scale(sr[m], off, b);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[j][t][q] = load_at(x0, xoff[t] + off + q * 16, b * 256);
+    };
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+        load(j, j);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int i = 0; i < n; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            const bool in = i + j < n;   // uniform; past the end the sums stay as they are
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const v4f v = block_mma(w[j][m], x[j][t]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[m][t][r] = in ? __builtin_fmaf(v[r], s[j][m], acc[m][t][r]) : acc[m][t][r];
+                }
+            load(j, i + j + D);
+            __builtin_amdgcn_sched_barrier(0);   // each block waits for its own loads only
+        }
+    }
+}
+
+// h is kept as the down products read it: tiles of 16 tokens of one expert x 128 columns (4 KiB),
+// 16-byte piece q of lane l at q * 1024 + l * 16: token l % 16, columns 32 (l / 16) + 8 q ..
+constexpr int H_TILE = 4096, H_PIECE = 1024;
+
+// Sum over the eight lanes of an aligned group.
+__device__ __forceinline__ int sum8(int c) {
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) c += __shfl_xor(c, o);
+    return c;
+}
+
+// Maximum over the wavefront (in every lane).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    // row_shr 1, 2, 4, 8, then lane 15 of each row to the next row and lane 31 to the upper half;
+    // lanes without a source keep the identity 0
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 struct UpArgs {
     const float* logits;
     const uint16_t* xb;
-    int32_t *ids, *count, *pairs;
+    int32_t *ids, *pos;
     float* p;
     uint16_t* h;
     int T, E, k, renorm, f, by_slot;
-    int nkb_d, f_pad, n_pad;                 // d blocks of 128, roundup(f, 128), roundup(f, 32)
+    int rs, ks;                              // wavefronts along the rows (16 each) and along d
+    int nkb_d, f_pad, n_pad;                 // d blocks of 128, roundup(f, 128), roundup(f, 16)
     const uint8_t *gate, *up;
     const float *gate_s, *up_s;
     int64_t mat_codes, mat_scales;           // bytes / scales per expert
@@ -150,137 +272,158 @@ struct UpArgs {
 
 // ---------------------------------------------------------------- 2. up
 
-template <bool GATED, int NT>
-__device__ __forceinline__ void up_chunk(const UpArgs& a, int e, int row0, const int32_t* list, int c0, int n, float* red) {
-    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int NM = GATED ? 2 : 1, LD = 20;
-    const int64_t cofs = (int64_t)e * a.mat_codes + (int64_t)(row0 / 32) * a.nkb_d * 4096 + lane_off((row0 >> 4) & 1);
-    const int64_t sofs = (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * a.nkb_d;
-    const uint16_t* xp[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int q = c0 + i * 16 + r;
-        xp[i] = a.xb + (int64_t)(list[q < n ? q : c0] / a.k) * a.nkb_d * 128 + g * 32;
-    }
-    v4f acc[NM][NT];
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[m][i] = v4f{0, 0, 0, 0};
-    for (int kb = wave; kb < a.nkb_d; kb += WAVES) {
-        Codes w[NM];
-        float s[NM];
-        w[0] = load_codes(a.up + cofs + (int64_t)kb * 4096);
-        s[0] = a.up_s[sofs + kb];
-        if constexpr (GATED) {
-            w[1] = load_codes(a.gate + cofs + (int64_t)kb * 4096);
-            s[1] = a.gate_s[sofs + kb];
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            uint4 x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(xp[i] + kb * 128 + 8 * j);
-#pragma unroll
-            for (int m = 0; m < NM; ++m) block_mma(acc[m][i], w[m], x, s[m]);
-        }
-    }
-    // lane: token r of tile i, rows 4 g .. 4 g + 3
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            *reinterpret_cast<v4f*>(red + (((m * WAVES + wave) * NT + i) * 16 + r) * LD + 4 * g) = acc[m][i];
-    __syncthreads();
-    for (int i = tid; i < NT * 256; i += WAVES * 64) {
-        const int tok = i >> 4, row = i & 15;
-        if (c0 + tok < n) {
-            float u = 0.0f, v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) {
-                u += red[(w * NT * 16 + tok) * LD + row];
-                if constexpr (GATED) v += red[((WAVES + w) * NT * 16 + tok) * LD + row];
-            }
-            float y;
-            if constexpr (GATED) y = v / (1.0f + expf(-v)) * u;
-            else y = gelu_tanh_f32(u);
-            a.h[(int64_t)list[c0 + tok] * a.f_pad + row0 + row] = row0 + row < a.f ? bf16_rne(y) : 0;
-        }
-    }
-    __syncthreads();
-}
+// A list entry: token, and the rank that the expert has there.
+__device__ __forceinline__ int entry(int t, int rank) { return t << 8 | rank; }
+__device__ __forceinline__ int entry_pair(int v, int k) { return (v >> 8) * k + (v & 255); }
 
-template <bool GATED>
-__global__ __launch_bounds__(WAVES * 64) void moe_up_kernel(UpArgs a) {
+// NT: token tiles that a pass over the codes takes.  The workgroup computes rs row tiles, each summed
+// over ks wavefronts.
+template <bool GATED, int NT>
+__global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe_up_kernel(UpArgs a) {
+    constexpr int NM = GATED ? 2 : 1, LD = 20;
+    constexpr int D = NT == 1 ? (GATED ? 2 : 4) : NT == 2 ? 2 : 1;
     __shared__ int32_t list[MAX_T];
     __shared__ int32_t rank[MAX_T];
     __shared__ uint32_t top[MAX_T];          // key of the token's largest logit
-    __shared__ int32_t head[2];              // expert, tokens of it
-    __shared__ uint32_t keys[W4A4_MOE_MAX_E];
-    __shared__ __attribute__((aligned(16))) float red[(GATED ? 2 : 1) * WAVES * 4 * 16 * 20];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int row0 = blockIdx.x * 16;
+    __shared__ int32_t count;                // tokens of the expert
+    __shared__ __attribute__((aligned(16))) float red[NM * WAVES * NT * 16 * LD];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ld = logits_ld(a.E);
 
     // Which expert: the grid's second dimension counts experts, or, where the tokens choose
     // fewer than there are, slots t * k + rank; a slot whose expert an earlier token chose too is
     // left to that token's slot.
-    int e = blockIdx.y;
+    int e = blockIdx.y, n = 1;
     if (a.by_slot) {
+        // the (want + 1)-th of the token's logits, by every wavefront for itself: logit j * 64 + lane
+        // in a lane's j-th register, the largest taken want times
         const int t = blockIdx.y / a.k, want = blockIdx.y - t * a.k;
-        for (int i = tid; i < a.E; i += WAVES * 64) keys[i] = rank_key(a.logits[(int64_t)t * a.E + i]);
-        __syncthreads();
-        for (int i = tid; i < a.E; i += WAVES * 64) {
-            const uint32_t key = keys[i];
-            int c = 0;
-            for (int j = 0; j < a.E; ++j) c += before(keys[j], j, key, i) ? 1 : 0;
-            if (c == want) head[0] = i;
-        }
-        __syncthreads();
-        e = head[0];
-    }
-    // The rank of e in every token: eight lanes a token.
-    for (int t = tid >> 3; t < a.T; t += WAVES * 8) {
-        const float* l = a.logits + (int64_t)t * a.E;
-        const uint32_t key = rank_key(l[e]);
-        int c = 0;
-        uint32_t m = 0;
-        for (int j = tid & 7; j < a.E; j += 8) {
-            const uint32_t kj = rank_key(l[j]);
-            c += before(kj, j, key, e) ? 1 : 0;
-            m = max(m, kj);
-        }
+        const float* l = a.logits + t * ld;
+        uint32_t key[SLOT_E / 64];
 #pragma unroll
-        for (int o = 1; o < 8; o *= 2) {
-            c += __shfl_xor(c, o);
-            m = max(m, (uint32_t)__shfl_xor((int)m, o));
+        for (int j = 0; j < SLOT_E / 64; ++j) key[j] = j * 64 + lane < a.E ? rank_key(l[j * 64 + lane]) : 0u;   // 0: no logit's key
+        for (int i = 0; i <= want; ++i) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < SLOT_E / 64; ++j) m = max(m, key[j]);
+            m = wave_max(m);
+            if (i == 0) top[t] = m;
+            e = -1;
+#pragma unroll
+            for (int j = 0; j < SLOT_E / 64; ++j) {
+                const uint64_t b = __ballot(key[j] == m);
+                const bool here = e < 0 && b;
+                const int at = __builtin_ctzll(b | 1ull << 63);
+                e = here ? j * 64 + at : e;
+                key[j] = here && lane == at ? 0u : key[j];
+            }
         }
-        if ((tid & 7) == 0) {
-            rank[t] = c;
-            top[t] = m;
+        e = __builtin_amdgcn_readfirstlane(e);
+        list[0] = entry(t, want);   // every lane writes what it reads: one token needs no barrier
+    }
+    if (!a.by_slot || a.T > 1) {
+        if (a.by_slot) __syncthreads();
+        // the rank of e in every token: eight lanes a token
+        for (int t = tid >> 3; t < a.T; t += WAVES * 8) {
+            const float* l = a.logits + t * ld;
+            const uint32_t key = rank_key(l[e]);
+            int c = 0;
+            uint32_t m = 0;
+#pragma unroll 2
+            for (int j = (tid & 7) * 4; j < a.E; j += 32) {
+                const float4 v = *reinterpret_cast<const float4*>(l + j);
+                const float lv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t kj = j + q < a.E ? rank_key(lv[q]) : 0u;
+                    c += before(kj, j + q, key, e) ? 1 : 0;
+                    m = max(m, kj);
+                }
+            }
+            c = sum8(c);
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+            if ((tid & 7) == 0) {
+                rank[t] = c;
+                top[t] = m;
+            }
+        }
+        __syncthreads();
+        if (tid < 64) {
+            n = 0;
+            for (int t0 = 0; t0 < a.T; t0 += 64) {
+                const int t = t0 + lane;
+                const bool in = t < a.T && rank[t < a.T ? t : 0] < a.k;
+                const uint64_t b = __ballot(in);
+                if (in) list[n + __popcll(b & ((1ull << lane) - 1))] = entry(t, rank[t]);
+                n += __popcll(b);
+            }
+            if (lane == 0) count = n;
+        }
+        __syncthreads();
+        n = __builtin_amdgcn_readfirstlane(count);
+        if (n == 0 || (a.by_slot && entry_pair(list[0], a.k) < (int)blockIdx.y)) return;
+    }
+
+    const int wk = wave % a.ks, row0 = (blockIdx.x * a.rs + wave / a.ks) * 16;
+    const int nkb = row0 < a.n_pad ? a.nkb_d : 0;   // past the packed rows: only h's padding
+    const int64_t cofs = (int64_t)e * a.mat_codes + (int64_t)(row0 / 16) * a.nkb_d * 2048;
+    const int64_t sofs = (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * a.nkb_d;
+    const Rsrc xr = rsrc(a.xb, (uint32_t)a.T * (uint32_t)a.nkb_d * 256u);
+    const int nb = nkb > wk ? (nkb - wk + a.ks - 1) / a.ks : 0;
+    const int64_t slot = (int64_t)(a.by_slot ? (int)blockIdx.y : e) * ((a.T + 15) / 16);
+    for (int c0 = 0; c0 < n; c0 += NT * 16) {
+        uint32_t xoff[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int q = c0 + i * 16 + r;
+            xoff[i] = (uint32_t)(list[q < n ? q : c0] >> 8) * (uint32_t)a.nkb_d * 256u + g * 64;
+        }
+        v4f acc[NM][NT];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[m][i] = v4f{0, 0, 0, 0};
+        if constexpr (GATED) {
+            const uint8_t* const wp[2] = {a.up + cofs, a.gate + cofs};
+            const float* const sp[2] = {a.up_s + sofs, a.gate_s + sofs};
+            stream_blocks<D, 2, NT>(acc, wp, sp, xr, xoff, a.nkb_d, wk, nb, a.ks);
+        } else {
+            const uint8_t* const wp[1] = {a.up + cofs};
+            const float* const sp[1] = {a.up_s + sofs};
+            stream_blocks<D, 1, NT>(acc, wp, sp, xr, xoff, a.nkb_d, wk, nb, a.ks);
+        }
+        if (c0) __syncthreads();
+        // lane: token r of tile i, rows 4 g .. 4 g + 3
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                *reinterpret_cast<v4f*>(red + (((m * WAVES + wave) * NT + i) * 16 + r) * LD + 4 * g) = acc[m][i];
+        __syncthreads();
+        for (int q = tid; q < a.rs * NT * 256; q += WAVES * 64) {
+            const int tile = q / (NT * 256), at = q / 16 % (NT * 16), row = q & 15;
+            const int hr = (blockIdx.x * a.rs + tile) * 16 + row;
+            if (c0 + at >= n || hr >= a.f_pad) continue;
+            float u = 0.0f, v = 0.0f;
+            for (int w = tile * a.ks; w < (tile + 1) * a.ks; ++w) {
+                u += red[(w * NT * 16 + at) * LD + row];
+                if constexpr (GATED) v += red[((WAVES + w) * NT * 16 + at) * LD + row];
+            }
+            if constexpr (GATED) u = v / (1.0f + expf(-v)) * u;
+            else u = gelu_tanh_f32(u);
+            const int64_t base = slot + c0 / 16 + at / 16;
+            uint8_t* const dst = reinterpret_cast<uint8_t*>(a.h) + (base * (a.f_pad / 128) + hr / 128) * H_TILE +
+                                 (hr % 32 / 8) * H_PIECE + ((hr % 128 / 32) * 16 + at % 16) * 16 + hr % 8 * 2;
+            *reinterpret_cast<uint16_t*>(dst) = hr < a.f ? bf16_rne(u) : 0;
         }
     }
-    __syncthreads();
-    if (tid < 64) {
-        int n = 0;
-        for (int t0 = 0; t0 < a.T; t0 += 64) {
-            const int t = t0 + lane;
-            const bool in = t < a.T && rank[t < a.T ? t : 0] < a.k;
-            const uint64_t b = __ballot(in);
-            if (in) list[n + __popcll(b & ((1ull << lane) - 1))] = t * a.k + rank[t];
-            n += __popcll(b);
-        }
-        if (lane == 0) head[1] = n;
-    }
-    __syncthreads();
-    const int n = head[1];
-    if (n == 0 || (a.by_slot && list[0] < (int)blockIdx.y)) return;
 
     if (blockIdx.x == 0) {   // what the down step reads of the routing, once per expert
-        if (tid == 0) a.count[e] = n;
         for (int q = tid >> 3; q < n; q += WAVES * 8) {
-            const int pair = list[q], t = pair / a.k;
-            const float* l = a.logits + (int64_t)t * a.E;
+            const int t = list[q] >> 8, pair = entry_pair(list[q], a.k);
+            const float* l = a.logits + t * ld;
             const uint32_t mk = top[t];
             const float mx = mk == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u)
                                                : __uint_as_float(mk ^ ((mk >> 31) ? 0x80000000u : 0xFFFFFFFFu));
@@ -294,26 +437,9 @@ __global__ __launch_bounds__(WAVES * 64) void moe_up_kernel(UpArgs a) {
             }
             if ((tid & 7) == 0) {
                 a.ids[pair] = e;
+                a.pos[pair] = q;
                 a.p[pair] = v;
-                a.pairs[(int64_t)e * a.T + q] = pair;
             }
-        }
-    }
-    if (row0 >= a.n_pad) {   // past the packed rows: only h's padding
-        for (int i = tid; i < n * 16; i += WAVES * 64) a.h[(int64_t)list[i >> 4] * a.f_pad + row0 + (i & 15)] = 0;
-        return;
-    }
-    for (int c0 = 0; c0 < n;) {
-        const int left = n - c0;
-        if (left <= 16) {
-            up_chunk<GATED, 1>(a, e, row0, list, c0, n, red);
-            c0 += 16;
-        } else if (left <= 32) {
-            up_chunk<GATED, 2>(a, e, row0, list, c0, n, red);
-            c0 += 32;
-        } else {
-            up_chunk<GATED, 4>(a, e, row0, list, c0, n, red);
-            c0 += 64;
         }
     }
 }
@@ -321,10 +447,10 @@ __global__ __launch_bounds__(WAVES * 64) void moe_up_kernel(UpArgs a) {
 // ---------------------------------------------------------------- 3. down
 
 struct DownArgs {
-    const int32_t *count, *pairs;
+    const int32_t *ids, *pos;
     const float* p;
     const uint16_t* h;
-    int T, E, k, renorm, d;
+    int T, E, k, renorm, d, by_slot;
     int nkb_f;                               // f blocks of 128
     const uint8_t* codes;
     const float* scales;
@@ -332,140 +458,264 @@ struct DownArgs {
     void* out;
 };
 
-// TB: tokens the sums are laid out for.  The wavefronts share the (expert, block) sequence in
-// equal consecutive ranges; each adds to sums of its own, which are added in wavefront order.
-template <int TB, int OUT>
-__global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(DownArgs a) {
-    __shared__ __attribute__((aligned(16))) float sums[WAVES * TB * 16];
-    __shared__ float den[TB];
-    __shared__ uint16_t active[W4A4_MOE_MAX_E];
-    __shared__ int n_active;
+// TB: tokens the sums are laid out for; RT: row tiles (16 outputs) per workgroup.  The work is one
+// sequence of groups of D blocks: segment by segment (up to 16 tokens of one expert), the segment's
+// nkb_f blocks, the last group of a segment cut short.  The W wavefronts take equal consecutive
+// ranges of it; a wavefront's ring of D blocks in flight runs on from segment to segment, and
+// where a segment ends its sums, times the tokens' probabilities, go to the wavefront's own sums in
+// LDS, which are added in wavefront order at the end.
+template <int TB, int W, int RT, int OUT>
+__global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_down_kernel(DownArgs a) {
+    constexpr int PB = TB * W4A4_MOE_MAX_K, SEGS = W4A4_MOE_MAX_E + PB / 16, RL = 16 * RT;
+    constexpr int D = 3;
+    __shared__ __attribute__((aligned(16))) float sums[W * TB * RL];
+    __shared__ float den[TB], prob[PB];
+    __shared__ uint16_t list[PB];              // pairs, expert by expert
+    __shared__ int32_t first[W4A4_MOE_MAX_E];  // by expert: pairs, then where its list starts
+    __shared__ uint16_t lead[W4A4_MOE_MAX_E];  // by expert: its first pair
+    __shared__ uint16_t seg_e[SEGS], seg_l[SEGS];   // by segment: expert, place in list
+    __shared__ uint8_t seg_c[SEGS], seg_n[SEGS];    // its number within the expert, tokens
+    __shared__ int n_seg;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row0 = blockIdx.x * 16;
-    for (int i = tid; i < WAVES * TB * 16; i += WAVES * 64) sums[i] = 0.0f;
-    for (int t = tid; t < a.T; t += WAVES * 64) {
+    const int row0 = blockIdx.x * RL, pairs = a.T * a.k, nkb = a.nkb_f, tt = (a.T + 15) / 16;
+    for (int i = tid; i < W * TB * RL; i += W * 64) sums[i] = 0.0f;
+    if (a.T == 1) {   // every pair is a segment
+        for (int i = tid; i < pairs; i += W * 64) {
+            const int e = a.ids[i];
+            prob[i] = a.p[i];
+            list[i] = seg_l[i] = lead[e] = (uint16_t)i;
+            seg_e[i] = (uint16_t)e;
+            seg_c[i] = 0;
+            seg_n[i] = 1;
+        }
+        if (tid == 0) n_seg = pairs;
+        __syncthreads();
+    } else {
+        for (int i = tid; i < a.E; i += W * 64) first[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < pairs; i += W * 64) {
+            prob[i] = a.p[i];
+            atomicAdd(&first[a.ids[i]], 1);
+        }
+        __syncthreads();
+        if (tid < 64) {
+            int at = 0, seg = 0;
+            for (int e0 = 0; e0 < a.E; e0 += 64) {
+                const int e = e0 + lane, c = e < a.E ? first[e] : 0;
+                int v = c | ((c + 15) / 16) << 16;       // pairs and segments, summed over the lanes before
+#pragma unroll
+                for (int o = 1; o < 64; o *= 2) {
+                    const int u = __shfl_up(v, o);
+                    v += lane >= o ? u : 0;
+                }
+                const int l0 = at + (v & 0xFFFF) - c;
+                int s = seg + (v >> 16) - (c + 15) / 16;
+                if (e < a.E) first[e] = l0;
+                for (int q = 0; q * 16 < c; ++q, ++s) {
+                    seg_e[s] = (uint16_t)e;
+                    seg_l[s] = (uint16_t)(l0 + q * 16);
+                    seg_c[s] = (uint8_t)q;
+                    seg_n[s] = (uint8_t)(c - q * 16 < 16 ? c - q * 16 : 16);
+                }
+                const int all = __shfl(v, 63);
+                at += all & 0xFFFF;
+                seg += all >> 16;
+            }
+            if (lane == 0) n_seg = seg;
+        }
+        __syncthreads();
+        for (int i = tid; i < pairs; i += W * 64) {   // in the order in which the up step laid h out
+            const int e = a.ids[i], q = a.pos[i];
+            list[first[e] + q] = (uint16_t)i;
+            if (q == 0) lead[e] = (uint16_t)i;
+        }
+    }
+    for (int t = tid; t < a.T; t += W * 64) {
         float s = 1.0f;
         if (a.renorm) {
             s = 0.0f;
-            for (int j = 0; j < a.k; ++j) s += a.p[t * a.k + j];
+            for (int j = 0; j < a.k; ++j) s += prob[t * a.k + j];
         }
         den[t] = s;
     }
-    if (tid < 64) {
-        int n = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 64) {
-            const bool in = e0 + lane < a.E && a.count[e0 + lane] > 0;
-            const uint64_t b = __ballot(in);
-            if (in) active[n + __popcll(b & ((1ull << lane) - 1))] = (uint16_t)(e0 + lane);
-            n += __popcll(b);
+    __syncthreads();
+
+    const int groups = (nkb + D - 1) / D;          // of a segment
+    const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(n_seg) * groups;
+    const int begin = (int)(total * wave / W), len = (int)(total * (wave + 1) / W) - begin;
+    const int tiles = (a.d + 15) / 16 - blockIdx.x * RT < RT ? (a.d + 15) / 16 - blockIdx.x * RT : RT;
+    float* const mine = sums + wave * TB * RL;
+    if (len > 0) {
+        int seg = begin / groups, lkb = (begin - seg * groups) * D;   // the group that is loaded
+        Rsrc wr, xr, sr;
+        uint32_t xoff;
+        auto open = [&](int sg) __attribute__((always_inline)) {
+            const int e = __builtin_amdgcn_readfirstlane(seg_e[sg]), n = __builtin_amdgcn_readfirstlane(seg_n[sg]);
+            const int slot = a.by_slot ? __builtin_amdgcn_readfirstlane(lead[e]) : e;
+            const int64_t tile = (int64_t)slot * tt + __builtin_amdgcn_readfirstlane(seg_c[sg]);
+            wr = rsrc(a.codes + (int64_t)e * a.mat_codes + (int64_t)blockIdx.x * RT * nkb * 2048, (uint32_t)tiles * nkb * 2048u);
+            xr = rsrc(reinterpret_cast<const uint8_t*>(a.h) + tile * nkb * H_TILE, (uint32_t)nkb * H_TILE);
+            sr = rsrc(a.scales + (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * nkb, (uint32_t)nkb * 4u);
+            // lanes past the segment's tokens read the first one's h
+            xoff = (uint32_t)(r < n ? lane : lane & 48) * 16;
+        };
+        Codes w[D][RT];
+        uint4 x[D][4];
+        float sc[D];
+        auto load = [&](int j) __attribute__((always_inline)) {
+            const uint32_t b = (uint32_t)(lkb + j), off = lkb + j < nkb ? 0 : NO_LOAD;
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const uint32_t woff = off + lane * 16 + t * (uint32_t)nkb * 2048u;
+                w[j][t] = Codes{load_once(wr, woff, b * 2048u), load_once(wr, woff + 1024, b * 2048u)};
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[j][q] = load_at(xr, xoff + off + q * H_PIECE, b * H_TILE);
+            sc[j] = load_scale(sr, off, b);
+        };
+        open(seg);
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            load(j);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (lane == 0) n_active = n;
+        v4f acc[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t] = v4f{0, 0, 0, 0};
+        for (int i = 0; i < len; ++i) {
+            const int kb = lkb, sg = seg;          // the group that is used
+            lkb += D;
+            const bool ends = lkb >= nkb;
+            if (i + 1 == len) {
+                lkb = nkb;                         // nothing left to load
+            } else if (ends) {
+                lkb = 0;
+                open(++seg);
+            }
+#pragma unroll
+            for (int j = 0; j < D; ++j) {
+                const bool in = kb + j < nkb;      // uniform; past the end the sums stay as they are
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const v4f v = block_mma(w[j][t], x[j]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[t][q] = in ? __builtin_fmaf(v[q], sc[j], acc[t][q]) : acc[t][q];
+                }
+                load(j);
+                __builtin_amdgcn_sched_barrier(0);   // each block waits for its own loads only
+            }
+            if (ends || i + 1 == len) {            // the segment, or the wavefront's part of it, ends
+                if (r < seg_n[sg]) {               // tokens of one expert are distinct: no two lanes meet
+                    const int pair = list[seg_l[sg] + r], t = pair / a.k;
+                    const float pw = a.renorm ? prob[pair] / den[t] : prob[pair];
+#pragma unroll
+                    for (int u = 0; u < RT; ++u) {
+                        v4f* const s = reinterpret_cast<v4f*>(mine + t * RL + u * 16 + 4 * g);
+                        v4f v = *s;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(acc[u][q], pw, v[q]);
+                        *s = v;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < RT; ++u) acc[u] = v4f{0, 0, 0, 0};
+            }
+        }
     }
     __syncthreads();
-    const int total = n_active * a.nkb_f;
-    int pos = (int)((int64_t)total * wave / WAVES);
-    const int end = (int)((int64_t)total * (wave + 1) / WAVES);
-    float* const mine = sums + wave * TB * 16;
-    while (pos < end) {
-        const int ai = pos / a.nkb_f, kb0 = pos - ai * a.nkb_f;
-        const int kb1 = end - pos < a.nkb_f - kb0 ? kb0 + (end - pos) : a.nkb_f;
-        pos += kb1 - kb0;
-        const int e = active[ai];
-        const int n = a.count[e];
-        const int32_t* const list = a.pairs + (int64_t)e * a.T;
-        const uint8_t* const wp = a.codes + (int64_t)e * a.mat_codes + (int64_t)(row0 / 32) * a.nkb_f * 4096 + lane_off((row0 >> 4) & 1);
-        const float* const sp = a.scales + (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * a.nkb_f;
-        for (int c0 = 0; c0 < n; c0 += 16) {
-            const int q = c0 + r;
-            const int pair = list[q < n ? q : c0];
-            const uint16_t* const hp = a.h + (int64_t)pair * a.nkb_f * 128 + g * 32;
-            v4f acc = v4f{0, 0, 0, 0};
-            for (int kb = kb0; kb < kb1; ++kb) {
-                const Codes w = load_codes(wp + (int64_t)kb * 4096);
-                uint4 x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(hp + kb * 128 + 8 * j);
-                block_mma(acc, w, x, sp[kb]);
-            }
-            if (q < n) {   // tokens of one expert are distinct: no two lanes meet
-                const int t = pair / a.k;
-                const float pw = a.renorm ? a.p[pair] / den[t] : a.p[pair];
-                v4f* const s = reinterpret_cast<v4f*>(mine + t * 16 + 4 * g);
-                v4f v = *s;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(acc[i], pw, v[i]);
-                *s = v;
-            }
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < a.T * 16; i += WAVES * 64) {
-        const int t = i >> 4, row = row0 + (i & 15);
+    for (int i = tid; i < a.T * RL; i += W * 64) {
+        const int t = i / RL, row = row0 + i % RL;
         if (row >= a.d) continue;
         float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) y += sums[w * TB * 16 + i];
+        for (int w = 0; w < W; ++w) y += sums[w * TB * RL + i];
         if constexpr (OUT == W4A4_Y_F32) reinterpret_cast<float*>(a.out)[(int64_t)t * a.d + row] = y;
         else reinterpret_cast<uint16_t*>(a.out)[(int64_t)t * a.d + row] = bf16_rne(y);
     }
 }
 
-template <typename X>
-void run_logits(const void* X_, const w4a4_moe& m, int T, float* logits, uint16_t* xb, int32_t* count, hipStream_t st) {
+template <int LT, typename X>
+void run_logits(const void* X_, const w4a4_moe& m, int T, bool copy, float* logits, uint16_t* xb, hipStream_t st) {
     const int d = (int)m.up.d_in, d_pad = (int)m.up.k_pad, E = (int)m.up.n_mat;
-    const dim3 grid((uint32_t)((E + 3) / 4 + 1), (uint32_t)((T + LT - 1) / LT));
+    const dim3 grid((uint32_t)((E + LE - 1) / LE + (copy ? (d_pad + 2047) / 2048 : 0)), (uint32_t)((T + LT - 1) / LT));
     const int vec = d % 8 == 0 ? 1 : 0;
     if (m.router_dtype == W4A4_X_BF16)
-        hipLaunchKernelGGL((moe_logits_kernel<X, uint16_t>), grid, dim3(256), 0, st, (const X*)X_, (const uint16_t*)m.router, T, d,
-                           d_pad, E, vec, logits, xb, count);
+        hipLaunchKernelGGL((moe_logits_kernel<LT, X, uint16_t>), grid, dim3(256), 0, st, (const X*)X_, (const uint16_t*)m.router, T,
+                           d, d_pad, E, vec, logits, xb);
     else
-        hipLaunchKernelGGL((moe_logits_kernel<X, float>), grid, dim3(256), 0, st, (const X*)X_, (const float*)m.router, T, d,
-                           d_pad, E, vec, logits, xb, count);
+        hipLaunchKernelGGL((moe_logits_kernel<LT, X, float>), grid, dim3(256), 0, st, (const X*)X_, (const float*)m.router, T, d,
+                           d_pad, E, vec, logits, xb);
+}
+
+template <bool GATED>
+void run_up(const UpArgs& a, int nt, dim3 grid, hipStream_t st) {
+    const dim3 block(WAVES * 64);
+    if (nt == 1) hipLaunchKernelGGL((moe_up_kernel<GATED, 1>), grid, block, 0, st, a);
+    else if (nt == 2) hipLaunchKernelGGL((moe_up_kernel<GATED, 2>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((moe_up_kernel<GATED, 4>), grid, block, 0, st, a);
 }
 
 template <int OUT>
-void run_down(const DownArgs& a, dim3 grid, hipStream_t st) {
-    const dim3 block(WAVES * 64);
-    if (a.T <= 16) hipLaunchKernelGGL((moe_down_kernel<16, OUT>), grid, block, 0, st, a);
-    else if (a.T <= 64) hipLaunchKernelGGL((moe_down_kernel<64, OUT>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((moe_down_kernel<MAX_T, OUT>), grid, block, 0, st, a);
+void run_down(const DownArgs& a, hipStream_t st) {
+    // 16 wavefronts fit a CU at this kernel's registers: one workgroup of 16, or two of 8 where one
+    // a CU would leave a second round.  Two row tiles halve the reads of h, which for many
+    // tokens come near the codes'.
+    const uint32_t n = (uint32_t)((a.d + 15) / 16);
+    if (a.T <= 16 && n <= 256) hipLaunchKernelGGL((moe_down_kernel<16, 16, 1, OUT>), dim3(n), dim3(1024), 0, st, a);
+    else if (a.T <= 16) hipLaunchKernelGGL((moe_down_kernel<16, 8, 1, OUT>), dim3(n), dim3(512), 0, st, a);
+    else if (a.T <= 64 && n <= 256) hipLaunchKernelGGL((moe_down_kernel<64, 16, 1, OUT>), dim3(n), dim3(1024), 0, st, a);
+    else if (a.T <= 64) hipLaunchKernelGGL((moe_down_kernel<64, 16, 2, OUT>), dim3((n + 1) / 2), dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL((moe_down_kernel<MAX_T, 8, 1, OUT>), dim3(n), dim3(512), 0, st, a);
 }
 
 }  // namespace
 
 hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, const MoeBuffers& b, void* Y, int y_dtype,
                       hipStream_t st) {
-    if (x_dtype == W4A4_X_BF16) run_logits<uint16_t>(X, m, (int)T, b.logits, b.xb, b.count, st);
-    else run_logits<float>(X, m, (int)T, b.logits, b.xb, b.count, st);
+    // X itself serves the products where it is bf16 and its rows need no padding
+    const bool copy = x_dtype != W4A4_X_BF16 || m.up.d_in != m.up.k_pad;
+    if (x_dtype == W4A4_X_BF16) {
+        if (T == 1) run_logits<1, uint16_t>(X, m, (int)T, copy, b.logits, b.xb, st);
+        else run_logits<4, uint16_t>(X, m, (int)T, copy, b.logits, b.xb, st);
+    } else {
+        if (T == 1) run_logits<1, float>(X, m, (int)T, copy, b.logits, b.xb, st);
+        else run_logits<4, float>(X, m, (int)T, copy, b.logits, b.xb, st);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 
     const bool gated = m.activation == W4A4_MOE_SILU_GATED;
     UpArgs u;
-    u.logits = b.logits; u.xb = b.xb; u.ids = b.ids; u.count = b.count; u.pairs = b.pairs; u.p = b.p; u.h = b.h;
+    u.logits = b.logits; u.xb = copy ? b.xb : (const uint16_t*)X; u.ids = b.ids; u.pos = b.pos; u.p = b.p; u.h = b.h;
     u.T = (int)T; u.E = (int)m.up.n_mat; u.k = m.top_k; u.renorm = m.renormalize != 0; u.f = (int)m.up.d_out;
-    u.by_slot = T * m.top_k < m.up.n_mat ? 1 : 0;
+    u.by_slot = moe_by_slot(T, m.top_k, m.up.n_mat) ? 1 : 0;
     u.nkb_d = (int)(m.up.k_pad / 128); u.f_pad = (int)m.down.k_pad; u.n_pad = (int)m.up.n_pad;
     u.gate = gated ? m.gate.codes : nullptr; u.gate_s = gated ? m.gate.scales : nullptr;
     u.up = m.up.codes; u.up_s = m.up.scales;
     u.mat_codes = m.up.n_pad * m.up.k_pad; u.mat_scales = (m.up.d_out + 127) / 128 * (m.up.k_pad / 128);
-    const dim3 grid((uint32_t)(u.f_pad / 16), (uint32_t)(u.by_slot ? T * m.top_k : m.up.n_mat));
-    if (gated) hipLaunchKernelGGL(moe_up_kernel<true>, grid, dim3(WAVES * 64), 0, st, u);
-    else hipLaunchKernelGGL(moe_up_kernel<false>, grid, dim3(WAVES * 64), 0, st, u);
+    const int64_t ny = u.by_slot ? T * m.top_k : m.up.n_mat, tiles = u.f_pad / 16;
+    // 16 wavefronts fit a CU at this kernel's registers: d is split over as many as keep all
+    // of them resident
+    u.ks = ny * tiles <= 1024 ? 4 : ny * tiles <= 2048 ? 2 : 1;
+    u.rs = WAVES / u.ks;
+    const dim3 grid((uint32_t)((tiles + u.rs - 1) / u.rs), (uint32_t)ny);
+    // tokens that an expert takes on average: one pass over its codes should do for most
+    const int nt = T <= 16 || T * m.top_k <= 10 * m.up.n_mat ? 1 : T * m.top_k <= 24 * m.up.n_mat ? 2 : 4;
+    if (gated) run_up<true>(u, nt, grid, st);
+    else run_up<false>(u, nt, grid, st);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
 
     DownArgs d;
-    d.count = b.count; d.pairs = b.pairs; d.p = b.p; d.h = b.h;
-    d.T = u.T; d.E = u.E; d.k = u.k; d.renorm = u.renorm; d.d = (int)m.down.d_out;
+    d.ids = b.ids; d.pos = b.pos; d.p = b.p; d.h = b.h;
+    d.T = u.T; d.E = u.E; d.k = u.k; d.renorm = u.renorm; d.d = (int)m.down.d_out; d.by_slot = u.by_slot;
     d.nkb_f = (int)(m.down.k_pad / 128);
     d.codes = m.down.codes; d.scales = m.down.scales;
     d.mat_codes = m.down.n_pad * m.down.k_pad; d.mat_scales = (m.down.d_out + 127) / 128 * (m.down.k_pad / 128);
     d.out = Y;
-    const dim3 gd((uint32_t)((d.d + 15) / 16));
-    if (y_dtype == W4A4_Y_F32) run_down<W4A4_Y_F32>(d, gd, st);
-    else run_down<W4A4_Y_BF16>(d, gd, st);
+    if (y_dtype == W4A4_Y_F32) run_down<W4A4_Y_F32>(d, st);
+    else run_down<W4A4_Y_BF16>(d, st);
     return hipGetLastError();
 }
 

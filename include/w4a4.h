@@ -370,14 +370,14 @@ enum { W4A4_Y_F32 = 0, W4A4_Y_BF16 = 1 };
 typedef struct w4a4_fp8_packed {
     int64_t n_mat, d_in, d_out;
     int64_t k_pad;           /* roundup(d_in, 128)                                          */
-    int64_t n_pad;           /* roundup(d_out, 32)                                          */
+    int64_t n_pad;           /* roundup(d_out, 16)                                          */
     int32_t scale_kind;      /* W4A4_FP8_SCALE_*: also the kind of the activations' scales  */
     int32_t reserved;
-    const uint8_t* codes;    /* device E4M3 [n_mat][n_pad/32][k_pad/64][2][64][16]: each run
-                                of 32 rows x 64 inputs is 2 KiB in the order the matrix
+    const uint8_t* codes;    /* device E4M3 [n_mat][n_pad/16][k_pad/128][2][64][16]: each run
+                                of 16 rows x 128 inputs is 2 KiB in the order the matrix
                                 instructions read it; the byte of row r, input p sits at
-                                  ((r/32)*(k_pad/64) + p/64)*2048 + ((p/16)%2)*1024
-                                  + (((p/32)%2)*32 + r%32)*16 + p%16;
+                                  ((r/16)*(k_pad/128) + p/128)*2048 + ((p/16)%2)*1024
+                                  + ((p/32)%4)*256 + (r%16)*16 + p%16;
                                 rows past d_out and inputs past d_in are zero              */
     const float* scales;     /* device [n_mat][ceil(d_out/128)][k_pad/128], as binary32 for
                                 both kinds                                                 */
@@ -405,7 +405,7 @@ int w4a4_fp8_pack_codes(const uint8_t* codes, const void* scales, int64_t n_mat,
 /* Offsets (bytes) inside a workspace for T tokens. */
 typedef struct w4a4_fp8_ws_layout {
     size_t a_q;       /* activation codes in the order of w4a4_fp8_packed.codes, tokens as
-                         rows: [ceil(T/32)][k_pad/64][2][64][16]; rows past T unwritten    */
+                         rows: [ceil(T/16)][k_pad/128][2][64][16]; rows past T unwritten   */
     size_t a_s;       /* fp32 [k_pad/128][roundup(T, 32)] activation scales; tokens past T
                          unwritten                                                         */
     size_t partial;   /* fp32 partial sums of K ranges (written and read back within a
@@ -465,15 +465,19 @@ typedef struct w4a4_moe {
 
 /* Offsets (bytes) inside a workspace for T tokens: what a call leaves there. */
 typedef struct w4a4_moe_ws_layout {
-    size_t logits;    /* fp32 [T][E]                                                        */
-    size_t xb;        /* bf16 [T][roundup(d, 128)], zero padded                             */
+    size_t logits;    /* fp32 [T][roundup(E, 4)]                                            */
+    size_t xb;        /* bf16 [T][roundup(d, 128)], zero padded (left alone where X itself is
+                         bf16 and d a multiple of 128)                                      */
     size_t ids;       /* int32 [T][top_k]: the chosen experts, largest logit first          */
     size_t p;         /* fp32 [T][top_k]: exp(l - max), divided by the sum over all experts
                          when renormalize == 0 (otherwise the down step divides by the sum
                          over the row)                                                      */
-    size_t count;     /* int32 [E]: tokens of each expert                                   */
-    size_t pairs;     /* int32 [E][T]: their entries t * top_k + rank of ids, ascending     */
-    size_t h;         /* bf16 [T * top_k][roundup(f, 128)], zero padded                     */
+    size_t pos;       /* int32 [T][top_k]: how many earlier tokens chose the same expert    */
+    size_t h;         /* bf16, by expert in tiles of 16 of its tokens x 128 columns, in the
+                         order in which the down products read them, zero padded: tile
+                         (s * ceil(T/16) + pos/16) * roundup(f, 128)/128 + column/128, where s is
+                         the expert, or, if T * top_k < E <= 256, its first entry of ids; in it
+                           ((c/8)%4)*512 + ((c/32)*16 + pos%16)*8 + c%8, c = column%128     */
     size_t total;
 } w4a4_moe_ws_layout;
 int w4a4_moe_workspace_layout(int64_t T, const w4a4_moe* moe, w4a4_moe_ws_layout* out);
