@@ -41,42 +41,45 @@ __device__ __forceinline__ uint4 encode16(const float* x, float s) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Values p .. p + 15 of a row of `cols`, zero past its end; `vec`: the row starts on a
-// 16-byte boundary (p is a multiple of 16).
-__device__ __forceinline__ void load16(const float* row, int64_t p, int64_t cols, bool vec, float* x) {
-    if (vec && p + 16 <= cols) {
+// Values p .. p + 7 of a row of `cols`, zero past its end; `vec`: the row starts on a
+// 16-byte boundary (p is a multiple of 8).
+__device__ __forceinline__ void load8(const float* row, int64_t p, int64_t cols, bool vec, float* x) {
+    if (vec && p + 8 <= cols) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const float4 v = *reinterpret_cast<const float4*>(row + p + 4 * i);
             x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = p + i < cols ? row[p + i] : 0.0f;
+    for (int i = 0; i < 8; ++i) x[i] = p + i < cols ? row[p + i] : 0.0f;
 }
-__device__ __forceinline__ void load16(const uint16_t* row, int64_t p, int64_t cols, bool vec, float* x) {
-    if (vec && p + 16 <= cols) {
+__device__ __forceinline__ void load8(const uint16_t* row, int64_t p, int64_t cols, bool vec, float* x) {
+    if (vec && p + 8 <= cols) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + p + 8 * i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-                x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-            }
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(w[j] << 16);
+            x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = p + i < cols ? bf16_to_f32(row[p + i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) x[i] = p + i < cols ? bf16_to_f32(row[p + i]) : 0.0f;
+}
+// The 16 values of one 16-byte piece of the packed order: inputs p .. + 7 and p + 32 .. + 39
+// (p = 64 half + 8 chunk of the block).
+template <typename X>
+__device__ __forceinline__ void load_piece(const X* row, int64_t p, int64_t cols, bool vec, float* x) {
+    load8(row, p, cols, vec, x);
+    load8(row, p + 32, cols, vec, x + 8);
 }
 
 // Activations.  A wavefront takes 8 tokens x one block of 128 inputs: lane l holds the 16
-// inputs 16 (l / 8) .. of token l % 8, whose codes are one 16-byte piece of the packed
-// order, and the pieces of 8 consecutive tokens are 128 contiguous bytes: every store
-// instruction writes whole cache lines.
+// inputs of the (l / 8)-th 16-byte piece of token l % 8, and the pieces of 8 consecutive
+// tokens are 128 contiguous bytes: every store instruction writes whole cache lines.
 template <typename X>
 __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__ x, int64_t T, int64_t d_in, int64_t nkb,
                                                            int64_t items, int kind, int vec, uint8_t* __restrict__ aq,
@@ -88,7 +91,7 @@ __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__
     const int64_t t = tg * 8 + tk;
     const bool live = t < T;
     float v[16];
-    load16(x + (live ? t : 0) * d_in, kb * 128 + i * 16, d_in, vec != 0, v);
+    load_piece(x + (live ? t : 0) * d_in, kb * 128 + (i >> 2) * 64 + (i & 3) * 8, d_in, vec != 0, v);
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[j]));
@@ -97,7 +100,7 @@ __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__
     const float s = block_scale(m, kind);
     const uint4 c = encode16(v, s);
     if (!live) return;
-    uint8_t* dst = aq + ((t / 16) * nkb + kb) * 2048 + (i & 1) * 1024 + (i >> 1) * 256 + (t & 15) * 16;
+    uint8_t* dst = aq + ((t / 16) * nkb + kb) * 2048 + i * 256 + (t & 15) * 16;
     *reinterpret_cast<uint4*>(dst) = c;
     if (i == 0) as[kb * t_ld + t] = s;
 }
@@ -117,7 +120,7 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (row < d_out) {
-            load16(w + (mat * d_out + row) * d_in, p0 + 16 * i, d_in, vec != 0, v[i]);
+            load_piece(w + (mat * d_out + row) * d_in, p0 + 8 * i, d_in, vec != 0, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
@@ -135,8 +138,7 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, 
     if (row >= n_pad) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t p = p0 + 16 * i;
-        uint8_t* dst = codes + ((mat * (n_pad / 16) + row / 16) * nkb + kb) * 2048 + ((p / 16) & 1) * 1024 + ((p / 32) & 3) * 256 +
+        uint8_t* dst = codes + ((mat * (n_pad / 16) + row / 16) * nkb + kb) * 2048 + (threadIdx.x & 1) * 1024 + i * 256 +
                        (row & 15) * 16;
         *reinterpret_cast<uint4*>(dst) = encode16(v[i], s);
     }
@@ -152,20 +154,23 @@ __global__ __launch_bounds__(256) void fp8_reorder_kernel(const uint8_t* __restr
     const int64_t run = q >> 7;                       // 16 rows x 128 inputs
     const int64_t rb = run / nkb, kb = run - rb * nkb;
     const int64_t mat = rb / (n_pad / 16), row = (rb - mat * (n_pad / 16)) * 16 + (l & 15);
-    const int64_t p = kb * 128 + (l >> 4) * 32 + h * 16;
-    uint4 v = make_uint4(0, 0, 0, 0);
+    uint2 v[2] = {make_uint2(0, 0), make_uint2(0, 0)};
     if (row < d_out) {
-        const uint8_t* s = src + (mat * d_out + row) * d_in + p;
-        if (vec && p + 16 <= d_in) {
-            v = *reinterpret_cast<const uint4*>(s);
-        } else {
-            uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i / 4] |= (p + i < d_in ? (uint32_t)s[i] : 0u) << (8 * (i & 3));
-            v = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int c = 0; c < 2; ++c) {
+            const int64_t p = kb * 128 + h * 64 + c * 32 + (l >> 4) * 8;
+            const uint8_t* s = src + (mat * d_out + row) * d_in + p;
+            if (vec && p + 8 <= d_in) {
+                v[c] = *reinterpret_cast<const uint2*>(s);
+            } else {
+                uint32_t w[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i / 4] |= (p + i < d_in ? (uint32_t)s[i] : 0u) << (8 * (i & 3));
+                v[c] = make_uint2(w[0], w[1]);
+            }
         }
     }
-    *reinterpret_cast<uint4*>(codes + q * 16) = v;
+    *reinterpret_cast<uint4*>(codes + q * 16) = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
 }
 
 __global__ __launch_bounds__(256) void fp8_scales_kernel(const void* __restrict__ src, int64_t n, int kind,
@@ -212,7 +217,7 @@ hipError_t launch_fp8_reorder(const uint8_t* src, const void* src_scales, const 
                               float* scales, hipStream_t st) {
     const int64_t nkb = d.k_pad / 128, pieces = d.n_mat * d.n_pad * d.k_pad / 16;
     hipLaunchKernelGGL(fp8_reorder_kernel, dim3((uint32_t)((pieces + 255) / 256)), dim3(256), 0, st, src, d.d_in, d.d_out, nkb,
-                       d.n_pad, pieces, d.d_in % 16 == 0 ? 1 : 0, codes);
+                       d.n_pad, pieces, d.d_in % 8 == 0 ? 1 : 0, codes);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n = d.n_mat * ((d.d_out + 127) / 128) * nkb;

@@ -109,14 +109,12 @@ int check_moe(int64_t T, const w4a4_moe* m) {
 w4a4_moe_ws_layout moe_layout(int64_t T, const w4a4_moe* m) {
     w4a4_moe_ws_layout w;
     const int64_t E = m->up.n_mat, pairs = T * m->top_k;
-    const int64_t h_tiles = (moe_by_slot(T, m->top_k, E) ? pairs : E) * ((T + 15) / 16);
     size_t off = 0;
     w.logits = off; off = align_up(off + (size_t)(T * round_up(E, 4)) * 4);
     w.xb = off;     off = align_up(off + (size_t)(T * m->up.k_pad) * 2);
     w.ids = off;    off = align_up(off + (size_t)pairs * 4);
     w.p = off;      off = align_up(off + (size_t)pairs * 4);
-    w.pos = off;    off = align_up(off + (size_t)pairs * 4);
-    w.h = off;      off = align_up(off + (size_t)(h_tiles * 16 * m->down.k_pad) * 2);
+    w.h = off;      off = align_up(off + (size_t)(pairs * m->down.k_pad) * 2);
     w.total = off;
     return w;
 }
@@ -244,7 +242,6 @@ int w4a4_moe_forward(const void* X, int x_dtype, int64_t T, const w4a4_moe* moe,
     m.xb = (uint16_t*)(b + w.xb);
     m.h = (uint16_t*)(b + w.h);
     m.ids = (int32_t*)(b + w.ids);
-    m.pos = (int32_t*)(b + w.pos);
     return dev_status(launch_moe(X, x_dtype, T, *moe, m, Y, y_dtype, (hipStream_t)stream));
 }
 

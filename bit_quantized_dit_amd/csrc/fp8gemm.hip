@@ -7,8 +7,10 @@
 // activation scale is one value per lane.
 //
 // Both operands lie in memory in runs of 16 rows x 128 inputs (2 KiB), in the order in which a
-// wavefront of a 16-row matrix instruction reads them: lane l takes row l % 16, inputs
-// 32 (l / 16) .. + 31, its two 16-byte halves at 16 l and 1024 + 16 l.  Runs of a row block
+// wavefront of a 16-row matrix instruction reads them: lane l takes row l % 16 and the 32 inputs
+// 32 q + 8 (l / 16) .. + 7, q < 4, its two 16-byte halves at 16 l and 1024 + 16 l.  (Which inputs
+// a lane takes is free as long as both operands agree; these let the unquantized operand of
+// moe.hip be read in 64-byte pieces of its rows.)  Runs of a row block
 // follow each other along the inputs, so that whoever streams 16 rows reads one contiguous
 // range; copies to LDS are linear; and a 32-row fragment takes 16 rows from each of two runs
 // in 256-byte pieces that no two of 16 neighbouring lanes' banks share.
@@ -241,8 +243,7 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
 // ---------------------------------------------------------------- few tokens
 //
 // Bound by reading the weight codes once.  A workgroup owns 16 weight rows; its eight
-// wavefronts take every eighth block of 128 inputs, read codes straight from memory (lane
-// l: row l % 16, inputs 32 (l / 16) .. + 31 of the block), widen them to bf16 and multiply
+// wavefronts take every eighth block of 128 inputs, read codes straight from memory, widen them to bf16 and multiply
 // them with up to NT tiles of 16 tokens by v_mfma_f32_16x16x32_bf16; the eight partial sums
 // meet in LDS and are added in wavefront order.
 template <int NT, int OUT>

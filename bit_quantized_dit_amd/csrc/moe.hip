@@ -8,9 +8,10 @@
 //
 // The layer is bound by reading the chosen experts' codes once.  Wavefronts read codes
 // straight from memory in the packed order (lane l of a run: row l % 16, inputs
-// 32 (l / 16) .. + 31), widen them to bf16 (exact) and feed
-// v_mfma_f32_16x16x32_bf16 with 16 tokens on the other side; a block's sum of 128 products
-// is scaled by the block's weight scale in fp32.
+// 32 q + 8 (l / 16) .. + 7 for q < 4), widen them to bf16 (exact) and feed
+// v_mfma_f32_16x16x32_bf16 with 16 tokens on the other side, whose operand of step q is 64
+// contiguous bytes of each token's row; a block's sum of 128 products is scaled by the block's
+// weight scale in fp32.
 //
 // No kernel waits for another workgroup and nothing is added by atomics: who chose what is
 // recomputed where it is needed by counting, for one expert, how many experts rank before
@@ -164,10 +165,10 @@ __device__ __forceinline__ float load_scale(Rsrc p, uint32_t lane_off, uint32_t 
     return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(p, (int)lane_off, (int)b * 4, 0));
 }
 // Added to the lane offset of a load that nothing needs: past every descriptor's range (which is
-// at most 2^26 bytes), it reads zeros and no memory.
+// below 2^30 bytes), it reads zeros and no memory.
 constexpr uint32_t NO_LOAD = 0x80000000u;
-// (16 rows x 128 inputs of codes) . (128 inputs x 16 tokens); x: this lane's 32 consecutive
-// bf16 values of its token.
+// (16 rows x 128 inputs of codes) . (128 inputs x 16 tokens); x: this lane's four pieces of its
+// token.
 __device__ __forceinline__ v4f block_mma(const Codes& c, const uint4* x) {
     const uint32_t w[8] = {c.lo.x, c.lo.y, c.lo.z, c.lo.w, c.hi.x, c.hi.y, c.hi.z, c.hi.w};
     v4f t = v4f{0, 0, 0, 0};
@@ -179,7 +180,7 @@ __device__ __forceinline__ v4f block_mma(const Codes& c, const uint4* x) {
 
 // acc[m][i] += the scaled blocks kb0, kb0 + step, ... (n of them) of NM row tiles (wp, sp: codes and
 // scales of the row tiles' nkb blocks, uniform) on NT token tiles, whose operand of block b starts
-// at x0 + b * 256 + xoff (the lane's 64 bytes).  A ring of D blocks per wavefront: a block's
+// at x0 + b * 256 + xoff, 64 bytes from piece to piece.  A ring of D blocks per wavefront: a block's
 // registers are refilled as soon as they are used, so D - 1 blocks are always in flight.  The code
 // is kept short: these kernels run
 // for a few microseconds from a cold instruction cache.
@@ -207,7 +208,7 @@ __device__ __forceinline__ void stream_blocks(v4f (&acc)[NM][NT], const uint8_t*
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[j][t][q] = load_at(x0, xoff[t] + off + q * 16, b * 256);
+            for (int q = 0; q < 4; ++q) x[j][t][q] = load_at(x0, xoff[t] + off + q * 64, b * 256);
     };
 #pragma unroll
     for (int j = 0; j < D; ++j) {
@@ -232,10 +233,6 @@ __device__ __forceinline__ void stream_blocks(v4f (&acc)[NM][NT], const uint8_t*
     }
 }
 
-// h is kept as the down products read it: tiles of 16 tokens of one expert x 128 columns (4 KiB),
-// 16-byte piece q of lane l at q * 1024 + l * 16: token l % 16, columns 32 (l / 16) + 8 q ..
-constexpr int H_TILE = 4096, H_PIECE = 1024;
-
 // Sum over the eight lanes of an aligned group.
 __device__ __forceinline__ int sum8(int c) {
 #pragma unroll
@@ -259,7 +256,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 struct UpArgs {
     const float* logits;
     const uint16_t* xb;
-    int32_t *ids, *pos;
+    int32_t* ids;
     float* p;
     uint16_t* h;
     int T, E, k, renorm, f, by_slot;
@@ -372,13 +369,12 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
     const int64_t sofs = (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * a.nkb_d;
     const Rsrc xr = rsrc(a.xb, (uint32_t)a.T * (uint32_t)a.nkb_d * 256u);
     const int nb = nkb > wk ? (nkb - wk + a.ks - 1) / a.ks : 0;
-    const int64_t slot = (int64_t)(a.by_slot ? (int)blockIdx.y : e) * ((a.T + 15) / 16);
     for (int c0 = 0; c0 < n; c0 += NT * 16) {
         uint32_t xoff[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int q = c0 + i * 16 + r;
-            xoff[i] = (uint32_t)(list[q < n ? q : c0] >> 8) * (uint32_t)a.nkb_d * 256u + g * 64;
+            xoff[i] = (uint32_t)(list[q < n ? q : c0] >> 8) * (uint32_t)a.nkb_d * 256u + g * 16;
         }
         v4f acc[NM][NT];
 #pragma unroll
@@ -413,10 +409,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
             }
             if constexpr (GATED) u = v / (1.0f + expf(-v)) * u;
             else u = gelu_tanh_f32(u);
-            const int64_t base = slot + c0 / 16 + at / 16;
-            uint8_t* const dst = reinterpret_cast<uint8_t*>(a.h) + (base * (a.f_pad / 128) + hr / 128) * H_TILE +
-                                 (hr % 32 / 8) * H_PIECE + ((hr % 128 / 32) * 16 + at % 16) * 16 + hr % 8 * 2;
-            *reinterpret_cast<uint16_t*>(dst) = hr < a.f ? bf16_rne(u) : 0;
+            a.h[(int64_t)entry_pair(list[c0 + at], a.k) * a.f_pad + hr] = hr < a.f ? bf16_rne(u) : 0;
         }
     }
 
@@ -437,7 +430,6 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
             }
             if ((tid & 7) == 0) {
                 a.ids[pair] = e;
-                a.pos[pair] = q;
                 a.p[pair] = v;
             }
         }
@@ -447,10 +439,10 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
 // ---------------------------------------------------------------- 3. down
 
 struct DownArgs {
-    const int32_t *ids, *pos;
+    const int32_t* ids;
     const float* p;
     const uint16_t* h;
-    int T, E, k, renorm, d, by_slot;
+    int T, E, k, renorm, d;
     int nkb_f;                               // f blocks of 128
     const uint8_t* codes;
     const float* scales;
@@ -471,22 +463,19 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
     __shared__ __attribute__((aligned(16))) float sums[W * TB * RL];
     __shared__ float den[TB], prob[PB];
     __shared__ uint16_t list[PB];              // pairs, expert by expert
-    __shared__ int32_t first[W4A4_MOE_MAX_E];  // by expert: pairs, then where its list starts
-    __shared__ uint16_t lead[W4A4_MOE_MAX_E];  // by expert: its first pair
+    __shared__ int32_t first[W4A4_MOE_MAX_E];  // by expert: pairs, then where its list goes on
     __shared__ uint16_t seg_e[SEGS], seg_l[SEGS];   // by segment: expert, place in list
-    __shared__ uint8_t seg_c[SEGS], seg_n[SEGS];    // its number within the expert, tokens
+    __shared__ uint8_t seg_n[SEGS];                 // its tokens
     __shared__ int n_seg;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row0 = blockIdx.x * RL, pairs = a.T * a.k, nkb = a.nkb_f, tt = (a.T + 15) / 16;
+    const int row0 = blockIdx.x * RL, pairs = a.T * a.k, nkb = a.nkb_f;
     for (int i = tid; i < W * TB * RL; i += W * 64) sums[i] = 0.0f;
     if (a.T == 1) {   // every pair is a segment
         for (int i = tid; i < pairs; i += W * 64) {
-            const int e = a.ids[i];
             prob[i] = a.p[i];
-            list[i] = seg_l[i] = lead[e] = (uint16_t)i;
-            seg_e[i] = (uint16_t)e;
-            seg_c[i] = 0;
+            list[i] = seg_l[i] = (uint16_t)i;
+            seg_e[i] = (uint16_t)a.ids[i];
             seg_n[i] = 1;
         }
         if (tid == 0) n_seg = pairs;
@@ -515,7 +504,6 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
                 for (int q = 0; q * 16 < c; ++q, ++s) {
                     seg_e[s] = (uint16_t)e;
                     seg_l[s] = (uint16_t)(l0 + q * 16);
-                    seg_c[s] = (uint8_t)q;
                     seg_n[s] = (uint8_t)(c - q * 16 < 16 ? c - q * 16 : 16);
                 }
                 const int all = __shfl(v, 63);
@@ -525,11 +513,9 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
             if (lane == 0) n_seg = seg;
         }
         __syncthreads();
-        for (int i = tid; i < pairs; i += W * 64) {   // in the order in which the up step laid h out
-            const int e = a.ids[i], q = a.pos[i];
-            list[first[e] + q] = (uint16_t)i;
-            if (q == 0) lead[e] = (uint16_t)i;
-        }
+        // in the order in which the lanes arrive: it decides the matrix column that a token takes,
+        // which changes no value
+        for (int i = tid; i < pairs; i += W * 64) list[atomicAdd(&first[a.ids[i]], 1)] = (uint16_t)i;
     }
     for (int t = tid; t < a.T; t += W * 64) {
         float s = 1.0f;
@@ -548,17 +534,15 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
     float* const mine = sums + wave * TB * RL;
     if (len > 0) {
         int seg = begin / groups, lkb = (begin - seg * groups) * D;   // the group that is loaded
-        Rsrc wr, xr, sr;
+        const Rsrc xr = rsrc(a.h, (uint32_t)pairs * (uint32_t)nkb * 256u);
+        Rsrc wr, sr;
         uint32_t xoff;
         auto open = [&](int sg) __attribute__((always_inline)) {
             const int e = __builtin_amdgcn_readfirstlane(seg_e[sg]), n = __builtin_amdgcn_readfirstlane(seg_n[sg]);
-            const int slot = a.by_slot ? __builtin_amdgcn_readfirstlane(lead[e]) : e;
-            const int64_t tile = (int64_t)slot * tt + __builtin_amdgcn_readfirstlane(seg_c[sg]);
             wr = rsrc(a.codes + (int64_t)e * a.mat_codes + (int64_t)blockIdx.x * RT * nkb * 2048, (uint32_t)tiles * nkb * 2048u);
-            xr = rsrc(reinterpret_cast<const uint8_t*>(a.h) + tile * nkb * H_TILE, (uint32_t)nkb * H_TILE);
             sr = rsrc(a.scales + (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * nkb, (uint32_t)nkb * 4u);
             // lanes past the segment's tokens read the first one's h
-            xoff = (uint32_t)(r < n ? lane : lane & 48) * 16;
+            xoff = (uint32_t)list[seg_l[sg] + (r < n ? r : 0)] * (uint32_t)nkb * 256u + g * 16;
         };
         Codes w[D][RT];
         uint4 x[D][4];
@@ -571,7 +555,7 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
                 w[j][t] = Codes{load_once(wr, woff, b * 2048u), load_once(wr, woff + 1024, b * 2048u)};
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[j][q] = load_at(xr, xoff + off + q * H_PIECE, b * H_TILE);
+            for (int q = 0; q < 4; ++q) x[j][q] = load_at(xr, xoff + off + q * 64, b * 256u);
             sc[j] = load_scale(sr, off, b);
         };
         open(seg);
@@ -687,9 +671,9 @@ hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, 
 
     const bool gated = m.activation == W4A4_MOE_SILU_GATED;
     UpArgs u;
-    u.logits = b.logits; u.xb = copy ? b.xb : (const uint16_t*)X; u.ids = b.ids; u.pos = b.pos; u.p = b.p; u.h = b.h;
+    u.logits = b.logits; u.xb = copy ? b.xb : (const uint16_t*)X; u.ids = b.ids; u.p = b.p; u.h = b.h;
     u.T = (int)T; u.E = (int)m.up.n_mat; u.k = m.top_k; u.renorm = m.renormalize != 0; u.f = (int)m.up.d_out;
-    u.by_slot = moe_by_slot(T, m.top_k, m.up.n_mat) ? 1 : 0;
+    u.by_slot = T * m.top_k < m.up.n_mat && m.up.n_mat <= SLOT_E ? 1 : 0;
     u.nkb_d = (int)(m.up.k_pad / 128); u.f_pad = (int)m.down.k_pad; u.n_pad = (int)m.up.n_pad;
     u.gate = gated ? m.gate.codes : nullptr; u.gate_s = gated ? m.gate.scales : nullptr;
     u.up = m.up.codes; u.up_s = m.up.scales;
@@ -708,8 +692,8 @@ hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, 
     if (e != hipSuccess) return e;
 
     DownArgs d;
-    d.ids = b.ids; d.pos = b.pos; d.p = b.p; d.h = b.h;
-    d.T = u.T; d.E = u.E; d.k = u.k; d.renorm = u.renorm; d.d = (int)m.down.d_out; d.by_slot = u.by_slot;
+    d.ids = b.ids; d.p = b.p; d.h = b.h;
+    d.T = u.T; d.E = u.E; d.k = u.k; d.renorm = u.renorm; d.d = (int)m.down.d_out;
     d.nkb_f = (int)(m.down.k_pad / 128);
     d.codes = m.down.codes; d.scales = m.down.scales;
     d.mat_codes = m.down.n_pad * m.down.k_pad; d.mat_scales = (m.down.d_out + 127) / 128 * (m.down.k_pad / 128);

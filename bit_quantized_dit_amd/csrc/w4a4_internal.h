@@ -86,11 +86,8 @@ hipError_t launch_fp8_gemm(const uint8_t* aq, const float* as, int64_t T, int64_
 struct MoeBuffers {
     float *logits, *p;
     uint16_t *xb, *h;
-    int32_t *ids, *pos;
+    int32_t* ids;
 };
-// Whether the up step's workgroups are dealt by (token, rank) rather than by expert, which also
-// decides where h lies: fewer pairs than experts, and no more experts than a wavefront searches.
-inline bool moe_by_slot(int64_t T, int64_t k, int64_t E) { return T * k < E && E <= 256; }
 hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, const MoeBuffers& b, void* Y, int y_dtype,
                       hipStream_t st);
 

@@ -94,7 +94,7 @@ class W4A4Moe(ctypes.Structure):
 
 class W4A4MoeWsLayout(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_size_t), ("xb", ctypes.c_size_t), ("ids", ctypes.c_size_t), ("p", ctypes.c_size_t),
-                ("pos", ctypes.c_size_t), ("h", ctypes.c_size_t), ("total", ctypes.c_size_t)]
+                ("h", ctypes.c_size_t), ("total", ctypes.c_size_t)]
 
 
 class W4A4Error(RuntimeError):
@@ -649,9 +649,10 @@ class PackedFp8:
 
 def untile_fp8(raw: torch.Tensor, rows: int, k_pad: int) -> torch.Tensor:
     """[rows, k_pad] row-major copy of E4M3 codes stored in the packed order (runs of 16
-    rows x 128 inputs: two halves of 16 inputs, four 32-input chunks, 16 rows, 16 bytes)."""
-    t = raw.view(rows // 16, k_pad // 128, 2, 4, 16, 16)     # run row, run input, half, chunk, row, byte
-    return t.permute(0, 4, 1, 3, 2, 5).reshape(rows, k_pad)
+    rows x 128 inputs: two halves of 64 inputs, four chunks, 16 rows, two 32-input parts of
+    the half, 8 bytes)."""
+    t = raw.view(rows // 16, k_pad // 128, 2, 4, 16, 2, 8)   # run row, run input, half, chunk, row, part, byte
+    return t.permute(0, 4, 1, 2, 5, 3, 6).reshape(rows, k_pad)
 
 
 def w4a4_fp8_packed_size(n_mat: int, d_in: int, d_out: int) -> int:
@@ -814,24 +815,15 @@ def alloc_workspace_moe(T: int, layer: MoeLayer, device="cuda") -> torch.Tensor:
 
 
 def workspace_moe_views(ws: torch.Tensor, T: int, layer: MoeLayer) -> dict:
-    """What a call left in ws: logits [T, E], ids and p [T, top_k] (views), h [T, top_k, f]
-    (a row-major copy)."""
+    """Device views of what a call left in ws: logits [T, E], ids and p [T, top_k], h
+    [T, top_k, f]."""
     L = w4a4_moe_workspace_layout(T, layer)
-    k, E, nkb, tt = layer.top_k, layer.n_experts, layer.desc.down.k_pad // 128, (T + 15) // 16
-    ids, pos = (ws[o:o + 4 * T * k].view(torch.int32).long() for o in (L.ids, L.pos))
-    slot = ids
-    by_slot = T * k < E <= 256
-    if by_slot:
-        start = torch.nonzero(pos == 0).flatten()
-        slot = torch.zeros(E, dtype=torch.long, device=ws.device).index_put_((ids[start],), start)[ids]
-    tiles = ws[L.h:L.h + (T * k if by_slot else E) * tt * 16 * nkb * 256].view(torch.bfloat16).view(-1, nkb, 4, 4, 16, 8)
-    h = tiles[slot * tt + pos // 16, :, :, :, pos % 16]          # pair, block, piece, chunk, column
-    h = h.permute(0, 1, 3, 2, 4).reshape(T, k, nkb * 128)[:, :, :layer.f]
+    k, E, fp = layer.top_k, layer.n_experts, layer.desc.down.k_pad
     e4 = (E + 3) // 4 * 4
     return {"logits": ws[L.logits:L.logits + 4 * T * e4].view(torch.float32).view(T, e4)[:, :E],
             "ids": ws[L.ids:L.ids + 4 * T * k].view(torch.int32).view(T, k),
             "p": ws[L.p:L.p + 4 * T * k].view(torch.float32).view(T, k),
-            "h": h}
+            "h": ws[L.h:L.h + 2 * T * k * fp].view(torch.bfloat16).view(T, k, fp)[:, :, :layer.f]}
 
 
 def w4a4_moe_forward(X: torch.Tensor, layer: MoeLayer, Y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:

@@ -376,8 +376,8 @@ typedef struct w4a4_fp8_packed {
     const uint8_t* codes;    /* device E4M3 [n_mat][n_pad/16][k_pad/128][2][64][16]: each run
                                 of 16 rows x 128 inputs is 2 KiB in the order the matrix
                                 instructions read it; the byte of row r, input p sits at
-                                  ((r/16)*(k_pad/128) + p/128)*2048 + ((p/16)%2)*1024
-                                  + ((p/32)%4)*256 + (r%16)*16 + p%16;
+                                  ((r/16)*(k_pad/128) + p/128)*2048 + ((p/64)%2)*1024
+                                  + ((p/8)%4)*256 + (r%16)*16 + ((p/32)%2)*8 + p%8;
                                 rows past d_out and inputs past d_in are zero              */
     const float* scales;     /* device [n_mat][ceil(d_out/128)][k_pad/128], as binary32 for
                                 both kinds                                                 */
@@ -472,12 +472,7 @@ typedef struct w4a4_moe_ws_layout {
     size_t p;         /* fp32 [T][top_k]: exp(l - max), divided by the sum over all experts
                          when renormalize == 0 (otherwise the down step divides by the sum
                          over the row)                                                      */
-    size_t pos;       /* int32 [T][top_k]: how many earlier tokens chose the same expert    */
-    size_t h;         /* bf16, by expert in tiles of 16 of its tokens x 128 columns, in the
-                         order in which the down products read them, zero padded: tile
-                         (s * ceil(T/16) + pos/16) * roundup(f, 128)/128 + column/128, where s is
-                         the expert, or, if T * top_k < E <= 256, its first entry of ids; in it
-                           ((c/8)%4)*512 + ((c/32)*16 + pos%16)*8 + c%8, c = column%128     */
+    size_t h;         /* bf16 [T * top_k][roundup(f, 128)], zero padded                     */
     size_t total;
 } w4a4_moe_ws_layout;
 int w4a4_moe_workspace_layout(int64_t T, const w4a4_moe* moe, w4a4_moe_ws_layout* out);

@@ -158,7 +158,7 @@ def test_choice_of_experts():
 def test_untile_inverts_the_packed_order():
     rows, k = 64, 256
     r, p = np.meshgrid(np.arange(rows), np.arange(k), indexing="ij")
-    off = ((r // 16) * (k // 128) + p // 128) * 2048 + ((p // 16) % 2) * 1024 + ((p // 32) % 4) * 256 + (r % 16) * 16 + p % 16
+    off = ((r // 16) * (k // 128) + p // 128) * 2048 + ((p // 64) % 2) * 1024 + ((p // 8) % 4) * 256 + (r % 16) * 16 + ((p // 32) % 2) * 8 + p % 8
     assert np.array_equal(np.sort(off.ravel()), np.arange(rows * k))
     val = ((r * 7 + p * 13) % 251).astype(np.uint8)
     raw = np.zeros(rows * k, np.uint8)
