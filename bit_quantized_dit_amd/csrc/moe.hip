@@ -159,11 +159,6 @@ __device__ __forceinline__ uint4 load_at(Rsrc p, uint32_t lane_off, uint32_t off
 __device__ __forceinline__ uint4 load_once(Rsrc p, uint32_t lane_off, uint32_t off) {
     return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(p, (int)lane_off, (int)off, 2));
 }
-// Scale of block b, the same address in every lane: a vector load, so that its wait is the codes'
-// (scalar loads return out of order and would each be waited for by themselves).
-__device__ __forceinline__ float load_scale(Rsrc p, uint32_t lane_off, uint32_t b) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(p, (int)lane_off, (int)b * 4, 0));
-}
 // Added to the lane offset of a load that nothing needs: past every descriptor's range (which is
 // below 2^30 bytes), it reads zeros and no memory.
 constexpr uint32_t NO_LOAD = 0x80000000u;
@@ -178,17 +173,46 @@ __device__ __forceinline__ v4f block_mma(const Codes& c, const uint4* x) {
     return t;
 }
 
+// The vector memory path moves about 30 bytes a cycle into a CU's registers, whatever the addresses:
+// with 2 KiB of codes a block it is the bound where the other operand is read for 16 tokens (4 KiB)
+// and only a few are there.  So a wavefront reads the rows of 4 XI tokens, one KiB for each four
+// (lane: row lane / 16, 16-byte chunk lane % 16), and passes them through LDS of its own to the
+// lanes that the matrix instruction wants them in.  XI == 4: 16 tokens, read in place.
+constexpr int tokens_of(int xi) { return xi == 4 ? 16 : 4 * xi; }
+// Where row `row`'s chunk c lies (16-byte units): four rows' chunks of one column in four bank groups.
+__device__ __forceinline__ int xs_at(int row, int c) { return row * 16 + (c ^ ((row & 3) * 4)); }
+template <int XI>
+__device__ __forceinline__ void spread(uint4 (&x)[4], const uint4 (&v)[XI], uint4* xs) {
+    if constexpr (XI == 4) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = v[q];
+    } else {
+        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+        const int row = r < 4 * XI ? r : 0;
+#pragma unroll
+        for (int i = 0; i < XI; ++i) xs[xs_at(i * 4 + g, r)] = v[i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = xs[xs_at(row, q * 4 + g)];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // acc[m][i] += the scaled blocks kb0, kb0 + step, ... (n of them) of NM row tiles (wp, sp: codes and
-// scales of the row tiles' nkb blocks, uniform) on NT token tiles, whose operand of block b starts
-// at x0 + b * 256 + xoff, 64 bytes from piece to piece.  A ring of D blocks per wavefront: a block's
-// registers are refilled as soon as they are used, so D - 1 blocks are always in flight.  The code
-// is kept short: these kernels run
-// for a few microseconds from a cold instruction cache.
-template <int D, int NM, int NT>
+// scales of the row tiles' nkb blocks, uniform) on NT token tiles, whose operand of block b is read
+// at x0 + b * 256 + xoff (XI == 4: in pieces 64 bytes apart).  A ring of D blocks per wavefront: a
+// block's registers are refilled as soon as they are used, so D - 1 blocks are always in flight.
+// A lane holds one block's scale of a group of D.  The code is kept short: these kernels run for a
+// few microseconds from a cold instruction cache.
+template <int D, int NM, int NT, int XI>
 __device__ __forceinline__ void stream_blocks(v4f (&acc)[NM][NT], const uint8_t* const (&wp)[NM], const float* const (&sp)[NM],
-                                              Rsrc x0, const uint32_t (&xoff)[NT], int nkb, int kb0, int n, int step) {
+                                              Rsrc x0, const uint32_t (&xoff)[NT * (XI == 4 ? 1 : XI)], uint4* xs, int nkb,
+                                              int kb0, int n, int step) {
+    static_assert(NT == 1 || XI == 4, "several token tiles are read in place");
     if (n <= 0) return;
-    const uint32_t woff = (threadIdx.x & 63) * 16;
+    const int lane = threadIdx.x & 63;
     Rsrc wr[NM], sr[NM];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
@@ -196,20 +220,25 @@ __device__ __forceinline__ void stream_blocks(v4f (&acc)[NM][NT], const uint8_t*
         sr[m] = rsrc(sp[m], (uint32_t)nkb * 4u);
     }
     Codes w[D][NM];
-    float s[D][NM];
-    uint4 x[D][NT][4];
+    float s[NM], next[NM];
+    uint4 x[D][NT][XI];
     auto load = [&](int j, int i) __attribute__((always_inline)) {
         const uint32_t b = (uint32_t)(kb0 + (i < n ? i : 0) * step), off = i < n ? 0 : NO_LOAD;
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            w[j][m] = Codes{load_once(wr[m], woff + off, b * 2048), load_once(wr[m], woff + off + 1024, b * 2048)};
-            s[j][m] = load_scale(sr[m], off, b);
-        }
+        for (int m = 0; m < NM; ++m)
+            w[j][m] = Codes{load_once(wr[m], lane * 16 + off, b * 2048), load_once(wr[m], lane * 16 + off + 1024, b * 2048)};
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[j][t][q] = load_at(x0, xoff[t] + off + q * 64, b * 256);
+            for (int q = 0; q < XI; ++q)
+                x[j][t][q] = load_at(x0, XI == 4 ? xoff[t] + off + q * 64 : xoff[q] + off, b * 256);
     };
+    auto load_scales = [&](int i) __attribute__((always_inline)) {   // of blocks i .. i + D - 1, one a lane
+        const uint32_t at = i + lane < n && lane < D ? (uint32_t)(kb0 + (i + lane) * step) * 4u : NO_LOAD;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) next[m] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr[m], (int)at, 0, 0));
+    };
+    load_scales(0);
 #pragma unroll
     for (int j = 0; j < D; ++j) {
         load(j, j);
@@ -217,16 +246,23 @@ __device__ __forceinline__ void stream_blocks(v4f (&acc)[NM][NT], const uint8_t*
     }
     for (int i = 0; i < n; i += D) {
 #pragma unroll
+        for (int m = 0; m < NM; ++m) s[m] = next[m];
+        load_scales(i + D);
+#pragma unroll
         for (int j = 0; j < D; ++j) {
             const bool in = i + j < n;   // uniform; past the end the sums stay as they are
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
+            for (int t = 0; t < NT; ++t) {
+                uint4 op[4];
+                spread<XI>(op, x[j][t], xs);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const v4f v = block_mma(w[j][m], x[j][t]);
+                for (int m = 0; m < NM; ++m) {
+                    const float sm = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s[m]), j));
+                    const v4f v = block_mma(w[j][m], op);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[m][t][r] = in ? __builtin_fmaf(v[r], s[j][m], acc[m][t][r]) : acc[m][t][r];
+                    for (int r = 0; r < 4; ++r) acc[m][t][r] = in ? __builtin_fmaf(v[r], sm, acc[m][t][r]) : acc[m][t][r];
                 }
+            }
             load(j, i + j + D);
             __builtin_amdgcn_sched_barrier(0);   // each block waits for its own loads only
         }
@@ -273,17 +309,19 @@ struct UpArgs {
 __device__ __forceinline__ int entry(int t, int rank) { return t << 8 | rank; }
 __device__ __forceinline__ int entry_pair(int v, int k) { return (v >> 8) * k + (v & 255); }
 
-// NT: token tiles that a pass over the codes takes.  The workgroup computes rs row tiles, each summed
-// over ks wavefronts.
-template <bool GATED, int NT>
+// A pass over the codes takes NT tiles of 16 tokens, or, NT == 1, 4 XI tokens.  The workgroup computes
+// rs row tiles, each summed over ks wavefronts.
+template <bool GATED, int NT, int XI>
 __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe_up_kernel(UpArgs a) {
     constexpr int NM = GATED ? 2 : 1, LD = 20;
-    constexpr int D = NT == 1 ? (GATED ? 2 : 4) : NT == 2 ? 2 : 1;
+    constexpr int D = NT == 4 ? 1 : NT == 2 ? 2 : GATED ? (XI == 4 ? 2 : 3) : (XI == 1 ? 6 : XI == 2 ? 5 : 4);
+    constexpr int TP = NT == 1 ? tokens_of(XI) : NT * 16, NX = XI == 4 ? NT : XI;
     __shared__ int32_t list[MAX_T];
     __shared__ int32_t rank[MAX_T];
     __shared__ uint32_t top[MAX_T];          // key of the token's largest logit
     __shared__ int32_t count;                // tokens of the expert
     __shared__ __attribute__((aligned(16))) float red[NM * WAVES * NT * 16 * LD];
+    __shared__ uint4 xs[XI == 4 ? 1 : WAVES * XI * 64];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ld = logits_ld(a.E);
@@ -369,12 +407,12 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
     const int64_t sofs = (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * a.nkb_d;
     const Rsrc xr = rsrc(a.xb, (uint32_t)a.T * (uint32_t)a.nkb_d * 256u);
     const int nb = nkb > wk ? (nkb - wk + a.ks - 1) / a.ks : 0;
-    for (int c0 = 0; c0 < n; c0 += NT * 16) {
-        uint32_t xoff[NT];
+    for (int c0 = 0; c0 < n; c0 += TP) {
+        uint32_t xoff[NX];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int q = c0 + i * 16 + r;
-            xoff[i] = (uint32_t)(list[q < n ? q : c0] >> 8) * (uint32_t)a.nkb_d * 256u + g * 16;
+        for (int i = 0; i < NX; ++i) {
+            const int q = c0 + (XI == 4 ? i * 16 + r : i * 4 + g);
+            xoff[i] = (uint32_t)(list[q < n ? q : c0] >> 8) * (uint32_t)a.nkb_d * 256u + (XI == 4 ? g : r) * 16;
         }
         v4f acc[NM][NT];
 #pragma unroll
@@ -384,11 +422,11 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
         if constexpr (GATED) {
             const uint8_t* const wp[2] = {a.up + cofs, a.gate + cofs};
             const float* const sp[2] = {a.up_s + sofs, a.gate_s + sofs};
-            stream_blocks<D, 2, NT>(acc, wp, sp, xr, xoff, a.nkb_d, wk, nb, a.ks);
+            stream_blocks<D, 2, NT, XI>(acc, wp, sp, xr, xoff, xs + wave * XI * 64, a.nkb_d, wk, nb, a.ks);
         } else {
             const uint8_t* const wp[1] = {a.up + cofs};
             const float* const sp[1] = {a.up_s + sofs};
-            stream_blocks<D, 1, NT>(acc, wp, sp, xr, xoff, a.nkb_d, wk, nb, a.ks);
+            stream_blocks<D, 1, NT, XI>(acc, wp, sp, xr, xoff, xs + wave * XI * 64, a.nkb_d, wk, nb, a.ks);
         }
         if (c0) __syncthreads();
         // lane: token r of tile i, rows 4 g .. 4 g + 3
@@ -401,7 +439,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
         for (int q = tid; q < a.rs * NT * 256; q += WAVES * 64) {
             const int tile = q / (NT * 256), at = q / 16 % (NT * 16), row = q & 15;
             const int hr = (blockIdx.x * a.rs + tile) * 16 + row;
-            if (c0 + at >= n || hr >= a.f_pad) continue;
+            if (at >= TP || c0 + at >= n || hr >= a.f_pad) continue;
             float u = 0.0f, v = 0.0f;
             for (int w = tile * a.ks; w < (tile + 1) * a.ks; ++w) {
                 u += red[(w * NT * 16 + at) * LD + row];
@@ -442,7 +480,7 @@ struct DownArgs {
     const int32_t* ids;
     const float* p;
     const uint16_t* h;
-    int T, E, k, renorm, d;
+    int T, E, k, renorm, d, y_dtype;
     int nkb_f;                               // f blocks of 128
     const uint8_t* codes;
     const float* scales;
@@ -450,17 +488,18 @@ struct DownArgs {
     void* out;
 };
 
-// TB: tokens the sums are laid out for; RT: row tiles (16 outputs) per workgroup.  The work is one
-// sequence of groups of D blocks: segment by segment (up to 16 tokens of one expert), the segment's
-// nkb_f blocks, the last group of a segment cut short.  The W wavefronts take equal consecutive
-// ranges of it; a wavefront's ring of D blocks in flight runs on from segment to segment, and
-// where a segment ends its sums, times the tokens' probabilities, go to the wavefront's own sums in
-// LDS, which are added in wavefront order at the end.
-template <int TB, int W, int RT, int OUT>
-__global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_down_kernel(DownArgs a) {
-    constexpr int PB = TB * W4A4_MOE_MAX_K, SEGS = W4A4_MOE_MAX_E + PB / 16, RL = 16 * RT;
-    constexpr int D = 3;
+// TB: tokens the sums are laid out for; RT: row tiles (16 outputs) of a workgroup.  The work is one sequence of groups of D blocks: segment by
+// segment (up to S tokens of one expert), the segment's nkb_f blocks, the last group of a segment cut
+// short.  The W wavefronts take equal consecutive ranges of it; a wavefront's ring of D blocks in
+// flight runs on from segment to segment, and where a segment ends its sums, times the tokens'
+// probabilities, go to the wavefront's own sums in LDS, which are added in wavefront order at the end.
+template <int TB, int W, int XI, int RT>
+__global__ __launch_bounds__(W * 64, TB < MAX_T ? 4 : 2) void moe_down_kernel(DownArgs a) {
+    constexpr int S = tokens_of(XI), NX = XI == 4 ? 1 : XI, RL = 16 * RT;
+    constexpr int PB = TB * W4A4_MOE_MAX_K, SEGS = W4A4_MOE_MAX_E + PB / S;
+    constexpr int D = XI == 1 ? 6 : XI == 2 ? 4 : 3;
     __shared__ __attribute__((aligned(16))) float sums[W * TB * RL];
+    __shared__ uint4 xs[XI == 4 ? 1 : W * XI * 64];
     __shared__ float den[TB], prob[PB];
     __shared__ uint16_t list[PB];              // pairs, expert by expert
     __shared__ int32_t first[W4A4_MOE_MAX_E];  // by expert: pairs, then where its list goes on
@@ -492,19 +531,19 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
             int at = 0, seg = 0;
             for (int e0 = 0; e0 < a.E; e0 += 64) {
                 const int e = e0 + lane, c = e < a.E ? first[e] : 0;
-                int v = c | ((c + 15) / 16) << 16;       // pairs and segments, summed over the lanes before
+                int v = c | ((c + S - 1) / S) << 16;       // pairs and segments, summed over the lanes before
 #pragma unroll
                 for (int o = 1; o < 64; o *= 2) {
                     const int u = __shfl_up(v, o);
                     v += lane >= o ? u : 0;
                 }
                 const int l0 = at + (v & 0xFFFF) - c;
-                int s = seg + (v >> 16) - (c + 15) / 16;
+                int s = seg + (v >> 16) - (c + S - 1) / S;
                 if (e < a.E) first[e] = l0;
-                for (int q = 0; q * 16 < c; ++q, ++s) {
+                for (int q = 0; q * S < c; ++q, ++s) {
                     seg_e[s] = (uint16_t)e;
-                    seg_l[s] = (uint16_t)(l0 + q * 16);
-                    seg_n[s] = (uint8_t)(c - q * 16 < 16 ? c - q * 16 : 16);
+                    seg_l[s] = (uint16_t)(l0 + q * S);
+                    seg_n[s] = (uint8_t)(c - q * S < S ? c - q * S : S);
                 }
                 const int all = __shfl(v, 63);
                 at += all & 0xFFFF;
@@ -536,29 +575,37 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
         int seg = begin / groups, lkb = (begin - seg * groups) * D;   // the group that is loaded
         const Rsrc xr = rsrc(a.h, (uint32_t)pairs * (uint32_t)nkb * 256u);
         Rsrc wr, sr;
-        uint32_t xoff;
+        uint32_t xoff[NX];
         auto open = [&](int sg) __attribute__((always_inline)) {
             const int e = __builtin_amdgcn_readfirstlane(seg_e[sg]), n = __builtin_amdgcn_readfirstlane(seg_n[sg]);
             wr = rsrc(a.codes + (int64_t)e * a.mat_codes + (int64_t)blockIdx.x * RT * nkb * 2048, (uint32_t)tiles * nkb * 2048u);
             sr = rsrc(a.scales + (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * nkb, (uint32_t)nkb * 4u);
-            // lanes past the segment's tokens read the first one's h
-            xoff = (uint32_t)list[seg_l[sg] + (r < n ? r : 0)] * (uint32_t)nkb * 256u + g * 16;
+            // rows past the segment's tokens read the first one's h
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int q = XI == 4 ? r : i * 4 + g;
+                xoff[i] = (uint32_t)list[seg_l[sg] + (q < n ? q : 0)] * (uint32_t)nkb * 256u + (XI == 4 ? g : r) * 16;
+            }
         };
         Codes w[D][RT];
-        uint4 x[D][4];
-        float sc[D];
+        uint4 x[D][XI];
+        float sc, next;
         auto load = [&](int j) __attribute__((always_inline)) {
             const uint32_t b = (uint32_t)(lkb + j), off = lkb + j < nkb ? 0 : NO_LOAD;
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const uint32_t woff = off + lane * 16 + t * (uint32_t)nkb * 2048u;
-                w[j][t] = Codes{load_once(wr, woff, b * 2048u), load_once(wr, woff + 1024, b * 2048u)};
+                const uint32_t at = off + lane * 16 + t * (uint32_t)nkb * 2048u;
+                w[j][t] = Codes{load_once(wr, at, b * 2048u), load_once(wr, at + 1024, b * 2048u)};
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[j][q] = load_at(xr, xoff + off + q * 64, b * 256u);
-            sc[j] = load_scale(sr, off, b);
+            for (int q = 0; q < XI; ++q) x[j][q] = load_at(xr, XI == 4 ? xoff[0] + off + q * 64 : xoff[q] + off, b * 256u);
+        };
+        auto load_scales = [&]() __attribute__((always_inline)) {   // of the group, one a lane
+            const uint32_t at = lane < D && lkb + lane < nkb ? (uint32_t)(lkb + lane) * 4u : NO_LOAD;
+            next = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr, (int)at, 0, 0));
         };
         open(seg);
+        load_scales();
 #pragma unroll
         for (int j = 0; j < D; ++j) {
             load(j);
@@ -577,14 +624,19 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
                 lkb = 0;
                 open(++seg);
             }
+            sc = next;
+            load_scales();
 #pragma unroll
             for (int j = 0; j < D; ++j) {
                 const bool in = kb + j < nkb;      // uniform; past the end the sums stay as they are
+                uint4 op[4];
+                spread<XI>(op, x[j], xs + wave * XI * 64);
+                const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sc), j));
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const v4f v = block_mma(w[j][t], x[j]);
+                    const v4f v = block_mma(w[j][t], op);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[t][q] = in ? __builtin_fmaf(v[q], sc[j], acc[t][q]) : acc[t][q];
+                    for (int q = 0; q < 4; ++q) acc[t][q] = in ? __builtin_fmaf(v[q], s, acc[t][q]) : acc[t][q];
                 }
                 load(j);
                 __builtin_amdgcn_sched_barrier(0);   // each block waits for its own loads only
@@ -614,7 +666,7 @@ __global__ __launch_bounds__(W * 64, W == 16 || TB < MAX_T ? 4 : 2) void moe_dow
         float y = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) y += sums[w * TB * RL + i];
-        if constexpr (OUT == W4A4_Y_F32) reinterpret_cast<float*>(a.out)[(int64_t)t * a.d + row] = y;
+        if (a.y_dtype == W4A4_Y_F32) reinterpret_cast<float*>(a.out)[(int64_t)t * a.d + row] = y;
         else reinterpret_cast<uint16_t*>(a.out)[(int64_t)t * a.d + row] = bf16_rne(y);
     }
 }
@@ -632,25 +684,46 @@ void run_logits(const void* X_, const w4a4_moe& m, int T, bool copy, float* logi
                            d_pad, E, vec, logits, xb);
 }
 
-template <bool GATED>
-void run_up(const UpArgs& a, int nt, dim3 grid, hipStream_t st) {
-    const dim3 block(WAVES * 64);
-    if (nt == 1) hipLaunchKernelGGL((moe_up_kernel<GATED, 1>), grid, block, 0, st, a);
-    else if (nt == 2) hipLaunchKernelGGL((moe_up_kernel<GATED, 2>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((moe_up_kernel<GATED, 4>), grid, block, 0, st, a);
+// Tokens of an expert that a pass over its codes takes (xi and, above 16, nt tiles), from the number
+// that it has on average: a second pass reads the codes again, a wider one reads more of the other
+// operand than there is.
+struct Pass {
+    int xi, nt;
+};
+Pass pass_of(int64_t T, int64_t k, int64_t E) {
+    const int64_t pairs = T * k;
+    if (T <= 4 || pairs <= E) return {1, 1};
+    if (T <= 8 || pairs <= 4 * E) return {2, 1};
+    if (T <= 16 || pairs <= 10 * E) return {4, 1};
+    return {4, pairs <= 24 * E ? 2 : 4};
 }
 
-template <int OUT>
+template <bool GATED>
+void run_up(const UpArgs& a, Pass p, dim3 grid, hipStream_t st) {
+    const dim3 block(WAVES * 64);
+    if (p.xi == 1) hipLaunchKernelGGL((moe_up_kernel<GATED, 1, 1>), grid, block, 0, st, a);
+    else if (p.xi == 2) hipLaunchKernelGGL((moe_up_kernel<GATED, 1, 2>), grid, block, 0, st, a);
+    else if (p.nt == 1) hipLaunchKernelGGL((moe_up_kernel<GATED, 1, 4>), grid, block, 0, st, a);
+    else if (p.nt == 2) hipLaunchKernelGGL((moe_up_kernel<GATED, 2, 4>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((moe_up_kernel<GATED, 4, 4>), grid, block, 0, st, a);
+}
+
+template <int XI>
 void run_down(const DownArgs& a, hipStream_t st) {
     // 16 wavefronts fit a CU at this kernel's registers: one workgroup of 16, or two of 8 where one
-    // a CU would leave a second round.  Two row tiles halve the reads of h, which for many
-    // tokens come near the codes'.
+    // a CU would leave a second round
     const uint32_t n = (uint32_t)((a.d + 15) / 16);
-    if (a.T <= 16 && n <= 256) hipLaunchKernelGGL((moe_down_kernel<16, 16, 1, OUT>), dim3(n), dim3(1024), 0, st, a);
-    else if (a.T <= 16) hipLaunchKernelGGL((moe_down_kernel<16, 8, 1, OUT>), dim3(n), dim3(512), 0, st, a);
-    else if (a.T <= 64 && n <= 256) hipLaunchKernelGGL((moe_down_kernel<64, 16, 1, OUT>), dim3(n), dim3(1024), 0, st, a);
-    else if (a.T <= 64) hipLaunchKernelGGL((moe_down_kernel<64, 16, 2, OUT>), dim3((n + 1) / 2), dim3(1024), 0, st, a);
-    else hipLaunchKernelGGL((moe_down_kernel<MAX_T, 8, 1, OUT>), dim3(n), dim3(512), 0, st, a);
+    const bool wide = n <= 256;
+    if (a.T <= 16 && wide) hipLaunchKernelGGL((moe_down_kernel<16, 16, XI, 1>), dim3(n), dim3(1024), 0, st, a);
+    else if (a.T <= 16) hipLaunchKernelGGL((moe_down_kernel<16, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
+    else if (a.T <= 64 && wide) hipLaunchKernelGGL((moe_down_kernel<64, 16, XI, 1>), dim3(n), dim3(1024), 0, st, a);
+    else if constexpr (XI == 4) {
+        // two row tiles for one read of h, where its 16 tokens' rows are twice the codes of one (64
+        // tokens, 6 of 64 experts, 1536 -> 5120: 145 to 120 us)
+        if (a.T <= 64) hipLaunchKernelGGL((moe_down_kernel<64, 16, XI, 2>), dim3((n + 1) / 2), dim3(1024), 0, st, a);
+        else hipLaunchKernelGGL((moe_down_kernel<MAX_T, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
+    } else if (a.T <= 64) hipLaunchKernelGGL((moe_down_kernel<64, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((moe_down_kernel<MAX_T, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
 }
 
 }  // namespace
@@ -684,10 +757,9 @@ hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, 
     u.ks = ny * tiles <= 1024 ? 4 : ny * tiles <= 2048 ? 2 : 1;
     u.rs = WAVES / u.ks;
     const dim3 grid((uint32_t)((tiles + u.rs - 1) / u.rs), (uint32_t)ny);
-    // tokens that an expert takes on average: one pass over its codes should do for most
-    const int nt = T <= 16 || T * m.top_k <= 10 * m.up.n_mat ? 1 : T * m.top_k <= 24 * m.up.n_mat ? 2 : 4;
-    if (gated) run_up<true>(u, nt, grid, st);
-    else run_up<false>(u, nt, grid, st);
+    const Pass pass = pass_of(T, m.top_k, m.up.n_mat);
+    if (gated) run_up<true>(u, pass, grid, st);
+    else run_up<false>(u, pass, grid, st);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
 
@@ -698,8 +770,10 @@ hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, 
     d.codes = m.down.codes; d.scales = m.down.scales;
     d.mat_codes = m.down.n_pad * m.down.k_pad; d.mat_scales = (m.down.d_out + 127) / 128 * (m.down.k_pad / 128);
     d.out = Y;
-    if (y_dtype == W4A4_Y_F32) run_down<W4A4_Y_F32>(d, st);
-    else run_down<W4A4_Y_BF16>(d, st);
+    d.y_dtype = y_dtype;
+    if (pass.xi == 1) run_down<1>(d, st);
+    else if (pass.xi == 2) run_down<2>(d, st);
+    else run_down<4>(d, st);
     return hipGetLastError();
 }
 
