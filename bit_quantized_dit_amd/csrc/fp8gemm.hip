@@ -12,8 +12,7 @@
 // a lane takes is free as long as both operands agree; these let the unquantized operand of
 // moe.hip be read in 64-byte pieces of its rows.)  Runs of a row block
 // follow each other along the inputs, so that whoever streams 16 rows reads one contiguous
-// range; copies to LDS are linear; and a 32-row fragment takes 16 rows from each of two runs
-// in 256-byte pieces that no two of 16 neighbouring lanes' banks share.
+// range, and copies to LDS and fragment reads are linear.
 //
 // Precision.  The FP8 matrix instructions (all of them, whatever their shape) line the
 // products of a few inputs up with the largest one and drop what falls about 13 bits below
@@ -35,7 +34,6 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 
 // How a tile computes: FP8 MFMA and scaling after each block, FP8 MFMA with scale operands,
 // or bf16 MFMA on widened codes and scaling after each block.
@@ -67,24 +65,32 @@ __device__ __forceinline__ void tile_at(uint32_t bid, uint32_t nt_m, uint32_t nt
 
 // ---------------------------------------------------------------- many tokens
 //
-// A workgroup of WT x WF wavefronts owns (WT FT 32) tokens x (WF FF 32) features, a
-// wavefront FT x FF tiles of 32 x 32.  The K loop walks blocks of 128 inputs through
-// two LDS slots filled by global -> LDS copies: block b + 1 arrives while b is computed.
+// A workgroup of WT x WF wavefronts owns (WT FT 16) tokens x (WF FF 16) features, a
+// wavefront FT x FF tiles of 16 x 16: with the 16-row instructions a block's sum takes four
+// registers until it is scaled, with the 32-row ones sixteen, which do not fit beside the
+// accumulators and the fragments.  The K loop walks blocks of 128 inputs through two LDS
+// slots filled by global -> LDS copies.  A wavefront has read all of a slot when it starts
+// its last token tile of the block; the block's one barrier sits there: behind it the slot's
+// refill (block b + 2) is issued, and the next block's first fragments are read from the
+// other slot while the last tiles' MFMAs run.  A tile is scaled LAG tiles later, across
+// block boundaries too, so that nothing waits for an MFMA's result.
 template <int FT, int FF, int WT, int WF, int MUL, int OUT>
 __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
     const uint8_t* __restrict__ Aq, const float* __restrict__ As, int64_t T, int64_t t_ld, const uint8_t* __restrict__ Bq,
     const float* __restrict__ Bs, int64_t N, int64_t nkb64, void* __restrict__ out, int vec_store) {
-    constexpr int BT = WT * FT * 32, BF = WF * FF * 32, NW = WT * WF;
+    constexpr int BT = WT * FT * 16, BF = WF * FF * 16, NW = WT * WF, NT = FT * FF, LAG = 3;
     constexpr int NFB = (BF + 127) / 128;                 // weight scale blocks across the tile
-    constexpr int PIECES = (BT + BF) / 32 * 4;            // 1 KiB copies per block
+    constexpr int PIECES = (BT + BF) / 16 * 2;            // 1 KiB copies per block
     constexpr int B_OFF = BT * 128, AS_OFF = (BT + BF) * 128, BS_OFF = AS_OFF + BT * 4;
     constexpr int SLOT = BS_OFF + NFB * 256;
     static_assert(PIECES % NW == 0 && BT / 64 + NFB <= NW && 32 * 128 * NW <= 2 * SLOT, "tile geometry");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SLOT];
+    static_assert(FT % 2 == 0 && NT % 4 == 0 && FF == 4, "buffers by parity; 64 features a wavefront");
+    // the slots, then 256 bytes that wavefronts without scales to copy fill with zeros
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SLOT + 256];
 
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wt = wave % WT, wf = wave / WT, l32 = lane & 31, lh = lane >> 5;
+    const int wt = wave % WT, wf = wave / WT;
     const int nkb = (int)nkb64;
     uint32_t tm, tn;
     tile_at<4>(blockIdx.x, (uint32_t)((T + BT - 1) / BT), (uint32_t)((N + BF - 1) / BF), tm, tn);
@@ -95,148 +101,166 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
     const v4i srd_b = make_srd(Bq + f0 / 16 * blk, (uint32_t)((rows_b + 15) / 16 * blk));
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
-    // copy the operands and scales of block kb into slot kb & 1
+    // What this wavefront copies of a block's scales: 64 tokens', or one 128-feature block's (the same
+    // word into 64 places), or nothing.
+    const bool sc_a = wave < BT / 64, sc_b = !sc_a && wave < BT / 64 + NFB && (wave - BT / 64) * 128 < rows_b;
+    const float* const sc_p = sc_a ? As + t0 : Bs + (sc_b ? (f0 / 128 + wave - BT / 64) * nkb64 : 0);
+    const int64_t sc_step = sc_a ? t_ld : sc_b ? 1 : 0;
+    const uint32_t sc_bytes = sc_a ? (uint32_t)(rows_a * 4) : sc_b ? 4u : 0u;
+    const int sc_off = sc_a ? wave * 256 + lane * 4 : 0;
+    // Copy the operands and scales of block kb into slot kb & 1.  Past the last block the same
+    // copies run with empty ranges (they write zeros): without branches, every wait below counts the
+    // same number of copies, and the compiler cannot move the tiles' arithmetic past one.
+    constexpr int COPIES = PIECES / NW + 1;
     auto issue = [&](int kb) __attribute__((always_inline)) {
+        const bool on = kb < nkb;
         const uint32_t slot = lds0 + (uint32_t)(kb & 1) * SLOT;
+        v4i a = srd_a, b = srd_b;
+        a[2] = on ? a[2] : 0;
+        b[2] = on ? b[2] : 0;
 #pragma unroll
         for (int i = 0; i < PIECES / NW; ++i) {
-            const int q = wave * (PIECES / NW) + i;       // wave-uniform
-            const int rb = q >> 1, sub = q & 1;
-            const bool is_a = rb < BT / 16;
-            const int r = is_a ? rb : rb - BT / 16;
-            dma16(is_a ? srd_a : srd_b, slot + q * 1024, (int)(r * blk) + sub * 1024 + lane * 16, kb * 2048);
+            constexpr int PA = BT / 16 * 2 / NW, PB = BF / 16 * 2 / NW;   // pieces of each operand a wavefront copies
+            static_assert(PA * NW == BT / 8 && PB * NW == BF / 8, "pieces divide evenly");
+            const bool is_a = i < PA;
+            const int q = is_a ? wave * PA + i : wave * PB + i - PA;      // wave-uniform
+            dma16(is_a ? a : b, slot + (is_a ? 0 : B_OFF) + q * 1024, (int)((q >> 1) * blk) + (q & 1) * 1024 + lane * 16, kb * 2048);
         }
-        if (wave < BT / 64) {
-            dma4(make_srd(As + (int64_t)kb * t_ld + t0, (uint32_t)(rows_a * 4)), slot + AS_OFF + wave * 256,
-                 wave * 256 + lane * 4, 0);
-        } else if (wave < BT / 64 + NFB) {
-            const int fb = wave - BT / 64;
-            const bool in = fb * 128 < rows_b;
-            dma4(make_srd(Bs + (in ? (f0 / 128 + fb) * nkb64 : 0) + kb, in ? 4u : 0u), slot + BS_OFF + fb * 256, 0, 0);
+        dma4(make_srd(sc_p + (on ? kb : 0) * sc_step, on ? sc_bytes : 0u),
+             sc_a ? slot + AS_OFF + wave * 256 : sc_b ? slot + BS_OFF + (wave - BT / 64) * 256 : lds0 + 2 * SLOT, sc_off, 0);
+    };
+
+    v4f acc[FT][FF];
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+#pragma unroll
+        for (int i = 0; i < FF; ++i) acc[j][i] = v4f{0, 0, 0, 0};
+    v8i fb[FF], fa[2];             // weight fragments; token fragments of tiles j, j + 1
+    float sa[2], sb = 0.f;
+    const uint8_t* const pa = smem + wt * FT * 2048 + lane * 16;
+    const uint8_t* const pb = smem + B_OFF + wf * FF * 2048 + lane * 16;
+    const uint8_t* const ps = smem + AS_OFF + (wt * FT * 16 + r16) * 4;
+    const uint8_t* const pw = smem + BS_OFF + (wf * FF * 16 / 128) * 256 + lane * 4;
+    auto frag = [&](const uint8_t* p) __attribute__((always_inline)) {
+        return join(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024));
+    };
+    auto load_a = [&](int slot, int j) __attribute__((always_inline)) {
+        fa[j & 1] = frag(pa + slot * SLOT + j * 2048);
+        sa[j & 1] = *reinterpret_cast<const float*>(ps + slot * SLOT + j * 64);
+    };
+    auto load_b = [&](int slot, int i) __attribute__((always_inline)) {
+        fb[i] = frag(pb + slot * SLOT + i * 2048);
+        if (i == FF - 1) sb = *reinterpret_cast<const float*>(pw + slot * SLOT);
+    };
+    v4f t[4];                      // sums of the last tiles
+    float st[2] = {0.f, 0.f};      // scales of the current and the last token tile
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = v4f{0, 0, 0, 0};
+    auto scale = [&](int n) __attribute__((always_inline)) {   // the tile LAG tiles before tile n
+        if constexpr (MUL != MUL_FP8_E8M0) {
+            const int q = (n + NT - LAG) % NT;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[q / FF][q % FF][r] = __builtin_fmaf(t[q & 3][r], st[(q / FF) & 1], acc[q / FF][q % FF][r]);
         }
     };
 
-    v16f acc[FF][FT];
-#pragma unroll
-    for (int i = 0; i < FF; ++i)
-#pragma unroll
-        for (int j = 0; j < FT; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
     issue(0);
+    issue(1);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"i"(COPIES) : "memory");   // block 0 is there
+    __syncthreads();
+    load_a(0, 0);
+#pragma unroll
+    for (int i = 0; i < FF; ++i) load_b(0, i);
     for (int kb = 0; kb < nkb; ++kb) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (kb + 1 < nkb) issue(kb + 1);
-        const uint8_t* slot = smem + (kb & 1) * SLOT;
-        auto frag = [&](int off, int rb, int half) __attribute__((always_inline)) {
-            const uint8_t* p = slot + off + (rb * 2 + (l32 >> 4)) * 2048 + half * 512 + lh * 256 + (lane & 15) * 16;
-            return join(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024));
-        };
-        v8i b[FF][2];
-#pragma unroll
-        for (int i = 0; i < FF; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) b[i][h] = frag(B_OFF, wf * FF + i, h);
-        const float sb = *reinterpret_cast<const float*>(slot + BS_OFF + (wf * FF * 32 / 128) * 256 + lane * 4);
-        static_assert(FF * 32 <= 128 && 128 % (FF * 32) == 0, "one weight scale per wavefront");
+        const int slot = kb & 1;
 #pragma unroll
         for (int j = 0; j < FT; ++j) {
-            const v8i a0 = frag(0, wt * FT + j, 0), a1 = frag(0, wt * FT + j, 1);
-            const float sa = *reinterpret_cast<const float*>(slot + AS_OFF + ((wt * FT + j) * 32 + l32) * 4);
-            if constexpr (MUL != MUL_FP8_E8M0) {
-                const float s = sa * sb;
-#pragma unroll
-                for (int i = 0; i < FF; ++i) {
-                    v16f t = v16f{};
-                    if constexpr (MUL == MUL_FP8) {
-                        t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[i][0], a0, t, 0, 0, 0, 0, 0, 0);
-                        t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[i][1], a1, t, 0, 0, 0, 0, 0, 0);
-                    } else {
-                        // a lane's 32 inputs in four steps of 8: any order of inputs, the same on both sides
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_e4m3(b[i][h][2 * q], b[i][h][2 * q + 1]),
-                                                                            h ? widen_e4m3(a1[2 * q], a1[2 * q + 1])
-                                                                              : widen_e4m3(a0[2 * q], a0[2 * q + 1]), t, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(t[r], s, acc[i][j][r]);
-                }
+            if (j + 1 < FT) {
+                load_a(slot, j + 1);
             } else {
-                // exponent field of a power of two; a NaN scale gives 0xFF, the E8M0 NaN
-                const int ea = (int)((__float_as_uint(sa) >> 23) & 0xFFu), eb = (int)((__float_as_uint(sb) >> 23) & 0xFFu);
+                // every read of this slot is in registers; the other slot's copies have landed
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                issue(kb + 2);
+            }
+            const int ea = (int)((__float_as_uint(sa[j & 1]) >> 23) & 0xFFu), eb = (int)((__float_as_uint(sb) >> 23) & 0xFFu);
+            st[j & 1] = sa[j & 1] * sb;
+            v8bf wa[4];
+            if constexpr (MUL == MUL_BF16) {
 #pragma unroll
-                for (int i = 0; i < FF; ++i) {
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[i][0], a0, acc[i][j], 0, 0, 0, eb, 0, ea);
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[i][1], a1, acc[i][j], 0, 0, 0, eb, 0, ea);
+                for (int q = 0; q < 4; ++q) wa[q] = widen_e4m3(fa[j & 1][2 * q], fa[j & 1][2 * q + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < FF; ++i) {
+                const int n = j * FF + i;
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (MUL == MUL_FP8) {
+                    t[n & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i], fa[j & 1], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                } else if constexpr (MUL == MUL_FP8_E8M0) {
+                    // exponent field of a power of two; a NaN scale gives 0xFF, the E8M0 NaN
+                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i], fa[j & 1], acc[j][i], 0, 0, 0, eb, 0, ea);
+                } else {
+                    t[n & 3] = v4f{0, 0, 0, 0};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        t[n & 3] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_e4m3(fb[i][2 * q], fb[i][2 * q + 1]), wa[q], t[n & 3], 0, 0, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                scale(n);
+                if (j + 1 == FT) {   // fragments of the next block, as theirs are used up (after the last: not used)
+                    if (i == 0) load_a(slot ^ 1, 0);
+                    load_b(slot ^ 1, i);
                 }
             }
         }
     }
+#pragma unroll
+    for (int n = 0; n < LAG; ++n) scale(n);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();   // the slots are free: each wavefront stages its tiles through 4 KiB of its own
 
-    // Lane l holds token l32 and features 8q + 4 lh + e of each tile; tiles are restaged
-    // so that stores write whole 128-byte lines (16-byte chunk c of row r at c ^ (r % 8)).
+    // Lane l holds token l % 16 and features 4 (l / 16) .. + 3 of each tile; 32 tokens are
+    // restaged so that stores write whole 128-byte lines (16-byte chunk c of row r at c ^ (r % 8)).
     uint8_t* const stage = smem + wave * 4096;
     const int rr = lane >> 3, cc = lane & 7;
-    if constexpr (OUT == W4A4_Y_F32) {
-        float* const Y = reinterpret_cast<float*>(out);
 #pragma unroll
-        for (int j = 0; j < FT; ++j)
+    for (int j = 0; j < FT; j += 2) {
+        constexpr int FP = OUT == W4A4_Y_F32 ? 2 : 4;      // feature tiles of a 128-byte row
 #pragma unroll
-            for (int i = 0; i < FF; ++i) {
+        for (int ip = 0; ip < FF; ip += FP) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<v4f*>(stage + l32 * 128 + (((2 * q + lh) ^ (l32 & 7)) << 4)) =
-                        v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = rr + 8 * k;
-                    const v4f v = *reinterpret_cast<const v4f*>(stage + r * 128 + ((cc ^ (r & 7)) << 4));
-                    const int64_t t = t0 + (wt * FT + j) * 32 + r, n = f0 + (wf * FF + i) * 32 + cc * 4;
-                    if (t >= T) continue;
-                    if (vec_store && n + 3 < N) {
-                        __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(Y + t * N + n));
-                    } else {
+                for (int i = 0; i < FP; ++i) {
+                    const v4f v = acc[j + h][ip + i];
+                    uint8_t* const row = stage + (h * 16 + r16) * 128;
+                    if constexpr (OUT == W4A4_Y_F32)
+                        *reinterpret_cast<v4f*>(row + (((i * 4 + g) ^ (r16 & 7)) << 4)) = v;
+                    else
+                        *reinterpret_cast<uint2*>(row + (((i * 2 + (g >> 1)) ^ (r16 & 7)) << 4) + (g & 1) * 8) =
+                            make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+                }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n + e < N) Y[t * N + n + e] = v[e];
+            for (int k = 0; k < 4; ++k) {
+                const int r = rr + 8 * k;
+                const v4i v = *reinterpret_cast<const v4i*>(stage + r * 128 + ((cc ^ (r & 7)) << 4));
+                constexpr int EL = OUT == W4A4_Y_F32 ? 4 : 8;
+                const int64_t tt = t0 + (wt * FT + j) * 16 + r, n = f0 + (wf * FF + ip) * 16 + cc * EL;
+                if (tt >= T) continue;
+                if (vec_store && n + EL - 1 < N) {
+                    __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(reinterpret_cast<uint8_t*>(out) + (tt * N + n) * (16 / EL)));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < EL; ++e) {
+                        if (n + e >= N) continue;
+                        if constexpr (OUT == W4A4_Y_F32) reinterpret_cast<int*>(out)[tt * N + n + e] = v[e];
+                        else reinterpret_cast<uint16_t*>(out)[tt * N + n + e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
                     }
                 }
             }
-    } else {
-        static_assert(FF % 2 == 0, "bf16 staging takes two feature tiles");
-        uint16_t* const Y = reinterpret_cast<uint16_t*>(out);
-#pragma unroll
-        for (int j = 0; j < FT; ++j)
-#pragma unroll
-            for (int ip = 0; ip < FF; ip += 2) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint2*>(stage + l32 * 128 + (((4 * i + q) ^ (l32 & 7)) << 4) + lh * 8) =
-                            make_uint2(pk_bf16(acc[ip + i][j][4 * q], acc[ip + i][j][4 * q + 1]),
-                                       pk_bf16(acc[ip + i][j][4 * q + 2], acc[ip + i][j][4 * q + 3]));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = rr + 8 * k;
-                    const v4i v = *reinterpret_cast<const v4i*>(stage + r * 128 + ((cc ^ (r & 7)) << 4));
-                    const int64_t t = t0 + (wt * FT + j) * 32 + r, n = f0 + (wf * FF + ip) * 32 + cc * 8;
-                    if (t >= T) continue;
-                    if (vec_store && n + 7 < N) {
-                        __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(Y + t * N + n));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (n + e < N) Y[t * N + n + e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
-                    }
-                }
-            }
+        }
     }
 }
 
@@ -328,7 +352,7 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
 template <int FT, int FF, int WT, int WF, int MUL, int OUT>
 hipError_t run_tiles(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
                      hipStream_t st) {
-    constexpr int BT = WT * FT * 32, BF = WF * FF * 32;
+    constexpr int BT = WT * FT * 16, BF = WF * FF * 16;
     const int64_t tiles = ((T + BT - 1) / BT) * ((d.d_out + BF - 1) / BF);
     hipLaunchKernelGGL((fp8_gemm_kernel<FT, FF, WT, WF, MUL, OUT>), dim3((uint32_t)tiles), dim3(WT * WF * 64), 0, st, aq, as, T,
                        t_ld, d.codes, d.scales, d.d_out, d.k_pad / 128, out, d.d_out % (OUT == W4A4_Y_F32 ? 4 : 8) == 0 ? 1 : 0);
@@ -339,8 +363,8 @@ template <int MUL, int OUT>
 hipError_t run_many(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
                     hipStream_t st) {
     if (((T + 255) / 256) * ((d.d_out + 255) / 256) >= 192)
-        return run_tiles<4, 2, 2, 4, MUL, OUT>(aq, as, T, t_ld, d, out, st);
-    return run_tiles<2, 2, 2, 2, MUL, OUT>(aq, as, T, t_ld, d, out, st);
+        return run_tiles<8, 4, 2, 4, MUL, OUT>(aq, as, T, t_ld, d, out, st);
+    return run_tiles<4, 4, 2, 2, MUL, OUT>(aq, as, T, t_ld, d, out, st);
 }
 
 template <int NT, int OUT>
