@@ -64,7 +64,7 @@ w4a4_fp8_ws_layout ws_layout(int64_t T, const w4a4_fp8_packed* d) {
     size_t off = 0;
     w.a_q = off;     off = align_up(off + (size_t)(round_up(T, 16) * d->k_pad));
     w.a_s = off;     off = align_up(off + (size_t)(d->k_pad / 128 * t_ld_of(T)) * 4);
-    w.partial = off;
+    w.partial = off; off = align_up(off + fp8_plan(T, d->d_out, d->k_pad).part_bytes);
     w.total = off;
     return w;
 }
@@ -197,7 +197,7 @@ int w4a4_fp8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_
     if (T == 0) return W4A4_OK;
     uint8_t* b = (uint8_t*)ws;
     return dev_status(launch_fp8_gemm(b + w.a_q, (const float*)(b + w.a_s), T, t_ld_of(T), *desc, Y, y_dtype,
-                                      (hipStream_t)stream));
+                                      (float*)(b + w.partial), (hipStream_t)stream));
 }
 
 int w4a4_fp8_linear(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc, void* Y, int y_dtype, void* ws,

@@ -39,6 +39,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // or bf16 MFMA on widened codes and scaling after each block.
 constexpr int MUL_FP8 = 0, MUL_FP8_E8M0 = 1, MUL_BF16 = 2;
 
+constexpr int64_t FP8_FEW = 64;   // up to here the few-token kernel
+
 __device__ __forceinline__ v8i join(const uint4& a, const uint4& b) {
     return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
@@ -64,7 +66,55 @@ __device__ __forceinline__ void tile_at(uint32_t bid, uint32_t nt_m, uint32_t nt
 }
 
 // ---------------------------------------------------------------- many tokens
-//
+
+// The outputs of a wavefront's FT x FF tiles, the first at token t0 and feature f0, through 4 KiB of
+// LDS of its own.
+template <int FT, int FF, int OUT>
+__device__ __forceinline__ void store_tiles(const v4f (&acc)[FT][FF], uint8_t* stage, int64_t t0, int64_t f0, int64_t T,
+                                            int64_t N, void* __restrict__ out, int vec_store) {
+    // Lane l holds token l % 16 and features 4 (l / 16) .. + 3 of each tile; 32 tokens are
+    // restaged so that stores write whole 128-byte lines (16-byte chunk c of row r at c ^ (r % 8)).
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int rr = lane >> 3, cc = lane & 7;
+#pragma unroll
+    for (int j = 0; j < FT; j += 2) {
+        constexpr int FP = OUT == W4A4_Y_F32 ? 2 : 4;      // feature tiles of a 128-byte row
+#pragma unroll
+        for (int ip = 0; ip < FF; ip += FP) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < FP; ++i) {
+                    const v4f v = acc[j + h][ip + i];
+                    uint8_t* const row = stage + (h * 16 + r16) * 128;
+                    if constexpr (OUT == W4A4_Y_F32)
+                        *reinterpret_cast<v4f*>(row + (((i * 4 + g) ^ (r16 & 7)) << 4)) = v;
+                    else
+                        *reinterpret_cast<uint2*>(row + (((i * 2 + (g >> 1)) ^ (r16 & 7)) << 4) + (g & 1) * 8) =
+                            make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = rr + 8 * k;
+                const v4i v = *reinterpret_cast<const v4i*>(stage + r * 128 + ((cc ^ (r & 7)) << 4));
+                constexpr int EL = OUT == W4A4_Y_F32 ? 4 : 8;
+                const int64_t tt = t0 + j * 16 + r, n = f0 + ip * 16 + cc * EL;
+                if (tt >= T) continue;
+                if (vec_store && n + EL - 1 < N) {
+                    __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(reinterpret_cast<uint8_t*>(out) + (tt * N + n) * (16 / EL)));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < EL; ++e) {
+                        if (n + e >= N) continue;
+                        if constexpr (OUT == W4A4_Y_F32) reinterpret_cast<int*>(out)[tt * N + n + e] = v[e];
+                        else reinterpret_cast<uint16_t*>(out)[tt * N + n + e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+                    }
+                }
+            }
+        }
+    }
+}
+
 // A workgroup of WT x WF wavefronts owns (WT FT 16) tokens x (WF FF 16) features, a
 // wavefront FT x FF tiles of 16 x 16: with the 16-row instructions a block's sum takes four
 // registers until it is scaled, with the 32-row ones sixteen, which do not fit beside the
@@ -74,10 +124,17 @@ __device__ __forceinline__ void tile_at(uint32_t bid, uint32_t nt_m, uint32_t nt
 // refill (block b + 2) is issued, and the next block's first fragments are read from the
 // other slot while the last tiles' MFMAs run.  A tile is scaled LAG tiles later, across
 // block boundaries too, so that nothing waits for an MFMA's result.
+//
+// Tiles that would leave most CUs idle in a last round run as sp.n ranges of their blocks, whose
+// sums go to memory; fp8_reduce_kernel adds them in order.
+struct Split {
+    float* part;
+    uint32_t full, n;
+};
 template <int FT, int FF, int WT, int WF, int MUL, int OUT>
 __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
     const uint8_t* __restrict__ Aq, const float* __restrict__ As, int64_t T, int64_t t_ld, const uint8_t* __restrict__ Bq,
-    const float* __restrict__ Bs, int64_t N, int64_t nkb64, void* __restrict__ out, int vec_store) {
+    const float* __restrict__ Bs, int64_t N, int64_t nkb64, void* __restrict__ out, int vec_store, Split sp) {
     constexpr int BT = WT * FT * 16, BF = WF * FF * 16, NW = WT * WF, NT = FT * FF, LAG = 3;
     constexpr int NFB = (BF + 127) / 128;                 // weight scale blocks across the tile
     constexpr int PIECES = (BT + BF) / 16 * 2;            // 1 KiB copies per block
@@ -91,20 +148,26 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wt = wave % WT, wf = wave / WT;
-    const int nkb = (int)nkb64;
+    // a whole tile, or one of sp.n ranges of a later tile's blocks
+    const uint32_t late = blockIdx.x < sp.full ? 0 : blockIdx.x - sp.full;
+    const uint32_t id = blockIdx.x < sp.full ? blockIdx.x : sp.full + late / sp.n;
+    const int part = blockIdx.x < sp.full ? 0 : (int)(late % sp.n), parts = blockIdx.x < sp.full ? 1 : (int)sp.n;
+    const int kb0 = (int)(nkb64 * part / parts), nkb = (int)(nkb64 * (part + 1) / parts) - kb0;
     uint32_t tm, tn;
-    tile_at<4>(blockIdx.x, (uint32_t)((T + BT - 1) / BT), (uint32_t)((N + BF - 1) / BF), tm, tn);
+    tile_at<4>(id, (uint32_t)((T + BT - 1) / BT), (uint32_t)((N + BF - 1) / BF), tm, tn);
     const int64_t t0 = (int64_t)tm * BT, f0 = (int64_t)tn * BF;
     const int64_t rows_a = T - t0 < BT ? T - t0 : BT, rows_b = N - f0 < BF ? N - f0 : BF;
     const int64_t blk = nkb64 * 2048;                     // bytes of 16 rows
-    const v4i srd_a = make_srd(Aq + t0 / 16 * blk, (uint32_t)((rows_a + 15) / 16 * blk));
-    const v4i srd_b = make_srd(Bq + f0 / 16 * blk, (uint32_t)((rows_b + 15) / 16 * blk));
+    // (a range's first block goes into the bases; a row block then still passes the range check
+    // exactly when it is valid, as kb0 * 2048 is less than one row block)
+    const v4i srd_a = make_srd(Aq + t0 / 16 * blk + kb0 * 2048, (uint32_t)((rows_a + 15) / 16 * blk - kb0 * 2048));
+    const v4i srd_b = make_srd(Bq + f0 / 16 * blk + kb0 * 2048, (uint32_t)((rows_b + 15) / 16 * blk - kb0 * 2048));
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
     // What this wavefront copies of a block's scales: 64 tokens', or one 128-feature block's (the same
     // word into 64 places), or nothing.
     const bool sc_a = wave < BT / 64, sc_b = !sc_a && wave < BT / 64 + NFB && (wave - BT / 64) * 128 < rows_b;
-    const float* const sc_p = sc_a ? As + t0 : Bs + (sc_b ? (f0 / 128 + wave - BT / 64) * nkb64 : 0);
+    const float* const sc_p = sc_a ? As + (int64_t)kb0 * t_ld + t0 : Bs + (sc_b ? (f0 / 128 + wave - BT / 64) * nkb64 + kb0 : 0);
     const int64_t sc_step = sc_a ? t_ld : sc_b ? 1 : 0;
     const uint32_t sc_bytes = sc_a ? (uint32_t)(rows_a * 4) : sc_b ? 4u : 0u;
     const int sc_off = sc_a ? wave * 256 + lane * 4 : 0;
@@ -219,49 +282,46 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
 #pragma unroll
     for (int n = 0; n < LAG; ++n) scale(n);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (blockIdx.x >= sp.full) {   // a range's sums as they lie in the registers, 1 KiB a store
+        v4f* const p = reinterpret_cast<v4f*>(sp.part) + ((int64_t)late * NW + wave) * NT * 64 + lane;
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int i = 0; i < FF; ++i) p[(j * FF + i) * 64] = acc[j][i];
+        return;
+    }
     __syncthreads();   // the slots are free: each wavefront stages its tiles through 4 KiB of its own
 
-    // Lane l holds token l % 16 and features 4 (l / 16) .. + 3 of each tile; 32 tokens are
-    // restaged so that stores write whole 128-byte lines (16-byte chunk c of row r at c ^ (r % 8)).
-    uint8_t* const stage = smem + wave * 4096;
-    const int rr = lane >> 3, cc = lane & 7;
+    store_tiles<FT, FF, OUT>(acc, smem + wave * 4096, t0 + wt * FT * 16, f0 + wf * FF * 16, T, N, out, vec_store);
+}
+
+// One wavefront per FT x FF sub-tile of a split tile: its ranges' sums, in order, then the outputs.
+template <int FT, int FF, int WT, int WF, int OUT>
+__global__ __launch_bounds__(64) void fp8_reduce_kernel(int64_t T, int64_t N, void* __restrict__ out, int vec_store, Split sp) {
+    constexpr int BT = WT * FT * 16, BF = WF * FF * 16, NW = WT * WF, NT = FT * FF;
+    __shared__ __attribute__((aligned(1024))) uint8_t stage[4096];
+    const uint32_t tile = blockIdx.x / NW, wave = blockIdx.x % NW;
+    uint32_t tm, tn;
+    tile_at<4>(sp.full + tile, (uint32_t)((T + BT - 1) / BT), (uint32_t)((N + BF - 1) / BF), tm, tn);
+    const v4f* p = reinterpret_cast<const v4f*>(sp.part) + ((int64_t)tile * sp.n * NW + wave) * NT * 64 + threadIdx.x;
+    v4f acc[FT][FF];
 #pragma unroll
-    for (int j = 0; j < FT; j += 2) {
-        constexpr int FP = OUT == W4A4_Y_F32 ? 2 : 4;      // feature tiles of a 128-byte row
+    for (int j = 0; j < FT; ++j)
 #pragma unroll
-        for (int ip = 0; ip < FF; ip += FP) {
+        for (int i = 0; i < FF; ++i) acc[j][i] = p[(j * FF + i) * 64];
+    for (uint32_t c = 1; c < sp.n; ++c) {
+        p += NW * NT * 64;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < FT; ++j)
 #pragma unroll
-                for (int i = 0; i < FP; ++i) {
-                    const v4f v = acc[j + h][ip + i];
-                    uint8_t* const row = stage + (h * 16 + r16) * 128;
-                    if constexpr (OUT == W4A4_Y_F32)
-                        *reinterpret_cast<v4f*>(row + (((i * 4 + g) ^ (r16 & 7)) << 4)) = v;
-                    else
-                        *reinterpret_cast<uint2*>(row + (((i * 2 + (g >> 1)) ^ (r16 & 7)) << 4) + (g & 1) * 8) =
-                            make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
-                }
+            for (int i = 0; i < FF; ++i) {
+                const v4f v = p[(j * FF + i) * 64];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = rr + 8 * k;
-                const v4i v = *reinterpret_cast<const v4i*>(stage + r * 128 + ((cc ^ (r & 7)) << 4));
-                constexpr int EL = OUT == W4A4_Y_F32 ? 4 : 8;
-                const int64_t tt = t0 + (wt * FT + j) * 16 + r, n = f0 + (wf * FF + ip) * 16 + cc * EL;
-                if (tt >= T) continue;
-                if (vec_store && n + EL - 1 < N) {
-                    __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(reinterpret_cast<uint8_t*>(out) + (tt * N + n) * (16 / EL)));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < EL; ++e) {
-                        if (n + e >= N) continue;
-                        if constexpr (OUT == W4A4_Y_F32) reinterpret_cast<int*>(out)[tt * N + n + e] = v[e];
-                        else reinterpret_cast<uint16_t*>(out)[tt * N + n + e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
-                    }
-                }
+                for (int r = 0; r < 4; ++r) acc[j][i][r] += v[r];
             }
-        }
     }
+    store_tiles<FT, FF, OUT>(acc, stage, (int64_t)tm * BT + wave % WT * FT * 16, (int64_t)tn * BF + wave / WT * FF * 16, T, N, out,
+                             vec_store);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -350,21 +410,26 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
 }
 
 template <int FT, int FF, int WT, int WF, int MUL, int OUT>
-hipError_t run_tiles(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
-                     hipStream_t st) {
-    constexpr int BT = WT * FT * 16, BF = WF * FF * 16;
-    const int64_t tiles = ((T + BT - 1) / BT) * ((d.d_out + BF - 1) / BF);
-    hipLaunchKernelGGL((fp8_gemm_kernel<FT, FF, WT, WF, MUL, OUT>), dim3((uint32_t)tiles), dim3(WT * WF * 64), 0, st, aq, as, T,
-                       t_ld, d.codes, d.scales, d.d_out, d.k_pad / 128, out, d.d_out % (OUT == W4A4_Y_F32 ? 4 : 8) == 0 ? 1 : 0);
+hipError_t run_tiles(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out, float* part,
+                     const Fp8Plan& plan, hipStream_t st) {
+    const int vec = d.d_out % (OUT == W4A4_Y_F32 ? 4 : 8) == 0 ? 1 : 0;
+    const Split sp = {part, (uint32_t)plan.full, (uint32_t)plan.split};
+    const int64_t tail = plan.tiles - plan.full;
+    hipLaunchKernelGGL((fp8_gemm_kernel<FT, FF, WT, WF, MUL, OUT>), dim3((uint32_t)(plan.full + tail * plan.split)), dim3(WT * WF * 64),
+                       0, st, aq, as, T, t_ld, d.codes, d.scales, d.d_out, d.k_pad / 128, out, vec, sp);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !tail) return e;
+    hipLaunchKernelGGL((fp8_reduce_kernel<FT, FF, WT, WF, OUT>), dim3((uint32_t)(tail * WT * WF)), dim3(64), 0, st, T, d.d_out, out,
+                       vec, sp);
     return hipGetLastError();
 }
 
 template <int MUL, int OUT>
-hipError_t run_many(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
+hipError_t run_many(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out, float* part,
                     hipStream_t st) {
-    if (((T + 255) / 256) * ((d.d_out + 255) / 256) >= 192)
-        return run_tiles<8, 4, 2, 4, MUL, OUT>(aq, as, T, t_ld, d, out, st);
-    return run_tiles<4, 4, 2, 2, MUL, OUT>(aq, as, T, t_ld, d, out, st);
+    const Fp8Plan plan = fp8_plan(T, d.d_out, d.k_pad);
+    if (plan.big) return run_tiles<8, 4, 2, 4, MUL, OUT>(aq, as, T, t_ld, d, out, part, plan, st);
+    return run_tiles<4, 4, 2, 2, MUL, OUT>(aq, as, T, t_ld, d, out, part, plan, st);
 }
 
 template <int NT, int OUT>
@@ -376,22 +441,46 @@ hipError_t run_few(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, 
 }
 
 template <int OUT>
-hipError_t run_out(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
+hipError_t run_out(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out, float* part,
                    hipStream_t st) {
     if (T <= 16) return run_few<1, OUT>(aq, as, T, t_ld, d, out, st);
     if (T <= 32) return run_few<2, OUT>(aq, as, T, t_ld, d, out, st);
-    if (T <= 64) return run_few<4, OUT>(aq, as, T, t_ld, d, out, st);
-    if constexpr (OUT == W4A4_Y_F32) return run_many<MUL_BF16, OUT>(aq, as, T, t_ld, d, out, st);
-    else if (d.scale_kind == W4A4_FP8_SCALE_F32) return run_many<MUL_FP8, OUT>(aq, as, T, t_ld, d, out, st);
-    else return run_many<MUL_FP8_E8M0, OUT>(aq, as, T, t_ld, d, out, st);
+    if (T <= FP8_FEW) return run_few<4, OUT>(aq, as, T, t_ld, d, out, st);
+    if constexpr (OUT == W4A4_Y_F32) return run_many<MUL_BF16, OUT>(aq, as, T, t_ld, d, out, part, st);
+    else if (d.scale_kind == W4A4_FP8_SCALE_F32) return run_many<MUL_FP8, OUT>(aq, as, T, t_ld, d, out, part, st);
+    else return run_many<MUL_FP8_E8M0, OUT>(aq, as, T, t_ld, d, out, part, st);
 }
 
 }  // namespace
 
+// Big tiles are 256 x 256, one workgroup a CU; small ones 128 x 128, two a CU.  The tiles that fill
+// whole rounds of the CUs run whole; the rest are cut along the inputs into as many ranges as there
+// are free CUs, at least MIN_BLOCKS blocks each.
+Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t k_pad) {
+    Fp8Plan p = {0, 0, 1, false, 0};
+    if (T <= FP8_FEW) return p;
+    constexpr int64_t CUS = 256, MIN_BLOCKS = 4, MAX_SPLIT = 16;
+    const int64_t nkb = k_pad / 128, big = ((T + 255) / 256) * ((N + 255) / 256);
+    p.big = big >= 64;
+    p.tiles = p.big ? big : ((T + 127) / 128) * ((N + 127) / 128);
+    const int64_t round = p.big ? CUS : 2 * CUS, tail = p.tiles % round;
+    p.full = p.tiles;
+    if (tail) {
+        int64_t s = round / tail < MAX_SPLIT ? round / tail : MAX_SPLIT;
+        if (s > nkb / MIN_BLOCKS) s = nkb / MIN_BLOCKS;
+        if (s >= 2) {
+            p.full -= tail;
+            p.split = (int32_t)s;
+            p.part_bytes = (size_t)(tail * s) * (p.big ? 256 * 256 : 128 * 128) * 4;
+        }
+    }
+    return p;
+}
+
 hipError_t launch_fp8_gemm(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
-                           int y_dtype, hipStream_t st) {
-    return y_dtype == W4A4_Y_F32 ? run_out<W4A4_Y_F32>(aq, as, T, t_ld, d, out, st)
-                                 : run_out<W4A4_Y_BF16>(aq, as, T, t_ld, d, out, st);
+                           int y_dtype, float* part, hipStream_t st) {
+    return y_dtype == W4A4_Y_F32 ? run_out<W4A4_Y_F32>(aq, as, T, t_ld, d, out, part, st)
+                                 : run_out<W4A4_Y_BF16>(aq, as, T, t_ld, d, out, part, st);
 }
 
 }  // namespace w4a4
