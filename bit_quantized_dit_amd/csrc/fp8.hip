@@ -4,71 +4,13 @@
 //
 //   s = max(fl32(amax / 448), 2^-60), or the smallest power of two >= 2^-60 with
 //   amax <= 448 s;  q = e4m3_rne(fl32(x / s)).
-//
-// fl32(x / s) is the double product x * RN64(1 / s) rounded to binary32: it lies within
-// 2^-52 (relative) of x / s, and a quotient of two binary32 numbers stays further than
-// that from every binary32 rounding midpoint, so the rounding lands on the same value
-// (quotients below the normal range become the code 0 either way).
-#include "w4a4_device.h"
+#include "fp8_device.h"
 #include "w4a4_internal.h"
 
 namespace w4a4 {
 
 namespace {
 
-// Scale of a block from the bit pattern of its largest |x|.
-__device__ __forceinline__ float block_scale(uint32_t amax_bits, int kind) {
-    if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-    if (kind == W4A4_FP8_SCALE_F32) return __builtin_fmaxf(__uint_as_float(amax_bits) / 448.0f, 0x1p-60f);
-    // amax = (1 + m / 2^23) 2^(e - 127), 448 = 1.75 * 2^8
-    const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return __uint_as_float((uint32_t)(e < 127 - 60 ? 127 - 60 : e) << 23);
-}
-
-// 16 values to 16 codes; a block whose scale is NaN has zero codes.
-__device__ __forceinline__ uint4 encode16(const float* x, float s) {
-    if (s != s) return make_uint4(0, 0, 0, 0);
-    const double rinv = 1.0 / (double)s;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = (float)((double)x[4 * i + j] * rinv);
-        int r = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], r, true);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Values p .. p + 7 of a row of `cols`, zero past its end; `vec`: the row starts on a
-// 16-byte boundary (p is a multiple of 8).
-__device__ __forceinline__ void load8(const float* row, int64_t p, int64_t cols, bool vec, float* x) {
-    if (vec && p + 8 <= cols) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(row + p + 4 * i);
-            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p + i < cols ? row[p + i] : 0.0f;
-}
-__device__ __forceinline__ void load8(const uint16_t* row, int64_t p, int64_t cols, bool vec, float* x) {
-    if (vec && p + 8 <= cols) {
-        const uint4 v = *reinterpret_cast<const uint4*>(row + p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p + i < cols ? bf16_to_f32(row[p + i]) : 0.0f;
-}
 // The 16 values of one 16-byte piece of the packed order: inputs p .. + 7 and p + 32 .. + 39
 // (p = 64 half + 8 chunk of the block).
 template <typename X>
@@ -77,32 +19,43 @@ __device__ __forceinline__ void load_piece(const X* row, int64_t p, int64_t cols
     load8(row, p + 32, cols, vec, x + 8);
 }
 
-// Activations.  A wavefront takes 8 tokens x one block of 128 inputs: lane l holds the 16
-// inputs of the (l / 8)-th 16-byte piece of token l % 8, and the pieces of 8 consecutive
-// tokens are 128 contiguous bytes: every store instruction writes whole cache lines.
+template <typename Inv>
+__device__ __forceinline__ uint4 encode_piece(const float* x, float s, const Inv& inv) {
+    const uint2 a = encode8(x, s, inv), b = encode8(x + 8, s, inv);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+// Activations.  A wavefront takes 16 tokens x one block of 128 inputs, one run of the packed order:
+// lane l holds the 32 inputs that it has in the matrix instructions (token l % 16, inputs
+// 32 q + 8 (l / 16) .. + 7), so that the two stores write one KiB each.
 template <typename X>
 __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__ x, int64_t T, int64_t d_in, int64_t nkb,
                                                            int64_t items, int kind, int vec, uint8_t* __restrict__ aq,
                                                            float* __restrict__ as, int64_t t_ld) {
-    const int lane = threadIdx.x & 63, tk = lane & 7, i = lane >> 3;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (item >= items) return;
     const int64_t tg = item / nkb, kb = item - tg * nkb;
-    const int64_t t = tg * 8 + tk;
+    const int64_t t = tg * 16 + r;
     const bool live = t < T;
-    float v[16];
-    load_piece(x + (live ? t : 0) * d_in, kb * 128 + (i >> 2) * 64 + (i & 3) * 8, d_in, vec != 0, v);
+    const X* const row = x + (live ? t : T - 1) * d_in;
+    float v[2][16];
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[j]));
+    for (int h = 0; h < 2; ++h) load_piece(row, kb * 128 + h * 64 + g * 8, d_in, vec != 0, v[h]);
 #pragma unroll
-    for (int o = 8; o < 64; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[h][j]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
     const float s = block_scale(m, kind);
-    const uint4 c = encode16(v, s);
+    const typename InverseOf<X>::type inv(s);
     if (!live) return;
-    uint8_t* dst = aq + ((t / 16) * nkb + kb) * 2048 + i * 256 + (t & 15) * 16;
-    *reinterpret_cast<uint4*>(dst) = c;
-    if (i == 0) as[kb * t_ld + t] = s;
+    uint8_t* const dst = aq + item * 2048 + lane * 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + h * 1024) = encode_piece(v[h], s, inv);
+    if (g == 0) as[kb * t_ld + t] = s;
 }
 
 // Weights: one workgroup per 128 x 128 block; thread = (row, half of the block's inputs).
@@ -136,11 +89,12 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, 
     const float s = block_scale(m, kind);
     if (threadIdx.x == 0) scales[b] = s;
     if (row >= n_pad) return;
+    const typename InverseOf<W>::type inv(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint8_t* dst = codes + ((mat * (n_pad / 16) + row / 16) * nkb + kb) * 2048 + (threadIdx.x & 1) * 1024 + i * 256 +
                        (row & 15) * 16;
-        *reinterpret_cast<uint4*>(dst) = encode16(v[i], s);
+        *reinterpret_cast<uint4*>(dst) = encode_piece(v[i], s, inv);
     }
 }
 
@@ -189,7 +143,7 @@ __global__ __launch_bounds__(256) void fp8_scales_kernel(const void* __restrict_
 
 hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_in, int kind, uint8_t* aq, float* as,
                                int64_t t_ld, hipStream_t st) {
-    const int64_t nkb = (d_in + 127) / 128, items = (T + 7) / 8 * nkb;
+    const int64_t nkb = (d_in + 127) / 128, items = (T + 15) / 16 * nkb;
     const dim3 grid((uint32_t)((items + 3) / 4));
     if (x_dtype == W4A4_X_BF16)
         hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, items,

@@ -50,9 +50,9 @@ int check_layer(int64_t T, const w4a4_fp8_packed* d) {
     const int st = check_packed(d);
     if (st) return st;
     if (d->n_mat != 1) return W4A4_ERR_INVALID;
-    // one workgroup per 128 x 128 outputs, one wavefront per 8 tokens x 128 inputs
+    // one workgroup per 128 x 128 outputs, one wavefront per 16 tokens x 128 inputs
     if (T > kMaxBlocks * 4 || (T + 127) / 128 * ((d->d_out + 127) / 128) > kMaxBlocks ||
-        ((T + 7) / 8 * (d->k_pad / 128) + 3) / 4 > kMaxBlocks)
+        ((T + 15) / 16 * (d->k_pad / 128) + 3) / 4 > kMaxBlocks)
         return W4A4_ERR_SHAPE;
     return W4A4_OK;
 }
@@ -67,6 +67,14 @@ w4a4_fp8_ws_layout ws_layout(int64_t T, const w4a4_fp8_packed* d) {
     w.partial = off; off = align_up(off + fp8_plan(T, d->d_out, d->k_pad).part_bytes);
     w.total = off;
     return w;
+}
+
+int check_quantize(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* d, const void* ws, size_t ws_bytes) {
+    const int st = check_layer(T, d);
+    if (st) return st;
+    if (!X || !ws || !valid_x(x_dtype)) return W4A4_ERR_INVALID;
+    if (misaligned(X) || misaligned(ws)) return W4A4_ERR_ALIGN;
+    return ws_bytes < ws_layout(T, d).total ? W4A4_ERR_SHAPE : W4A4_OK;
 }
 
 int describe(int64_t n_mat, int64_t d_in, int64_t d_out, int kind, void* blob, size_t blob_bytes, w4a4_fp8_packed* out) {
@@ -174,13 +182,9 @@ int w4a4_fp8_workspace_size(int64_t T, const w4a4_fp8_packed* desc, size_t* byte
 
 int w4a4_fp8_quantize_activations(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc, void* ws, size_t ws_bytes,
                                   void* stream) {
-    const int st = check_layer(T, desc);
-    if (st) return st;
-    if (!X || !ws || !valid_x(x_dtype)) return W4A4_ERR_INVALID;
-    if (misaligned(X) || misaligned(ws)) return W4A4_ERR_ALIGN;
+    const int st = check_quantize(X, x_dtype, T, desc, ws, ws_bytes);
+    if (st || T == 0) return st;
     const w4a4_fp8_ws_layout w = ws_layout(T, desc);
-    if (ws_bytes < w.total) return W4A4_ERR_SHAPE;
-    if (T == 0) return W4A4_OK;
     uint8_t* b = (uint8_t*)ws;
     return dev_status(launch_fp8_actquant(X, x_dtype, T, desc->d_in, desc->scale_kind, b + w.a_q, (float*)(b + w.a_s),
                                           t_ld_of(T), (hipStream_t)stream));

@@ -25,7 +25,7 @@
 // Scales.  The MFMAs of a block start from zero, and acc += (s_x s_w) * sum is one fused
 // multiply-add per output and block.  E8M0 scales with bf16 outputs: the instruction's own
 // scale operands apply both scales and the accumulators run through.
-#include "w4a4_device.h"
+#include "fp8_device.h"
 #include "w4a4_internal.h"
 
 namespace w4a4 {
@@ -39,7 +39,11 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // or bf16 MFMA on widened codes and scaling after each block.
 constexpr int MUL_FP8 = 0, MUL_FP8_E8M0 = 1, MUL_BF16 = 2;
 
-constexpr int64_t FP8_FEW = 64;   // up to here the few-token kernel
+// Whether the few-token kernel runs: up to 64 tokens, and small layers, whose tiles would fill few
+// CUs for many latencies (256 x 512 -> 1024: 9.9 us in tiles, NOTE here).
+bool fp8_few(int64_t T, int64_t N, int64_t k_pad) {
+    return T <= 64 || (T <= 1024 && (T + 63) / 64 * ((N + 15) / 16) * (k_pad / 128) <= 8192);
+}
 
 __device__ __forceinline__ v8i join(const uint4& a, const uint4& b) {
     return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
@@ -145,7 +149,7 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
     // the slots, then 256 bytes that wavefronts without scales to copy fill with zeros
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SLOT + 256];
 
-    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wt = wave % WT, wf = wave / WT;
     // a whole tile, or one of sp.n ranges of a later tile's blocks
@@ -295,41 +299,60 @@ __global__ __launch_bounds__(WT * WF * 64, 1) void fp8_gemm_kernel(
     store_tiles<FT, FF, OUT>(acc, smem + wave * 4096, t0 + wt * FT * 16, f0 + wf * FF * 16, T, N, out, vec_store);
 }
 
-// One wavefront per FT x FF sub-tile of a split tile: its ranges' sums, in order, then the outputs.
+// One wavefront per two token tiles x FF of a split tile: its ranges' sums, in order, then the outputs.
 template <int FT, int FF, int WT, int WF, int OUT>
 __global__ __launch_bounds__(64) void fp8_reduce_kernel(int64_t T, int64_t N, void* __restrict__ out, int vec_store, Split sp) {
     constexpr int BT = WT * FT * 16, BF = WF * FF * 16, NW = WT * WF, NT = FT * FF;
     __shared__ __attribute__((aligned(1024))) uint8_t stage[4096];
-    const uint32_t tile = blockIdx.x / NW, wave = blockIdx.x % NW;
+    const uint32_t jp = blockIdx.x % (FT / 2) * 2, sub = blockIdx.x / (FT / 2), tile = sub / NW, wave = sub % NW;
     uint32_t tm, tn;
     tile_at<4>(sp.full + tile, (uint32_t)((T + BT - 1) / BT), (uint32_t)((N + BF - 1) / BF), tm, tn);
-    const v4f* p = reinterpret_cast<const v4f*>(sp.part) + ((int64_t)tile * sp.n * NW + wave) * NT * 64 + threadIdx.x;
-    v4f acc[FT][FF];
+    const int64_t t0 = (int64_t)tm * BT + (wave % WT * FT + jp) * 16, f0 = (int64_t)tn * BF + wave / WT * FF * 16;
+    if (t0 >= T || f0 >= N) return;
+    const v4f* p = reinterpret_cast<const v4f*>(sp.part) + (((int64_t)tile * sp.n * NW + wave) * NT + jp * FF) * 64 + threadIdx.x;
+    v4f acc[2][FF];
 #pragma unroll
-    for (int j = 0; j < FT; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < FF; ++i) acc[j][i] = p[(j * FF + i) * 64];
-    for (uint32_t c = 1; c < sp.n; ++c) {
-        p += NW * NT * 64;
+        for (int i = 0; i < FF; ++i) acc[j][i] = v4f{0, 0, 0, 0};
+    for (uint32_t c = 0; c < sp.n; c += 4) {   // four ranges' loads in flight
+        v4f v[4][2][FF];
 #pragma unroll
-        for (int j = 0; j < FT; ++j)
+        for (int u = 0; u < 4; ++u) {
+            const v4f* const q = p + (int64_t)(c + u < sp.n ? c + u : c) * NW * NT * 64;
 #pragma unroll
-            for (int i = 0; i < FF; ++i) {
-                const v4f v = p[(j * FF + i) * 64];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[j][i][r] += v[r];
+                for (int i = 0; i < FF; ++i) v[u][j][i] = q[(j * FF + i) * 64];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (c + u < sp.n) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < FF; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[j][i][r] += v[u][j][i][r];
             }
     }
-    store_tiles<FT, FF, OUT>(acc, stage, (int64_t)tm * BT + wave % WT * FT * 16, (int64_t)tn * BF + wave / WT * FF * 16, T, N, out,
-                             vec_store);
+    store_tiles<2, FF, OUT>(acc, stage, t0, f0, T, N, out, vec_store);
 }
 
 // ---------------------------------------------------------------- few tokens
 //
 // Bound by reading the weight codes once.  A workgroup owns 16 weight rows; its eight
-// wavefronts take every eighth block of 128 inputs, read codes straight from memory, widen them to bf16 and multiply
-// them with up to NT tiles of 16 tokens by v_mfma_f32_16x16x32_bf16; the eight partial sums
-// meet in LDS and are added in wavefront order.
+// wavefronts take every eighth block of 128 inputs, read codes straight from memory, widen
+// them to bf16 and multiply them with up to NT tiles of 16 tokens by v_mfma_f32_16x16x32_bf16;
+// the eight partial sums meet in LDS and are added in wavefront order.
+//
+// The loop is as simple as it looks on purpose: at 40 registers all 864 workgroups of a 13824-row
+// layer are resident and cover each other's waits (one token, 5120 -> 13824: 12.6 us).  A ring of
+// blocks in flight per wavefront with the registers that it takes was slower (16.8), so was
+// quantizing the token in the same kernel (17.9, against 3.3 more for the quantization's launch),
+// and non-temporal loads lose a layer that stays in the 256 MB memory-side cache (24 tokens,
+// 13824 -> 5120: 29 against 19 us).
 template <int NT, int OUT>
 __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict__ Aq, const float* __restrict__ As, int64_t T,
                                                        int64_t t_ld, const uint8_t* __restrict__ Bq,
@@ -339,13 +362,13 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
     __shared__ __attribute__((aligned(16))) float red[8 * NT * 16 * LD];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * NT * 16;
     const int64_t blk = nkb * 2048;
     const uint8_t* const bp = Bq + blockIdx.x * blk + lane * 16;
     const float* const sp = Bs + n0 / 128 * nkb;
     const uint8_t* ap[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) ap[i] = Aq + (i * 16 < T ? i : 0) * blk + lane * 16;
+    for (int i = 0; i < NT; ++i) ap[i] = Aq + (t0 + i * 16 < T ? t0 + i * 16 : t0) / 16 * blk + lane * 16;
 
     v4f acc[NT];
 #pragma unroll
@@ -361,7 +384,7 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
         for (int i = 0; i < NT; ++i) {
             const uint8_t* const x = ap[i] + kb * 2048;
             const v8i a = join(*reinterpret_cast<const uint4*>(x), *reinterpret_cast<const uint4*>(x + 1024));
-            const float s = As[kb * t_ld + i * 16 + r] * sb;
+            const float s = As[kb * t_ld + min(t0 + i * 16 + r, t_ld - 1)] * sb;
             v4f t = v4f{0, 0, 0, 0};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -376,18 +399,19 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
         *reinterpret_cast<v4f*>(red + (wave * NT * 16 + i * 16 + r) * LD + 4 * g) = acc[i];
     __syncthreads();
     if (tid >= NT * 64) return;
-    const int tok = tid >> 2, c = tid & 3;
+    const int c = tid & 3;
+    const int64_t tok = t0 + (tid >> 2);
     v4f y = v4f{0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-        const v4f v = *reinterpret_cast<const v4f*>(red + (w * NT * 16 + tok) * LD + 4 * c);
+        const v4f v = *reinterpret_cast<const v4f*>(red + (w * NT * 16 + (tid >> 2)) * LD + 4 * c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] += v[e];
     }
     if (tok >= T) return;
     const int64_t n = n0 + 4 * c;
     if constexpr (OUT == W4A4_Y_F32) {
-        float* const Y = reinterpret_cast<float*>(out) + (int64_t)tok * N + n;
+        float* const Y = reinterpret_cast<float*>(out) + tok * N + n;
         if (vec_store && n + 3 < N) {
             *reinterpret_cast<v4f*>(Y) = y;
         } else {
@@ -396,7 +420,7 @@ __global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict
                 if (n + e < N) Y[e] = y[e];
         }
     } else {
-        uint16_t* const Y = reinterpret_cast<uint16_t*>(out) + (int64_t)tok * N + n;
+        uint16_t* const Y = reinterpret_cast<uint16_t*>(out) + tok * N + n;
         const uint32_t lo = pk_bf16(y[0], y[1]), hi = pk_bf16(y[2], y[3]);
         if (vec_store && n + 3 < N) {
             *reinterpret_cast<uint2*>(Y) = make_uint2(lo, hi);
@@ -419,7 +443,7 @@ hipError_t run_tiles(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld
                        0, st, aq, as, T, t_ld, d.codes, d.scales, d.d_out, d.k_pad / 128, out, vec, sp);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !tail) return e;
-    hipLaunchKernelGGL((fp8_reduce_kernel<FT, FF, WT, WF, OUT>), dim3((uint32_t)(tail * WT * WF)), dim3(64), 0, st, T, d.d_out, out,
+    hipLaunchKernelGGL((fp8_reduce_kernel<FT, FF, WT, WF, OUT>), dim3((uint32_t)(tail * WT * WF * (FT / 2))), dim3(64), 0, st, T, d.d_out, out,
                        vec, sp);
     return hipGetLastError();
 }
@@ -435,7 +459,7 @@ hipError_t run_many(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld,
 template <int NT, int OUT>
 hipError_t run_few(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
                    hipStream_t st) {
-    hipLaunchKernelGGL((fp8_gemv_kernel<NT, OUT>), dim3((uint32_t)((d.d_out + 15) / 16)), dim3(512), 0, st, aq, as, T, t_ld,
+    hipLaunchKernelGGL((fp8_gemv_kernel<NT, OUT>), dim3((uint32_t)((d.d_out + 15) / 16), (uint32_t)((T + NT * 16 - 1) / (NT * 16))), dim3(512), 0, st, aq, as, T, t_ld,
                        d.codes, d.scales, d.d_out, d.k_pad / 128, out, d.d_out % 4 == 0 ? 1 : 0);
     return hipGetLastError();
 }
@@ -445,7 +469,7 @@ hipError_t run_out(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, 
                    hipStream_t st) {
     if (T <= 16) return run_few<1, OUT>(aq, as, T, t_ld, d, out, st);
     if (T <= 32) return run_few<2, OUT>(aq, as, T, t_ld, d, out, st);
-    if (T <= FP8_FEW) return run_few<4, OUT>(aq, as, T, t_ld, d, out, st);
+    if (fp8_few(T, d.d_out, d.k_pad)) return run_few<4, OUT>(aq, as, T, t_ld, d, out, st);
     if constexpr (OUT == W4A4_Y_F32) return run_many<MUL_BF16, OUT>(aq, as, T, t_ld, d, out, part, st);
     else if (d.scale_kind == W4A4_FP8_SCALE_F32) return run_many<MUL_FP8, OUT>(aq, as, T, t_ld, d, out, part, st);
     else return run_many<MUL_FP8_E8M0, OUT>(aq, as, T, t_ld, d, out, part, st);
@@ -458,7 +482,7 @@ hipError_t run_out(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, 
 // are free CUs, at least MIN_BLOCKS blocks each.
 Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t k_pad) {
     Fp8Plan p = {0, 0, 1, false, 0};
-    if (T <= FP8_FEW) return p;
+    if (fp8_few(T, N, k_pad)) return p;
     constexpr int64_t CUS = 256, MIN_BLOCKS = 4, MAX_SPLIT = 16;
     const int64_t nkb = k_pad / 128, big = ((T + 255) / 256) * ((N + 255) / 256);
     p.big = big >= 64;

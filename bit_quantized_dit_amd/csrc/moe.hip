@@ -16,7 +16,7 @@
 // No kernel waits for another workgroup and nothing is added by atomics: who chose what is
 // recomputed where it is needed by counting, for one expert, how many experts rank before
 // it (a total order, so every token's ranks 0 .. top_k - 1 are taken exactly once).
-#include "w4a4_device.h"
+#include "fp8_device.h"
 #include "w4a4_internal.h"
 
 namespace w4a4 {
@@ -40,11 +40,11 @@ __device__ __forceinline__ bool before(uint32_t k2, int e2, uint32_t k, int e) {
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ void load8(const float* p, float* v) {
+__device__ __forceinline__ void row8(const float* p, float* v) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
+__device__ __forceinline__ void row8(const uint16_t* p, float* v) {
     const uint4 a = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const X* __restrict__ x
             const X* const r = x + (int64_t)t * d;
             float v[8];
             if (vec && p + 8 <= d) {
-                load8(r + p, v);
+                row8(r + p, v);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = p + q < d ? load1(r + p + q) : 0.0f;
@@ -104,10 +104,10 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const X* __restrict__ x
         for (int p = tid * 8; p < d; p += 2048) {
             float a[LE][8], b[8];
 #pragma unroll
-            for (int j = 0; j < LE; ++j) load8(wr[j] + p, a[j]);
+            for (int j = 0; j < LE; ++j) row8(wr[j] + p, a[j]);
 #pragma unroll
             for (int i = 0; i < LT; ++i) {
-                load8(xr[i] + p, b);
+                row8(xr[i] + p, b);
 #pragma unroll
                 for (int j = 0; j < LE; ++j)
 #pragma unroll
@@ -144,24 +144,6 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const X* __restrict__ x
 struct Codes {
     uint4 lo, hi;   // a lane's 32 codes of one block
 };
-// Buffer loads: a uniform descriptor, a lane offset that stays in one register for a whole stream
-// and a uniform offset that walks it (flat addresses cost two registers a load in flight).
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-__device__ __forceinline__ Rsrc rsrc(const void* p, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ uint4 load_at(Rsrc p, uint32_t lane_off, uint32_t off) {
-    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(p, (int)lane_off, (int)off, 0));
-}
-// The same for codes, which a call reads once: marked non-temporal, they do not push what is read
-// again (tokens, h, routing) out of the L2 (up step of 64 tokens, 64 experts of 5120 x 1536: 190 to
-// 176 us).
-__device__ __forceinline__ uint4 load_once(Rsrc p, uint32_t lane_off, uint32_t off) {
-    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(p, (int)lane_off, (int)off, 2));
-}
-// Added to the lane offset of a load that nothing needs: past every descriptor's range (which is
-// below 2^30 bytes), it reads zeros and no memory.
-constexpr uint32_t NO_LOAD = 0x80000000u;
 // (16 rows x 128 inputs of codes) . (128 inputs x 16 tokens); x: this lane's four pieces of its
 // token.
 __device__ __forceinline__ v4f block_mma(const Codes& c, const uint4* x) {
@@ -236,7 +218,7 @@ __device__ __forceinline__ void stream_blocks(v4f (&acc)[NM][NT], const uint8_t*
     auto load_scales = [&](int i) __attribute__((always_inline)) {   // of blocks i .. i + D - 1, one a lane
         const uint32_t at = i + lane < n && lane < D ? (uint32_t)(kb0 + (i + lane) * step) * 4u : NO_LOAD;
 #pragma unroll
-        for (int m = 0; m < NM; ++m) next[m] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr[m], (int)at, 0, 0));
+        for (int m = 0; m < NM; ++m) next[m] = load_word(sr[m], at);
     };
     load_scales(0);
 #pragma unroll
@@ -602,7 +584,7 @@ __global__ __launch_bounds__(W * 64, TB < MAX_T ? 4 : 2) void moe_down_kernel(Do
         };
         auto load_scales = [&]() __attribute__((always_inline)) {   // of the group, one a lane
             const uint32_t at = lane < D && lkb + lane < nkb ? (uint32_t)(lkb + lane) * 4u : NO_LOAD;
-            next = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr, (int)at, 0, 0));
+            next = load_word(sr, at);
         };
         open(seg);
         load_scales();

@@ -352,8 +352,8 @@ int w4a4_linear_noalloc(const void* X, int x_dtype, int64_t T, const w4a4_packed
  *     output that reads the block is NaN).  A zero block has s = 2^-60.
  *   - Codes: e4m3_rne(fl32(x / s)), nearest, ties to the even mantissa, signs kept.
  *   - Sums, and the products with the scales, are binary32, and fp32 outputs are those
- *     sums.  For bf16 outputs of more than 64 tokens the matrix instructions take the codes
- *     as FP8 and drop what is 13 bits below the largest product beside it: 1.4e-5 to 4e-5
+ *     sums.  For bf16 outputs of more than 64 tokens the matrix instructions may take the
+ *     codes as FP8 and drop what is 13 bits below the largest product beside it: 1.4e-5 to 4e-5
  *     of a sum, a fiftieth of the outputs' own rounding.  The product of two scales
  *     s_x s_w is taken first: with scales of a checkpoint it has to be a normal number.
  *   - The inputs are zero padded to k_pad = roundup(d_in, 128); 1 <= d_in <=
@@ -423,8 +423,7 @@ int w4a4_fp8_quantize_activations(const void* X, int x_dtype, int64_t T, const w
  * fp32 sums rounded once to nearest even): y_dtype is W4A4_Y_F32 or W4A4_Y_BF16.  Async. */
 int w4a4_fp8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_fp8_packed* desc,
                                void* Y, int y_dtype, void* stream);
-/* Both.  Async.  (The codes and scales of X may stay out of ws where the product takes
- * them as it computes them.) */
+/* Both.  Async. */
 int w4a4_fp8_linear(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc, void* Y,
                     int y_dtype, void* ws, size_t ws_bytes, void* stream);
 

@@ -40,11 +40,14 @@ def _run(x, xt, w, kind, yt, stream=None):
     layer = B.w4a4_fp8_pack_weights(W, kind)
     ws = torch.full((max(B.w4a4_fp8_workspace_size(T, layer), 256) + 512,), 255, dtype=torch.uint8, device="cuda")
     buf, Y = _guarded(np.zeros((T, n), np.float32), yt, 7.0)
+    B.w4a4_fp8_quantize_activations(X, layer, ws[:-512])
+    v = {n: t.cpu().numpy() for n, t in B.workspace_fp8_views(ws, T, layer).items()}
+    ws.fill_(255)      # the one call may keep the codes of a few tokens out of the workspace
     B.w4a4_fp8_linear(X, layer, Y, ws[:-512])
     torch.cuda.synchronize()
     assert bool((ws[-512:] == 255).all()) and bool((buf[:256] == 7).all()) and bool((buf[256 + T * n:] == 7).all())
-    v, p = B.workspace_fp8_views(ws, T, layer), layer.views()
-    return v["A_q"].cpu().numpy(), v["A_s"].cpu().numpy(), Y.double().cpu().numpy(), p["codes"][0].cpu().numpy(), p["scales"][0].cpu().numpy()
+    p = layer.views()
+    return v["A_q"], v["A_s"], Y.double().cpu().numpy(), p["codes"][0].cpu().numpy(), p["scales"][0].cpu().numpy()
 
 
 def _check(x, xt, w, kind, yt):
