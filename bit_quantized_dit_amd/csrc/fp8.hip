@@ -14,9 +14,9 @@ namespace {
 // The 16 values of one 16-byte piece of the packed order: inputs p .. + 7 and p + 32 .. + 39
 // (p = 64 half + 8 chunk of the block).
 template <typename X>
-__device__ __forceinline__ void load_piece(const X* row, int64_t p, int64_t cols, bool vec, float* x) {
-    load8(row, p, cols, vec, x);
-    load8(row, p + 32, cols, vec, x + 8);
+__device__ __forceinline__ void load_piece(const X* row, int64_t p, int64_t cols, float* x) {
+    load8(row, p, cols, x);
+    load8(row, p + 32, cols, x + 8);
 }
 
 template <typename Inv>
@@ -30,7 +30,7 @@ __device__ __forceinline__ uint4 encode_piece(const float* x, float s, const Inv
 // 32 q + 8 (l / 16) .. + 7), so that the two stores write one KiB each.
 template <typename X>
 __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__ x, int64_t T, int64_t d_in, int64_t nkb,
-                                                           int64_t items, int kind, int vec, uint8_t* __restrict__ aq,
+                                                           int64_t items, int kind, uint8_t* __restrict__ aq,
                                                            float* __restrict__ as, int64_t t_ld) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__
     float v[2][16];
     uint32_t m = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) load_piece(row, kb * 128 + h * 64 + g * 8, d_in, vec != 0, v[h]);
+    for (int h = 0; h < 2; ++h) load_piece(row, kb * 128 + h * 64 + g * 8, d_in, v[h]);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__
 // Weights: one workgroup per 128 x 128 block; thread = (row, half of the block's inputs).
 template <typename W>
 __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, int64_t d_in, int64_t d_out, int64_t nkb,
-                                                       int64_t nnb, int64_t n_pad, int kind, int vec, uint8_t* __restrict__ codes,
+                                                       int64_t nnb, int64_t n_pad, int kind, uint8_t* __restrict__ codes,
                                                        float* __restrict__ scales) {
     __shared__ uint32_t wmax[4];
     const int64_t b = blockIdx.x;
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (row < d_out) {
-            load_piece(w + (mat * d_out + row) * d_in, p0 + 8 * i, d_in, vec != 0, v[i]);
+            load_piece(w + (mat * d_out + row) * d_in, p0 + 8 * i, d_in, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
@@ -146,11 +146,9 @@ hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_
     const int64_t nkb = (d_in + 127) / 128, items = (T + 15) / 16 * nkb;
     const dim3 grid((uint32_t)((items + 3) / 4));
     if (x_dtype == W4A4_X_BF16)
-        hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, items,
-                           kind, d_in % 8 == 0 ? 1 : 0, aq, as, t_ld);
+        hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, items, kind, aq, as, t_ld);
     else
-        hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, items, kind,
-                           d_in % 4 == 0 ? 1 : 0, aq, as, t_ld);
+        hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, items, kind, aq, as, t_ld);
     return hipGetLastError();
 }
 
@@ -160,10 +158,10 @@ hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d,
     const dim3 grid((uint32_t)(d.n_mat * nnb * nkb));
     if (w_dtype == W4A4_X_BF16)
         hipLaunchKernelGGL(fp8_pack_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)W, d.d_in, d.d_out, nkb, nnb,
-                           d.n_pad, d.scale_kind, d.d_in % 8 == 0 ? 1 : 0, codes, scales);
+                           d.n_pad, d.scale_kind, codes, scales);
     else
         hipLaunchKernelGGL(fp8_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)W, d.d_in, d.d_out, nkb, nnb,
-                           d.n_pad, d.scale_kind, d.d_in % 4 == 0 ? 1 : 0, codes, scales);
+                           d.n_pad, d.scale_kind, codes, scales);
     return hipGetLastError();
 }
 

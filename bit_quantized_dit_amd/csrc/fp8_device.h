@@ -53,28 +53,30 @@ __device__ __forceinline__ uint2 encode8(const float* x, float s, const Inv& inv
     return make_uint2(w[0], w[1]);
 }
 
-// Values p .. p + 7 of a row of `cols`, zero past its end; `vec`: the row starts on a
-// 16-byte boundary (p is a multiple of 8).
-__device__ __forceinline__ void load8(const float* row, int64_t p, int64_t cols, bool vec, float* x) {
-    if (vec && p + 8 <= cols) {
+// Values p .. p + 7 of a row of `cols`, zero past its end.  Rows of any alignment: the loads are
+// marked as aligned to an element only (the hardware takes unaligned vector loads).
+__device__ __forceinline__ void load8(const float* row, int64_t p, int64_t cols, float* x) {
+    typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
+    if (p + 8 <= cols) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(row + p + 4 * i);
-            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+            const v4 v = *reinterpret_cast<const v4*>(row + p + 4 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * i + j] = v[j];
         }
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = p + i < cols ? row[p + i] : 0.0f;
 }
-__device__ __forceinline__ void load8(const uint16_t* row, int64_t p, int64_t cols, bool vec, float* x) {
-    if (vec && p + 8 <= cols) {
-        const uint4 v = *reinterpret_cast<const uint4*>(row + p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void load8(const uint16_t* row, int64_t p, int64_t cols, float* x) {
+    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+    if (p + 8 <= cols) {
+        const v4 v = *reinterpret_cast<const v4*>(row + p);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            x[2 * j] = __uint_as_float(v[j] << 16);
+            x[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
         }
         return;
     }
