@@ -123,6 +123,9 @@ w4a4_moe_ws_layout moe_layout(int64_t T, const w4a4_moe* m) {
     w.ids = off;    off = align_up(off + (size_t)pairs * 4);
     w.p = off;      off = align_up(off + (size_t)pairs * 4);
     w.h = off;      off = align_up(off + (size_t)(pairs * m->down.k_pad) * 2);
+    w.place = off;  off = align_up(off + (size_t)pairs * 4);
+    w.count = off;  off = align_up(off + (size_t)((m->down.d_out + 15) / 16) * 4);
+    w.part = off;   off = align_up(off + (size_t)T * (2 * 512 * 16 * 4));   // two of 16 outputs for each of 512 workgroups
     w.total = off;
     return w;
 }
@@ -245,6 +248,9 @@ int w4a4_moe_forward(const void* X, int x_dtype, int64_t T, const w4a4_moe* moe,
     m.p = (float*)(b + w.p);
     m.xb = (uint16_t*)(b + w.xb);
     m.h = (uint16_t*)(b + w.h);
+    m.part = (float*)(b + w.part);
+    m.place = (int32_t*)(b + w.place);
+    m.count = (int32_t*)(b + w.count);
     m.ids = (int32_t*)(b + w.ids);
     return dev_status(launch_moe(X, x_dtype, T, *moe, m, Y, y_dtype, (hipStream_t)stream));
 }

@@ -65,11 +65,13 @@ constexpr int LE = 2;   // experts per workgroup
 template <int LT, typename X, typename R>
 __global__ __launch_bounds__(256) void moe_logits_kernel(const X* __restrict__ x, const R* __restrict__ router, int T, int d,
                                                          int d_pad, int E, int vec, float* __restrict__ logits,
-                                                         uint16_t* __restrict__ xb) {
+                                                         uint16_t* __restrict__ xb, int32_t* __restrict__ count) {
     __shared__ float part[4][LE * LT];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int t0 = blockIdx.y * LT;
     const int ne = (E + LE - 1) / LE;
+    if (blockIdx.x + blockIdx.y == 0)   // the down step's counters
+        for (int i = tid; i < (d + 15) / 16; i += 256) count[i] = 0;
     if ((int)blockIdx.x >= ne) {
         const int p = ((int)blockIdx.x - ne) * 2048 + tid * 8;
         if (p >= d_pad) return;
@@ -274,7 +276,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 struct UpArgs {
     const float* logits;
     const uint16_t* xb;
-    int32_t* ids;
+    int32_t *ids, *place;
     float* p;
     uint16_t* h;
     int T, E, k, renorm, f, by_slot;
@@ -450,6 +452,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
             }
             if ((tid & 7) == 0) {
                 a.ids[pair] = e;
+                a.place[pair] = q;
                 a.p[pair] = v;
             }
         }
@@ -459,7 +462,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 ? 4 : NT == 2 ? 3 : 2) void moe
 // ---------------------------------------------------------------- 3. down
 
 struct DownArgs {
-    const int32_t* ids;
+    const int32_t *ids, *place;
     const float* p;
     const uint16_t* h;
     int T, E, k, renorm, d, y_dtype;
@@ -468,7 +471,23 @@ struct DownArgs {
     const float* scales;
     int64_t mat_codes, mat_scales;
     void* out;
+    float* part;                             // [two a workgroup][T][16 RT]
+    int32_t* count;                          // by tile of 16 RT outputs: parts that are done
 };
+
+__device__ __forceinline__ void store_y(const DownArgs& a, int t, int row, float y) {
+    if (row >= a.d) return;
+    if (a.y_dtype == W4A4_Y_F32) reinterpret_cast<float*>(a.out)[(int64_t)t * a.d + row] = y;
+    else reinterpret_cast<uint16_t*>(a.out)[(int64_t)t * a.d + row] = bf16_rne(y);
+}
+
+// Values that workgroups of different XCDs pass each other go past the XCDs' caches, value by value: a
+// release or acquire fence would write back or drop a whole L2 (and made these kernels up to 8
+// times slower).
+__device__ __forceinline__ void put_shared(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ float get_shared(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+constexpr int DOWN_MIN = 2;   // groups a wavefront, below which tiles stay whole
 
 // TB: tokens the sums are laid out for; RT: row tiles (16 outputs) of a workgroup.  The work is one sequence of groups of D blocks: segment by
 // segment (up to S tokens of one expert), the segment's nkb_f blocks, the last group of a segment cut
@@ -479,19 +498,18 @@ template <int TB, int W, int XI, int RT>
 __global__ __launch_bounds__(W * 64, TB < MAX_T ? 4 : 2) void moe_down_kernel(DownArgs a) {
     constexpr int S = tokens_of(XI), NX = XI == 4 ? 1 : XI, RL = 16 * RT;
     constexpr int PB = TB * W4A4_MOE_MAX_K, SEGS = W4A4_MOE_MAX_E + PB / S;
-    constexpr int D = XI == 1 ? 6 : XI == 2 ? 4 : 3;
+    constexpr int D = XI == 1 ? 6 : XI == 2 ? 4 : RT == 2 ? 2 : 3;
     __shared__ __attribute__((aligned(16))) float sums[W * TB * RL];
     __shared__ uint4 xs[XI == 4 ? 1 : W * XI * 64];
     __shared__ float den[TB], prob[PB];
     __shared__ uint16_t list[PB];              // pairs, expert by expert
-    __shared__ int32_t first[W4A4_MOE_MAX_E];  // by expert: pairs, then where its list goes on
+    __shared__ int32_t first[W4A4_MOE_MAX_E];  // by expert: pairs, then where its list starts
     __shared__ uint16_t seg_e[SEGS], seg_l[SEGS];   // by segment: expert, place in list
     __shared__ uint8_t seg_n[SEGS];                 // its tokens
-    __shared__ int n_seg;
+    __shared__ int n_seg, done;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row0 = blockIdx.x * RL, pairs = a.T * a.k, nkb = a.nkb_f;
-    for (int i = tid; i < W * TB * RL; i += W * 64) sums[i] = 0.0f;
+    const int pairs = a.T * a.k, nkb = a.nkb_f;
     if (a.T == 1) {   // every pair is a segment
         for (int i = tid; i < pairs; i += W * 64) {
             prob[i] = a.p[i];
@@ -534,9 +552,7 @@ __global__ __launch_bounds__(W * 64, TB < MAX_T ? 4 : 2) void moe_down_kernel(Do
             if (lane == 0) n_seg = seg;
         }
         __syncthreads();
-        // in the order in which the lanes arrive: it decides the matrix column that a token takes,
-        // which changes no value
-        for (int i = tid; i < pairs; i += W * 64) list[atomicAdd(&first[a.ids[i]], 1)] = (uint16_t)i;
+        for (int i = tid; i < pairs; i += W * 64) list[first[a.ids[i]] + a.place[i]] = (uint16_t)i;
     }
     for (int t = tid; t < a.T; t += W * 64) {
         float s = 1.0f;
@@ -549,121 +565,153 @@ __global__ __launch_bounds__(W * 64, TB < MAX_T ? 4 : 2) void moe_down_kernel(Do
     __syncthreads();
 
     const int groups = (nkb + D - 1) / D;          // of a segment
-    const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(n_seg) * groups;
-    const int begin = (int)(total * wave / W), len = (int)(total * (wave + 1) / W) - begin;
-    const int tiles = (a.d + 15) / 16 - blockIdx.x * RT < RT ? (a.d + 15) / 16 - blockIdx.x * RT : RT;
-    float* const mine = sums + wave * TB * RL;
-    if (len > 0) {
-        int seg = begin / groups, lkb = (begin - seg * groups) * D;   // the group that is loaded
-        const Rsrc xr = rsrc(a.h, (uint32_t)pairs * (uint32_t)nkb * 256u);
-        Rsrc wr, sr;
-        uint32_t xoff[NX];
-        auto open = [&](int sg) __attribute__((always_inline)) {
-            const int e = __builtin_amdgcn_readfirstlane(seg_e[sg]), n = __builtin_amdgcn_readfirstlane(seg_n[sg]);
-            wr = rsrc(a.codes + (int64_t)e * a.mat_codes + (int64_t)blockIdx.x * RT * nkb * 2048, (uint32_t)tiles * nkb * 2048u);
-            sr = rsrc(a.scales + (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * nkb, (uint32_t)nkb * 4u);
-            // rows past the segment's tokens read the first one's h
-#pragma unroll
-            for (int i = 0; i < NX; ++i) {
-                const int q = XI == 4 ? r : i * 4 + g;
-                xoff[i] = (uint32_t)list[seg_l[sg] + (q < n ? q : 0)] * (uint32_t)nkb * 256u + (XI == 4 ? g : r) * 16;
-            }
-        };
-        Codes w[D][RT];
-        uint4 x[D][XI];
-        float sc, next;
-        auto load = [&](int j) __attribute__((always_inline)) {
-            const uint32_t b = (uint32_t)(lkb + j), off = lkb + j < nkb ? 0 : NO_LOAD;
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const uint32_t at = off + lane * 16 + t * (uint32_t)nkb * 2048u;
-                w[j][t] = Codes{load_once(wr, at, b * 2048u), load_once(wr, at + 1024, b * 2048u)};
-            }
-#pragma unroll
-            for (int q = 0; q < XI; ++q) x[j][q] = load_at(xr, XI == 4 ? xoff[0] + off + q * 64 : xoff[q] + off, b * 256u);
-        };
-        auto load_scales = [&]() __attribute__((always_inline)) {   // of the group, one a lane
-            const uint32_t at = lane < D && lkb + lane < nkb ? (uint32_t)(lkb + lane) * 4u : NO_LOAD;
-            next = load_word(sr, at);
-        };
-        open(seg);
-        load_scales();
-#pragma unroll
-        for (int j = 0; j < D; ++j) {
-            load(j);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        v4f acc[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] = v4f{0, 0, 0, 0};
-        for (int i = 0; i < len; ++i) {
-            const int kb = lkb, sg = seg;          // the group that is used
-            lkb += D;
-            const bool ends = lkb >= nkb;
-            if (i + 1 == len) {
-                lkb = nkb;                         // nothing left to load
-            } else if (ends) {
-                lkb = 0;
-                open(++seg);
-            }
-            sc = next;
-            load_scales();
-#pragma unroll
-            for (int j = 0; j < D; ++j) {
-                const bool in = kb + j < nkb;      // uniform; past the end the sums stay as they are
-                uint4 op[4];
-                spread<XI>(op, x[j], xs + wave * XI * 64);
-                const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sc), j));
-#pragma unroll
+    // all groups of all tiles, dealt evenly; 32 bits hold them (4096 tiles, 1500 segments, 171 groups)
+    const int per = __builtin_amdgcn_readfirstlane(n_seg) * groups, tiles = (a.d + RL - 1) / RL, all = tiles * per;
+    const int wgs = min(max(tiles, all / (DOWN_MIN * W)), (int)gridDim.x), q = blockIdx.x;
+    if (q >= wgs) return;
+    const int share = all / wgs, extra = all - share * wgs;   // the first `extra` workgroups take one more
+    auto start = [&](int u) { return share * u + min(u, extra); };
+    auto owner = [&](int x) { return x < extra * (share + 1) ? x / (share + 1) : extra + (x - extra * (share + 1)) / share; };
+    const int q_at = start(q), q_end = start(q + 1);
+    for (int at = q_at; at < q_end;) {
+        const int tile = at / per, stop = min(q_end, (tile + 1) * per);
+        const int row0 = tile * RL, from = at - tile * per, size = stop - at;
+        const int begin = from + size * wave / W, len = from + size * (wave + 1) / W - begin;
+        const int rts = min((a.d + 15) / 16 - tile * RT, RT);
+        float* const mine = sums + wave * TB * RL;
+        for (int i = lane; i < TB * RL; i += 64) mine[i] = 0.0f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (len > 0) {
+            int seg = begin / groups, lkb = (begin - seg * groups) * D;   // the group that is loaded
+            const Rsrc xr = rsrc(a.h, (uint32_t)pairs * (uint32_t)nkb * 256u);
+            Rsrc wr, sr;
+            uint32_t xoff[NX];
+            auto open = [&](int sg) __attribute__((always_inline)) {
+                const int e = __builtin_amdgcn_readfirstlane(seg_e[sg]), n = __builtin_amdgcn_readfirstlane(seg_n[sg]);
+                wr = rsrc(a.codes + (int64_t)e * a.mat_codes + (int64_t)tile * RT * nkb * 2048, (uint32_t)rts * nkb * 2048u);
+                sr = rsrc(a.scales + (int64_t)e * a.mat_scales + (int64_t)(row0 / 128) * nkb, (uint32_t)nkb * 4u);
+                // rows past the segment's tokens read the first one's h
+    #pragma unroll
+                for (int i = 0; i < NX; ++i) {
+                    const int q = XI == 4 ? r : i * 4 + g;
+                    xoff[i] = (uint32_t)list[seg_l[sg] + (q < n ? q : 0)] * (uint32_t)nkb * 256u + (XI == 4 ? g : r) * 16;
+                }
+            };
+            Codes w[D][RT];
+            uint4 x[D][XI];
+            float sc, next;
+            auto load = [&](int j) __attribute__((always_inline)) {
+                const uint32_t b = (uint32_t)(lkb + j), off = lkb + j < nkb ? 0 : NO_LOAD;
+    #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const v4f v = block_mma(w[j][t], op);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[t][q] = in ? __builtin_fmaf(v[q], s, acc[t][q]) : acc[t][q];
+                    const uint32_t at = off + lane * 16 + t * (uint32_t)nkb * 2048u;
+                    w[j][t] = Codes{load_once(wr, at, b * 2048u), load_once(wr, at + 1024, b * 2048u)};
                 }
+    #pragma unroll
+                for (int q = 0; q < XI; ++q) x[j][q] = load_at(xr, XI == 4 ? xoff[0] + off + q * 64 : xoff[q] + off, b * 256u);
+            };
+            auto load_scales = [&]() __attribute__((always_inline)) {   // of the group, one a lane
+                const uint32_t at = lane < D && lkb + lane < nkb ? (uint32_t)(lkb + lane) * 4u : NO_LOAD;
+                next = load_word(sr, at);
+            };
+            open(seg);
+            load_scales();
+    #pragma unroll
+            for (int j = 0; j < D; ++j) {
                 load(j);
-                __builtin_amdgcn_sched_barrier(0);   // each block waits for its own loads only
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (ends || i + 1 == len) {            // the segment, or the wavefront's part of it, ends
-                if (r < seg_n[sg]) {               // tokens of one expert are distinct: no two lanes meet
-                    const int pair = list[seg_l[sg] + r], t = pair / a.k;
-                    const float pw = a.renorm ? prob[pair] / den[t] : prob[pair];
-#pragma unroll
-                    for (int u = 0; u < RT; ++u) {
-                        v4f* const s = reinterpret_cast<v4f*>(mine + t * RL + u * 16 + 4 * g);
-                        v4f v = *s;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(acc[u][q], pw, v[q]);
-                        *s = v;
-                    }
+            v4f acc[RT];
+    #pragma unroll
+            for (int t = 0; t < RT; ++t) acc[t] = v4f{0, 0, 0, 0};
+            for (int i = 0; i < len; ++i) {
+                const int kb = lkb, sg = seg;          // the group that is used
+                lkb += D;
+                const bool ends = lkb >= nkb;
+                if (i + 1 == len) {
+                    lkb = nkb;                         // nothing left to load
+                } else if (ends) {
+                    lkb = 0;
+                    open(++seg);
                 }
-#pragma unroll
-                for (int u = 0; u < RT; ++u) acc[u] = v4f{0, 0, 0, 0};
+                sc = next;
+                load_scales();
+    #pragma unroll
+                for (int j = 0; j < D; ++j) {
+                    const bool in = kb + j < nkb;      // uniform; past the end the sums stay as they are
+                    uint4 op[4];
+                    spread<XI>(op, x[j], xs + wave * XI * 64);
+                    const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sc), j));
+    #pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        const v4f v = block_mma(w[j][t], op);
+    #pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[t][q] = in ? __builtin_fmaf(v[q], s, acc[t][q]) : acc[t][q];
+                    }
+                    load(j);
+                    __builtin_amdgcn_sched_barrier(0);   // each block waits for its own loads only
+                }
+                if (ends || i + 1 == len) {            // the segment, or the wavefront's part of it, ends
+                    if (r < seg_n[sg]) {               // tokens of one expert are distinct: no two lanes meet
+                        const int pair = list[seg_l[sg] + r], t = pair / a.k;
+                        const float pw = a.renorm ? prob[pair] / den[t] : prob[pair];
+    #pragma unroll
+                        for (int u = 0; u < RT; ++u) {
+                            v4f* const s = reinterpret_cast<v4f*>(mine + t * RL + u * 16 + 4 * g);
+                            v4f v = *s;
+    #pragma unroll
+                            for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(acc[u][q], pw, v[q]);
+                            *s = v;
+                        }
+                    }
+    #pragma unroll
+                    for (int u = 0; u < RT; ++u) acc[u] = v4f{0, 0, 0, 0};
+                }
             }
         }
-    }
-    __syncthreads();
-    for (int i = tid; i < a.T * RL; i += W * 64) {
-        const int t = i / RL, row = row0 + i % RL;
-        if (row >= a.d) continue;
-        float y = 0.0f;
+        __syncthreads();
+        const bool whole = size == per;
+        // the first of the workgroup's parts, or the last one
+        float* const part = a.part + (2 * q + (at != q_at)) * a.T * RL;
+        for (int i = tid; i < a.T * RL; i += W * 64) {
+            float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) y += sums[w * TB * RL + i];
-        if (a.y_dtype == W4A4_Y_F32) reinterpret_cast<float*>(a.out)[(int64_t)t * a.d + row] = y;
-        else reinterpret_cast<uint16_t*>(a.out)[(int64_t)t * a.d + row] = bf16_rne(y);
+            for (int w = 0; w < W; ++w) y += sums[w * TB * RL + i];
+            if (whole) store_y(a, i / RL, row0 + i % RL, y);
+            else put_shared(part + i, y);
+        }
+        if (!whole) {
+            const int q0 = owner(tile * per), q1 = owner((tile + 1) * per - 1);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this part is where every XCD sees it
+            __syncthreads();
+            if (tid == 0) done = __hip_atomic_fetch_add(a.count + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (done == q1 - q0) {          // the last part to be done adds them all, in order
+                const float* const p0 = a.part + (2 * q0 + (start(q0) < tile * per)) * a.T * RL;
+                for (int i = tid; i < a.T * RL; i += W * 64) {
+                    float y = get_shared(p0 + i);
+                    for (int u = q0 + 1; u <= q1; ++u) y += get_shared(a.part + 2 * u * a.T * RL + i);
+                    store_y(a, i / RL, row0 + i % RL, y);
+                }
+            }
+        }
+        __syncthreads();
+        at = stop;
     }
 }
 
 template <int LT, typename X>
-void run_logits(const void* X_, const w4a4_moe& m, int T, bool copy, float* logits, uint16_t* xb, hipStream_t st) {
+void run_logits(const void* X_, const w4a4_moe& m, int T, bool copy, float* logits, uint16_t* xb, int32_t* count, hipStream_t st) {
     const int d = (int)m.up.d_in, d_pad = (int)m.up.k_pad, E = (int)m.up.n_mat;
     const dim3 grid((uint32_t)((E + LE - 1) / LE + (copy ? (d_pad + 2047) / 2048 : 0)), (uint32_t)((T + LT - 1) / LT));
     const int vec = d % 8 == 0 ? 1 : 0;
     if (m.router_dtype == W4A4_X_BF16)
         hipLaunchKernelGGL((moe_logits_kernel<LT, X, uint16_t>), grid, dim3(256), 0, st, (const X*)X_, (const uint16_t*)m.router, T,
-                           d, d_pad, E, vec, logits, xb);
+                           d, d_pad, E, vec, logits, xb, count);
     else
         hipLaunchKernelGGL((moe_logits_kernel<LT, X, float>), grid, dim3(256), 0, st, (const X*)X_, (const float*)m.router, T, d,
-                           d_pad, E, vec, logits, xb);
+                           d_pad, E, vec, logits, xb, count);
 }
 
 // Tokens of an expert that a pass over its codes takes (xi and, above 16, nt tiles), from the number
@@ -690,22 +738,22 @@ void run_up(const UpArgs& a, Pass p, dim3 grid, hipStream_t st) {
     else hipLaunchKernelGGL((moe_up_kernel<GATED, 4, 4>), grid, block, 0, st, a);
 }
 
+// One workgroup of 16 wavefronts or two of 8 fit a CU.
+template <int TB, int W, int XI, int RT>
+void down(const DownArgs& a, int wgs, hipStream_t st) {
+    hipLaunchKernelGGL((moe_down_kernel<TB, W, XI, RT>), dim3((uint32_t)wgs), dim3(W * 64), 0, st, a);
+}
 template <int XI>
 void run_down(const DownArgs& a, hipStream_t st) {
-    // 16 wavefronts fit a CU at this kernel's registers: one workgroup of 16, or two of 8 where one
-    // a CU would leave a second round
-    const uint32_t n = (uint32_t)((a.d + 15) / 16);
-    const bool wide = n <= 256;
-    if (a.T <= 16 && wide) hipLaunchKernelGGL((moe_down_kernel<16, 16, XI, 1>), dim3(n), dim3(1024), 0, st, a);
-    else if (a.T <= 16) hipLaunchKernelGGL((moe_down_kernel<16, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
-    else if (a.T <= 64 && wide) hipLaunchKernelGGL((moe_down_kernel<64, 16, XI, 1>), dim3(n), dim3(1024), 0, st, a);
-    else if constexpr (XI == 4) {
+    if (a.T <= 16) return down<16, 8, XI, 1>(a, 512, st);
+    if constexpr (XI == 4) {
         // two row tiles for one read of h, where its 16 tokens' rows are twice the codes of one (64
         // tokens, 6 of 64 experts, 1536 -> 5120: 145 to 120 us)
-        if (a.T <= 64) hipLaunchKernelGGL((moe_down_kernel<64, 16, XI, 2>), dim3((n + 1) / 2), dim3(1024), 0, st, a);
-        else hipLaunchKernelGGL((moe_down_kernel<MAX_T, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
-    } else if (a.T <= 64) hipLaunchKernelGGL((moe_down_kernel<64, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
-    else hipLaunchKernelGGL((moe_down_kernel<MAX_T, 8, XI, 1>), dim3(n), dim3(512), 0, st, a);
+        if (a.T <= 64 && a.d > 4096) return down<64, 16, XI, 2>(a, 256, st);
+        if (a.T <= 64) return down<64, 16, XI, 1>(a, 256, st);
+    }
+    if (a.T <= 64) return down<64, 8, XI, 1>(a, 512, st);
+    down<MAX_T, 8, XI, 1>(a, 256, st);
 }
 
 }  // namespace
@@ -715,18 +763,18 @@ hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, 
     // X itself serves the products where it is bf16 and its rows need no padding
     const bool copy = x_dtype != W4A4_X_BF16 || m.up.d_in != m.up.k_pad;
     if (x_dtype == W4A4_X_BF16) {
-        if (T == 1) run_logits<1, uint16_t>(X, m, (int)T, copy, b.logits, b.xb, st);
-        else run_logits<4, uint16_t>(X, m, (int)T, copy, b.logits, b.xb, st);
+        if (T == 1) run_logits<1, uint16_t>(X, m, (int)T, copy, b.logits, b.xb, b.count, st);
+        else run_logits<4, uint16_t>(X, m, (int)T, copy, b.logits, b.xb, b.count, st);
     } else {
-        if (T == 1) run_logits<1, float>(X, m, (int)T, copy, b.logits, b.xb, st);
-        else run_logits<4, float>(X, m, (int)T, copy, b.logits, b.xb, st);
+        if (T == 1) run_logits<1, float>(X, m, (int)T, copy, b.logits, b.xb, b.count, st);
+        else run_logits<4, float>(X, m, (int)T, copy, b.logits, b.xb, b.count, st);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 
     const bool gated = m.activation == W4A4_MOE_SILU_GATED;
     UpArgs u;
-    u.logits = b.logits; u.xb = copy ? b.xb : (const uint16_t*)X; u.ids = b.ids; u.p = b.p; u.h = b.h;
+    u.logits = b.logits; u.xb = copy ? b.xb : (const uint16_t*)X; u.ids = b.ids; u.place = b.place; u.p = b.p; u.h = b.h;
     u.T = (int)T; u.E = (int)m.up.n_mat; u.k = m.top_k; u.renorm = m.renormalize != 0; u.f = (int)m.up.d_out;
     u.by_slot = T * m.top_k < m.up.n_mat && m.up.n_mat <= SLOT_E ? 1 : 0;
     u.nkb_d = (int)(m.up.k_pad / 128); u.f_pad = (int)m.down.k_pad; u.n_pad = (int)m.up.n_pad;
@@ -746,12 +794,13 @@ hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, 
     if (e != hipSuccess) return e;
 
     DownArgs d;
-    d.ids = b.ids; d.p = b.p; d.h = b.h;
+    d.ids = b.ids; d.place = b.place; d.p = b.p; d.h = b.h;
     d.T = u.T; d.E = u.E; d.k = u.k; d.renorm = u.renorm; d.d = (int)m.down.d_out;
     d.nkb_f = (int)(m.down.k_pad / 128);
     d.codes = m.down.codes; d.scales = m.down.scales;
     d.mat_codes = m.down.n_pad * m.down.k_pad; d.mat_scales = (m.down.d_out + 127) / 128 * (m.down.k_pad / 128);
     d.out = Y;
+    d.part = b.part; d.count = b.count;
     d.y_dtype = y_dtype;
     if (pass.xi == 1) run_down<1>(d, st);
     else if (pass.xi == 2) run_down<2>(d, st);

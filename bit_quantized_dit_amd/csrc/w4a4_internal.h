@@ -93,9 +93,9 @@ hipError_t launch_fp8_gemm(const uint8_t* aq, const float* as, int64_t T, int64_
 
 // mixture of experts (moe.hip): the arrays of w4a4_moe_ws_layout
 struct MoeBuffers {
-    float *logits, *p;
+    float *logits, *p, *part;
     uint16_t *xb, *h;
-    int32_t* ids;
+    int32_t *ids, *place, *count;
 };
 hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, const MoeBuffers& b, void* Y, int y_dtype,
                       hipStream_t st);

@@ -94,7 +94,7 @@ class W4A4Moe(ctypes.Structure):
 
 class W4A4MoeWsLayout(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_size_t), ("xb", ctypes.c_size_t), ("ids", ctypes.c_size_t), ("p", ctypes.c_size_t),
-                ("h", ctypes.c_size_t), ("total", ctypes.c_size_t)]
+                ("h", ctypes.c_size_t), ("place", ctypes.c_size_t), ("count", ctypes.c_size_t), ("part", ctypes.c_size_t), ("total", ctypes.c_size_t)]
 
 
 class W4A4Error(RuntimeError):

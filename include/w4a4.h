@@ -472,6 +472,9 @@ typedef struct w4a4_moe_ws_layout {
                          when renormalize == 0 (otherwise the down step divides by the sum
                          over the row)                                                      */
     size_t h;         /* bf16 [T * top_k][roundup(f, 128)], zero padded                     */
+    size_t place;     /* int32 [T][top_k]: which of its expert's tokens it is, in their order */
+    size_t count;     /* int32 [roundup(d, 16) / 16]: the down step's parts that are done   */
+    size_t part;      /* fp32: their sums                                                   */
     size_t total;
 } w4a4_moe_ws_layout;
 int w4a4_moe_workspace_layout(int64_t T, const w4a4_moe* moe, w4a4_moe_ws_layout* out);
