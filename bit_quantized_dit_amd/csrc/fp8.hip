@@ -31,7 +31,9 @@ __device__ __forceinline__ uint4 encode_piece(const float* x, float s, const Inv
 template <typename X>
 __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__ x, int64_t T, int64_t d_in, int64_t nkb,
                                                            int64_t items, int kind, uint8_t* __restrict__ aq,
-                                                           float* __restrict__ as, int64_t t_ld) {
+                                                           float* __restrict__ as, int64_t t_ld, int32_t* __restrict__ count) {
+    if (count && blockIdx.x == 0)   // the product's counters
+        for (int i = threadIdx.x; i < FP8_COUNTERS; i += 256) count[i] = 0;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (item >= items) return;
@@ -142,13 +144,15 @@ __global__ __launch_bounds__(256) void fp8_scales_kernel(const void* __restrict_
 }  // namespace
 
 hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_in, int kind, uint8_t* aq, float* as,
-                               int64_t t_ld, hipStream_t st) {
+                               int64_t t_ld, int32_t* count, hipStream_t st) {
     const int64_t nkb = (d_in + 127) / 128, items = (T + 15) / 16 * nkb;
     const dim3 grid((uint32_t)((items + 3) / 4));
     if (x_dtype == W4A4_X_BF16)
-        hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, items, kind, aq, as, t_ld);
+        hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, items, kind, aq, as, t_ld,
+                           count);
     else
-        hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, items, kind, aq, as, t_ld);
+        hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, items, kind, aq, as, t_ld,
+                           count);
     return hipGetLastError();
 }
 

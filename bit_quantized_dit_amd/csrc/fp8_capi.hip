@@ -64,7 +64,9 @@ w4a4_fp8_ws_layout ws_layout(int64_t T, const w4a4_fp8_packed* d) {
     size_t off = 0;
     w.a_q = off;     off = align_up(off + (size_t)(round_up(T, 16) * d->k_pad));
     w.a_s = off;     off = align_up(off + (size_t)(d->k_pad / 128 * t_ld_of(T)) * 4);
-    w.partial = off; off = align_up(off + fp8_plan(T, d->d_out, d->k_pad).part_bytes);
+    const Fp8Plan plan = fp8_plan(T, d->d_out, d->k_pad);
+    w.partial = off; off = align_up(off + plan.part_bytes);
+    w.count = off;   off = align_up(off + (plan.few && plan.split > 1 ? FP8_COUNTERS * 4 : 0));
     w.total = off;
     return w;
 }
@@ -190,7 +192,7 @@ int w4a4_fp8_quantize_activations(const void* X, int x_dtype, int64_t T, const w
     const w4a4_fp8_ws_layout w = ws_layout(T, desc);
     uint8_t* b = (uint8_t*)ws;
     return dev_status(launch_fp8_actquant(X, x_dtype, T, desc->d_in, desc->scale_kind, b + w.a_q, (float*)(b + w.a_s),
-                                          t_ld_of(T), (hipStream_t)stream));
+                                          t_ld_of(T), w.total > w.count ? (int32_t*)(b + w.count) : nullptr, (hipStream_t)stream));
 }
 
 int w4a4_fp8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_fp8_packed* desc, void* Y, int y_dtype,
@@ -204,7 +206,7 @@ int w4a4_fp8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_
     if (T == 0) return W4A4_OK;
     uint8_t* b = (uint8_t*)ws;
     return dev_status(launch_fp8_gemm(b + w.a_q, (const float*)(b + w.a_s), T, t_ld_of(T), *desc, Y, y_dtype,
-                                      (float*)(b + w.partial), (hipStream_t)stream));
+                                      (float*)(b + w.partial), (int32_t*)(b + w.count), (hipStream_t)stream));
 }
 
 int w4a4_fp8_linear(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc, void* Y, int y_dtype, void* ws,

@@ -83,6 +83,12 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t p, int64_t co
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = p + i < cols ? bf16_to_f32(row[p + i]) : 0.0f;
 }
+// Values that workgroups of different XCDs pass each other go past the XCDs' caches, value by value: a
+// release or acquire fence would write back or drop a whole L2 (and made these kernels up to 8
+// times slower).
+__device__ __forceinline__ void put_shared(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ float get_shared(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
 // Buffer loads: a uniform descriptor, a lane offset that stays in one register for a whole stream
 // and a uniform offset that walks it (flat addresses cost two registers a load in flight).
 typedef __amdgpu_buffer_rsrc_t Rsrc;

@@ -40,7 +40,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int MUL_FP8 = 0, MUL_FP8_E8M0 = 1, MUL_BF16 = 2;
 
 // Whether the few-token kernel runs: up to 64 tokens, and small layers, whose tiles would fill few
-// CUs for many latencies (256 x 512 -> 1024: 9.9 us in tiles, NOTE here).
+// CUs for many latencies (256 x 512 -> 1024: 9.9 us in tiles, 4.0 here).
 bool fp8_few(int64_t T, int64_t N, int64_t k_pad) {
     return T <= 64 || (T <= 1024 && (T + 63) / 64 * ((N + 15) / 16) * (k_pad / 128) <= 8192);
 }
@@ -342,74 +342,120 @@ __global__ __launch_bounds__(64) void fp8_reduce_kernel(int64_t T, int64_t N, vo
 
 // ---------------------------------------------------------------- few tokens
 //
-// Bound by reading the weight codes once.  A workgroup owns 16 weight rows; its eight
+// Bound by reading the weight codes once.  A workgroup owns RT tiles of 16 weight rows; its eight
 // wavefronts take every eighth block of 128 inputs, read codes straight from memory, widen
 // them to bf16 and multiply them with up to NT tiles of 16 tokens by v_mfma_f32_16x16x32_bf16;
 // the eight partial sums meet in LDS and are added in wavefront order.
 //
 // The loop is as simple as it looks on purpose: at 40 registers all 864 workgroups of a 13824-row
-// layer are resident and cover each other's waits (one token, 5120 -> 13824: 12.6 us).  A ring of
+// layer are resident and cover each other's waits (one token, 5120 -> 13824: 12.6 us for 71 MB; a
+// kernel that only reads as much takes 14.4 from memory).  A ring of
 // blocks in flight per wavefront with the registers that it takes was slower (16.8), so was
 // quantizing the token in the same kernel (17.9, against 3.3 more for the quantization's launch),
 // and non-temporal loads lose a layer that stays in the 256 MB memory-side cache (24 tokens,
 // 13824 -> 5120: 29 against 19 us).
-template <int NT, int OUT>
-__global__ __launch_bounds__(512) void fp8_gemv_kernel(const uint8_t* __restrict__ Aq, const float* __restrict__ As, int64_t T,
+//
+// With several token tiles the vector memory path, not the memory, is what the reads of both operands
+// wait for: two row tiles use a token fragment once more, and the inputs split over gridDim.z
+// workgroups keep the CUs evenly filled.  Both pay from a layer that the L2s do not hold on
+// (24 tokens, 13824 -> 5120: 22.8 to 20.4 us a call, 64 tokens 32.5 to 25.6; but 32 tokens, 5120 -> 5120:
+// 12.7 to 14.5).  One row tile splits only where few workgroups would walk far (one token, 13824 ->
+// 5120, split in 3: 18.4 to 19.8 us; 32768 -> 512, in 8: 20.1 to 15.0).
+template <int NT, int RT, int OUT>
+__global__ __launch_bounds__(512, RT == 1 ? 1 : NT == 2 ? 4 : 2) void fp8_gemv_kernel(const uint8_t* __restrict__ Aq, const float* __restrict__ As, int64_t T,
                                                        int64_t t_ld, const uint8_t* __restrict__ Bq,
                                                        const float* __restrict__ Bs, int64_t N, int64_t nkb,
-                                                       void* __restrict__ out, int vec_store) {
+                                                       void* __restrict__ out, int vec_store, float* __restrict__ part,
+                                                       int32_t* __restrict__ count) {
     constexpr int LD = 20;                                 // staged row stride in floats
-    __shared__ __attribute__((aligned(16))) float red[8 * NT * 16 * LD];
+    __shared__ __attribute__((aligned(16))) float red[8 * RT * NT * 16 * LD];
+    __shared__ int done;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * NT * 16;
+    const int64_t n0 = (int64_t)blockIdx.x * RT * 16, t0 = (int64_t)blockIdx.y * NT * 16;
     const int64_t blk = nkb * 2048;
-    const uint8_t* const bp = Bq + blockIdx.x * blk + lane * 16;
+    const uint8_t* bp[RT];
+#pragma unroll
+    for (int m = 0; m < RT; ++m) bp[m] = Bq + (n0 + m * 16 < N ? n0 + m * 16 : n0) / 16 * blk + lane * 16;
     const float* const sp = Bs + n0 / 128 * nkb;
     const uint8_t* ap[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) ap[i] = Aq + (t0 + i * 16 < T ? t0 + i * 16 : t0) / 16 * blk + lane * 16;
 
-    v4f acc[NT];
+    v4f acc[RT][NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = v4f{0, 0, 0, 0};
-    for (int64_t kb = wave; kb < nkb; kb += 8) {
-        const uint8_t* const p = bp + kb * 2048;
-        const v8i b = join(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024));
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[m][i] = v4f{0, 0, 0, 0};
+    const int kb1 = (int)(nkb * (blockIdx.z + 1) / gridDim.z);
+    for (int kb = (int)(nkb * blockIdx.z / gridDim.z) + wave; kb < kb1; kb += 8) {
         const float sb = sp[kb];
-        v8bf wb[4];
+        v8bf wb[RT][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) wb[q] = widen_e4m3(b[2 * q], b[2 * q + 1]);
+        for (int m = 0; m < RT; ++m) {
+            const uint8_t* const p = bp[m] + kb * 2048;
+            const v8i b = join(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) wb[m][q] = widen_e4m3(b[2 * q], b[2 * q + 1]);
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const uint8_t* const x = ap[i] + kb * 2048;
             const v8i a = join(*reinterpret_cast<const uint4*>(x), *reinterpret_cast<const uint4*>(x + 1024));
             const float s = As[kb * t_ld + min(t0 + i * 16 + r, t_ld - 1)] * sb;
-            v4f t = v4f{0, 0, 0, 0};
+            v4f t[RT];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], widen_e4m3(a[2 * q], a[2 * q + 1]), t, 0, 0, 0);
+            for (int m = 0; m < RT; ++m) t[m] = v4f{0, 0, 0, 0};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(t[e], s, acc[i][e]);
+            for (int q = 0; q < 4; ++q) {
+                const v8bf wa = widen_e4m3(a[2 * q], a[2 * q + 1]);
+#pragma unroll
+                for (int m = 0; m < RT; ++m) t[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[m][q], wa, t[m], 0, 0, 0);
+            }
+#pragma unroll
+            for (int m = 0; m < RT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][i][e] = __builtin_fmaf(t[m][e], s, acc[m][i][e]);
         }
     }
     // lane: token r of tile i, rows 4 g .. 4 g + 3
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-        *reinterpret_cast<v4f*>(red + (wave * NT * 16 + i * 16 + r) * LD + 4 * g) = acc[i];
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            *reinterpret_cast<v4f*>(red + (((wave * RT + m) * NT + i) * 16 + r) * LD + 4 * g) = acc[m][i];
     __syncthreads();
-    if (tid >= NT * 64) return;
-    const int c = tid & 3;
-    const int64_t tok = t0 + (tid >> 2);
+    const int c = tid & 3, m = RT == 2 ? tid / (NT * 64) & 1 : 0;
+    const int64_t tok = t0 + tid % (NT * 64) / 4;
     v4f y = v4f{0, 0, 0, 0};
+    if (tid < RT * NT * 64)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        const v4f v = *reinterpret_cast<const v4f*>(red + (w * NT * 16 + (tid >> 2)) * LD + 4 * c);
+        for (int w = 0; w < 8; ++w) {
+            const v4f v = *reinterpret_cast<const v4f*>(red + (w * RT * NT * 16 + (tid >> 2)) * LD + 4 * c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += v[e];
+            for (int e = 0; e < 4; ++e) y[e] += v[e];
+        }
+    if (gridDim.z > 1) {   // the last of the tile's ranges to be done adds them all, in order
+        const uint32_t tile = blockIdx.y * gridDim.x + blockIdx.x, step = gridDim.x * gridDim.y * RT * NT * 256;
+        float* const p = part + tile * RT * NT * 256 + tid * 4;
+        if (tid < RT * NT * 64)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put_shared(p + blockIdx.z * step + e, y[e]);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the range is where every XCD sees it
+        __syncthreads();
+        if (tid == 0) done = __hip_atomic_fetch_add(count + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (done != (int)gridDim.z - 1) return;
+        if (tid == 0) count[tile] = 0;                     // for the next call
+        y = v4f{0, 0, 0, 0};
+        if (tid < RT * NT * 64)
+            for (uint32_t u = 0; u < gridDim.z; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] += get_shared(p + u * step + e);
     }
+    if (tid >= RT * NT * 64) return;
     if (tok >= T) return;
-    const int64_t n = n0 + 4 * c;
+    const int64_t n = n0 + m * 16 + 4 * c;
     if constexpr (OUT == W4A4_Y_F32) {
         float* const Y = reinterpret_cast<float*>(out) + tok * N + n;
         if (vec_store && n + 3 < N) {
@@ -450,41 +496,60 @@ hipError_t run_tiles(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld
 
 template <int MUL, int OUT>
 hipError_t run_many(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out, float* part,
-                    hipStream_t st) {
-    const Fp8Plan plan = fp8_plan(T, d.d_out, d.k_pad);
+                    const Fp8Plan& plan, hipStream_t st) {
     if (plan.big) return run_tiles<8, 4, 2, 4, MUL, OUT>(aq, as, T, t_ld, d, out, part, plan, st);
     return run_tiles<4, 4, 2, 2, MUL, OUT>(aq, as, T, t_ld, d, out, part, plan, st);
 }
 
-template <int NT, int OUT>
-hipError_t run_few(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
-                   hipStream_t st) {
-    hipLaunchKernelGGL((fp8_gemv_kernel<NT, OUT>), dim3((uint32_t)((d.d_out + 15) / 16), (uint32_t)((T + NT * 16 - 1) / (NT * 16))), dim3(512), 0, st, aq, as, T, t_ld,
-                       d.codes, d.scales, d.d_out, d.k_pad / 128, out, d.d_out % 4 == 0 ? 1 : 0);
+template <int NT, int RT, int OUT>
+hipError_t run_few(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out, float* part,
+                   int32_t* count, const Fp8Plan& plan, hipStream_t st) {
+    const dim3 grid((uint32_t)((d.d_out + RT * 16 - 1) / (RT * 16)), (uint32_t)((T + NT * 16 - 1) / (NT * 16)), (uint32_t)plan.split);
+    hipLaunchKernelGGL((fp8_gemv_kernel<NT, RT, OUT>), grid, dim3(512), 0, st, aq, as, T, t_ld, d.codes, d.scales, d.d_out,
+                       d.k_pad / 128, out, d.d_out % 4 == 0 ? 1 : 0, part, count);
     return hipGetLastError();
 }
 
 template <int OUT>
 hipError_t run_out(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out, float* part,
-                   hipStream_t st) {
-    if (T <= 16) return run_few<1, OUT>(aq, as, T, t_ld, d, out, st);
-    if (T <= 32) return run_few<2, OUT>(aq, as, T, t_ld, d, out, st);
-    if (fp8_few(T, d.d_out, d.k_pad)) return run_few<4, OUT>(aq, as, T, t_ld, d, out, st);
-    if constexpr (OUT == W4A4_Y_F32) return run_many<MUL_BF16, OUT>(aq, as, T, t_ld, d, out, part, st);
-    else if (d.scale_kind == W4A4_FP8_SCALE_F32) return run_many<MUL_FP8, OUT>(aq, as, T, t_ld, d, out, part, st);
-    else return run_many<MUL_FP8_E8M0, OUT>(aq, as, T, t_ld, d, out, part, st);
+                   int32_t* count, hipStream_t st) {
+    const Fp8Plan plan = fp8_plan(T, d.d_out, d.k_pad);
+    if (plan.few && T <= 16) return run_few<1, 1, OUT>(aq, as, T, t_ld, d, out, part, count, plan, st);
+    if (plan.few && T <= 32) return plan.rt == 2 ? run_few<2, 2, OUT>(aq, as, T, t_ld, d, out, part, count, plan, st)
+                            : run_few<2, 1, OUT>(aq, as, T, t_ld, d, out, part, count, plan, st);
+    if (plan.few) return plan.rt == 2 ? run_few<4, 2, OUT>(aq, as, T, t_ld, d, out, part, count, plan, st)
+                            : run_few<4, 1, OUT>(aq, as, T, t_ld, d, out, part, count, plan, st);
+    if constexpr (OUT == W4A4_Y_F32) return run_many<MUL_BF16, OUT>(aq, as, T, t_ld, d, out, part, plan, st);
+    else if (d.scale_kind == W4A4_FP8_SCALE_F32) return run_many<MUL_FP8, OUT>(aq, as, T, t_ld, d, out, part, plan, st);
+    else return run_many<MUL_FP8_E8M0, OUT>(aq, as, T, t_ld, d, out, part, plan, st);
 }
 
 }  // namespace
 
 // Big tiles are 256 x 256, one workgroup a CU; small ones 128 x 128, two a CU.  The tiles that fill
 // whole rounds of the CUs run whole; the rest are cut along the inputs into as many ranges as there
-// are free CUs, at least MIN_BLOCKS blocks each.
+// are free CUs, at least MIN_BLOCKS blocks each (4096 x 13824 -> 5120, 64 of 320 tiles in four ranges:
+// 346 to 286 us).
 Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t k_pad) {
-    Fp8Plan p = {0, 0, 1, false, 0};
-    if (fp8_few(T, N, k_pad)) return p;
-    constexpr int64_t CUS = 256, MIN_BLOCKS = 4, MAX_SPLIT = 16;
-    const int64_t nkb = k_pad / 128, big = ((T + 255) / 256) * ((N + 255) / 256);
+    Fp8Plan p = {0, 0, 1, 1, false, false, 0};
+    constexpr int64_t CUS = 256, MIN_BLOCKS = 4, MAX_SPLIT = 16, FEW_CODES = 1 << 25;
+    const int64_t nkb = k_pad / 128;
+    p.few = fp8_few(T, N, k_pad);
+    if (T == 0 || N == 0) return p;
+    if (p.few) {
+        const int64_t nt = T <= 16 ? 1 : T <= 32 ? 2 : 4;   // token tiles of a workgroup
+        p.rt = nt > 1 && N * k_pad > FEW_CODES ? 2 : 1;
+        p.tiles = ((N + 16 * p.rt - 1) / (16 * p.rt)) * ((T + nt * 16 - 1) / (nt * 16));
+        int64_t s = 2 * CUS / p.tiles, least = p.rt == 2 ? 16 : 32;   // ranges; blocks of each
+        if (s > nkb / least) s = nkb / least;
+        if (s > MAX_SPLIT) s = MAX_SPLIT;
+        if (s >= 2) {
+            p.split = (int32_t)s;
+            p.part_bytes = (size_t)(p.tiles * s * nt * p.rt) * 1024;
+        }
+        return p;
+    }
+    const int64_t big = ((T + 255) / 256) * ((N + 255) / 256);
     p.big = big >= 64;
     p.tiles = p.big ? big : ((T + 127) / 128) * ((N + 127) / 128);
     const int64_t round = p.big ? CUS : 2 * CUS, tail = p.tiles % round;
@@ -502,9 +567,9 @@ Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t k_pad) {
 }
 
 hipError_t launch_fp8_gemm(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
-                           int y_dtype, float* part, hipStream_t st) {
-    return y_dtype == W4A4_Y_F32 ? run_out<W4A4_Y_F32>(aq, as, T, t_ld, d, out, part, st)
-                                 : run_out<W4A4_Y_BF16>(aq, as, T, t_ld, d, out, part, st);
+                           int y_dtype, float* part, int32_t* count, hipStream_t st) {
+    return y_dtype == W4A4_Y_F32 ? run_out<W4A4_Y_F32>(aq, as, T, t_ld, d, out, part, count, st)
+                                 : run_out<W4A4_Y_BF16>(aq, as, T, t_ld, d, out, part, count, st);
 }
 
 }  // namespace w4a4

@@ -481,12 +481,6 @@ __device__ __forceinline__ void store_y(const DownArgs& a, int t, int row, float
     else reinterpret_cast<uint16_t*>(a.out)[(int64_t)t * a.d + row] = bf16_rne(y);
 }
 
-// Values that workgroups of different XCDs pass each other go past the XCDs' caches, value by value: a
-// release or acquire fence would write back or drop a whole L2 (and made these kernels up to 8
-// times slower).
-__device__ __forceinline__ void put_shared(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ __forceinline__ float get_shared(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-
 constexpr int DOWN_MIN = 2;   // groups a wavefront, below which tiles stay whole
 
 // TB: tokens the sums are laid out for; RT: row tiles (16 outputs) of a workgroup.  The work is one sequence of groups of D blocks: segment by

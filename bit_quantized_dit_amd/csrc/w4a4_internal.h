@@ -74,22 +74,24 @@ hipError_t launch_dyn_transpose(const float* W, int64_t d_in, int64_t d_out, uin
 // rows of t_ld scales), weight quantization, the reordering of a checkpoint's codes, the
 // product
 hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_in, int kind, uint8_t* aq, float* as,
-                               int64_t t_ld, hipStream_t st);
+                               int64_t t_ld, int32_t* count, hipStream_t st);
 hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d, uint8_t* codes, float* scales,
                            hipStream_t st);
 hipError_t launch_fp8_reorder(const uint8_t* src, const void* src_scales, const w4a4_fp8_packed& d, uint8_t* codes,
                               float* scales, hipStream_t st);
-// Plan of the product of more than a few tokens (host logic): tiles [0, full) whole, each later
-// one as `split` ranges of the inputs, whose fp32 sums take part_bytes of workspace.
+// Plan of the product (host logic): tiles [0, full) whole, each later one as `split` ranges of the
+// inputs, whose fp32 sums take part_bytes of workspace.  `few`: the few-token kernel, which splits all
+// its tiles or none and counts the ranges done in FP8_COUNTERS counters.
+constexpr int FP8_COUNTERS = 512;
 struct Fp8Plan {
     int64_t tiles, full;
-    int32_t split;
-    bool big;
+    int32_t split, rt;
+    bool few, big;
     size_t part_bytes;
 };
 Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t k_pad);
 hipError_t launch_fp8_gemm(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
-                           int y_dtype, float* part, hipStream_t st);
+                           int y_dtype, float* part, int32_t* count, hipStream_t st);
 
 // mixture of experts (moe.hip): the arrays of w4a4_moe_ws_layout
 struct MoeBuffers {

@@ -82,7 +82,7 @@ class W4A4Fp8Packed(ctypes.Structure):
 
 
 class W4A4Fp8WsLayout(ctypes.Structure):
-    _fields_ = [("a_q", ctypes.c_size_t), ("a_s", ctypes.c_size_t), ("partial", ctypes.c_size_t),
+    _fields_ = [("a_q", ctypes.c_size_t), ("a_s", ctypes.c_size_t), ("partial", ctypes.c_size_t), ("count", ctypes.c_size_t),
                 ("total", ctypes.c_size_t)]
 
 

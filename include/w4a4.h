@@ -410,6 +410,8 @@ typedef struct w4a4_fp8_ws_layout {
                          unwritten                                                         */
     size_t partial;   /* fp32 partial sums of K ranges (written and read back within a
                          call; empty when the plan does not split)                         */
+    size_t count;     /* int32 ranges done, zero between calls (of a few tokens' plan that
+                         splits; set by the quantization)                                  */
     size_t total;
 } w4a4_fp8_ws_layout;
 int w4a4_fp8_workspace_layout(int64_t T, const w4a4_fp8_packed* desc, w4a4_fp8_ws_layout* out);
