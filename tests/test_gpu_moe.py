@@ -215,3 +215,30 @@ def test_binding_refusals():
         B.moe_layer(router, None, up, up, 2)
     with pytest.raises(ValueError):
         B.moe_layer(router[:3], None, up, down, 2)
+
+
+@pytest.mark.parametrize("T,d,f,E,k,gated", [(1, 260, 1600, 8, 8, True), (12, 260, 1600, 8, 3, True), (7, 131, 1000, 10, 4, False),
+                                             (40, 260, 1600, 6, 3, True), (40, 4100, 1700, 2, 2, False), (100, 200, 900, 5, 3, True),
+                                             (2, 8300, 100, 2, 1, False), (64, 300, 400, 40, 6, True)])
+def test_divided_down_tiles(T, d, f, E, k, gated):
+    """Sizes at which several workgroups share a tile of outputs, or one takes several, and the
+    passes over codes of 4, 8 and 16 tokens and of two row tiles; twice, for the same bits."""
+    layer, r, mats = _layer(d, f, E, k, gated, True, BF16, T + d)
+    x = _tokens(T, d, BF16, 5)
+    Y, _ = _check(x, BF16, layer, r, mats, F32)
+    ws, again = B.alloc_workspace_moe(T, layer), torch.empty_like(Y)
+    X = torch.from_numpy(x).to(BF16).cuda()
+    for _ in range(3):
+        again.fill_(float("nan"))
+        B.w4a4_moe_forward(X, layer, again, ws)
+        assert torch.equal(again, Y)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        B.w4a4_moe_forward(X, layer, again, ws)
+    for _ in range(3):
+        again.fill_(float("nan"))
+        (X.float() @ torch.ones(d, 8, device="cuda")).sum().item()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, Y)
