@@ -131,6 +131,13 @@ __device__ __forceinline__ void store_tiles(const v4f (&acc)[FT][FF], uint8_t* s
 //
 // Tiles that would leave most CUs idle in a last round run as sp.n ranges of their blocks, whose
 // sums go to memory; fp8_reduce_kernel adds them in order.
+//
+// Measured: 57600 x 5120 -> 13824, bf16 outputs, 3.41 ms (2.39 PFLOP/s; the library's product with one
+// scale for each whole operand takes 2.76).  What shares a CU's LDS bounds it: the same loop takes 2.7 ms
+// without the copies into LDS, 2.1 without the fragment reads, 3.25 with a quarter of the scaling.
+// A second barrier and the copies in two halves changed nothing (3.64 against 3.62).  E8M0 scales in the
+// instruction: 4096 x 13824 -> 5120 in 263 us (library 210).  fp32 outputs run at the bf16
+// instructions' rate: 4096 x 5120 -> 13824 in 499 us, 1.16 PFLOP/s (library bf16 1.24).
 struct Split {
     float* part;
     uint32_t full, n;
