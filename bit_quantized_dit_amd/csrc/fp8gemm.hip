@@ -40,9 +40,11 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int MUL_FP8 = 0, MUL_FP8_E8M0 = 1, MUL_BF16 = 2;
 
 // Whether the few-token kernel runs: up to 64 tokens, and small layers, whose tiles would fill few
-// CUs for many latencies (256 x 512 -> 1024: 9.9 us in tiles, 4.0 here).
+// CUs for many latencies (256 x 512 -> 1024: 9.9 us in tiles, 4.0 here; whole calls, tiles against
+// this kernel: 333 x 4999 -> 1111 21.9 and 18.7, 512 x 2048 -> 2048 18.7 and 16.2, 256 x 5120 -> 3000 24.6 and 22.0;
+// even at 256 x 2048 -> 8192, 24.2 and 24.0).  Short inputs leave more to the writes: 1000 x 512 -> 4096 15.9 and 25.2.
 bool fp8_few(int64_t T, int64_t N, int64_t k_pad) {
-    return T <= 64 || (T <= 1024 && (T + 63) / 64 * ((N + 15) / 16) * (k_pad / 128) <= 8192);
+    return T <= 64 || (T <= 1024 && (T + 63) / 64 * ((N + 15) / 16) * (k_pad / 128) <= (k_pad < 1024 ? 8192 : 32768));
 }
 
 __device__ __forceinline__ v8i join(const uint4& a, const uint4& b) {

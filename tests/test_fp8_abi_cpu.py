@@ -171,7 +171,7 @@ def test_plans(L):
     whose last round is split, the few-token kernel's row tiles."""
     out = B.W4A4Fp8WsLayout()
     for T, d_in, d_out, tiles, floats in [(1, 5120, 13824, 0, 0), (64, 512, 1024, 0, 0), (1100, 400, 1501, 0, 0),
-                                          (1000, 2300, 1003, 8 * 8 * 4, 128 * 128), (2100, 1100, 2090, 9 * 9 * 2, 256 * 256),
+                                          (1000, 2300, 1003, 0, 0), (1050, 2300, 1003, 9 * 8 * 4, 128 * 128), (2100, 1100, 2090, 9 * 9 * 2, 256 * 256),
                                           (4096, 13824, 5120, 64 * 4, 256 * 256), (24, 13824, 5120, 160 * 3, 32 * 32),
                                           (50, 8200, 4111, 129 * 3, 64 * 32), (3, 16500, 41, 3 * 4, 16 * 16)]:
         assert L.w4a4_fp8_workspace_layout(T, _packed(1, d_in, d_out), out) == 0

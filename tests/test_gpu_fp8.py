@@ -233,7 +233,7 @@ def test_binding_refusals():
 # Each form of the product at ragged sizes: 128 x 128 tiles whole and with split inputs, 256 x 256
 # tiles with split inputs, the few-token kernel with several token groups, with two row tiles and
 # split inputs, and with split inputs of few rows.
-FORMS = [(1100, 400, 1501), (1000, 2300, 1003), (2100, 1100, 2090), (900, 384, 300), (20, 8200, 4111), (50, 8200, 4100), (3, 16500, 41), (40, 8300, 21)]
+FORMS = [(1100, 400, 1501), (1050, 2300, 1003), (1000, 2300, 1003), (2100, 1100, 2090), (900, 384, 300), (20, 8200, 4111), (50, 8200, 4100), (3, 16500, 41), (40, 8300, 21)]
 
 
 @pytest.mark.parametrize("kind", [0, 1])
@@ -246,12 +246,12 @@ def test_forms(T, d, n, kind):
         _check(_x(T, d, BF16, 51), BF16, w, kind, F32)
 
 
-@pytest.mark.parametrize("T,d,n,kind", [(1000, 2300, 1003, 0), (2100, 1100, 2090, 1), (50, 8200, 4111, 0), (3, 16500, 41, 1)])
+@pytest.mark.parametrize("T,d,n,kind", [(1050, 2300, 1003, 0), (1000, 2300, 1003, 1), (2100, 1100, 2090, 1), (50, 8200, 4111, 0), (3, 16500, 41, 1)])
 def test_split_forms_streams_and_repeats(T, d, n, kind):
     test_split_calls_streams_and_repeats(T, d, n, kind)
 
 
-@pytest.mark.parametrize("T,d,n", [(1000, 2300, 300), (20, 8200, 4111), (3, 16500, 41)])
+@pytest.mark.parametrize("T,d,n", [(1050, 2300, 300), (20, 8200, 4111), (3, 16500, 41)])
 def test_nan_token_of_split_inputs(T, d, n):
     """A NaN in one range of the inputs makes its token's row NaN and no other."""
     layer = B.w4a4_fp8_pack_weights(torch.randn(n, d, device="cuda") * 0.02)
