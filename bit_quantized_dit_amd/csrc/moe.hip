@@ -725,14 +725,18 @@ void run_logits(const void* X_, const w4a4_moe& m, int T, bool copy, float* logi
 
 // Tokens of an expert that a pass over its codes takes (xi and, above 16, nt tiles), from the number
 // that it has on average: a second pass reads the codes again, a wider one reads more of the other
-// operand than there is.
+// operand than there is.  Passes of 4, 8, 16 and 32 tokens, us a call, 2048 x 768 gated, 8 of 64 experts:
+//   8 tokens 58, 56, 57, 62;  16: 70, 62, 62, 67;  32: 95, 73, 67, 72;  64: 146, 104, 77, 80;
+// 64 tokens, 8 of 32 experts: 125, 86, 65, 58; 16 tokens, 5120 x 13824, 2 of 8 experts, 8 or 16 a pass: 196, 223; 40
+// tokens, 5120 x 1024 gated, 6 of 64 experts: 188, 181 (above 16 tokens, 16 a pass go with the down step's
+// two row tiles).
 struct Pass {
     int xi, nt;
 };
 Pass pass_of(int64_t T, int64_t k, int64_t E) {
     const int64_t pairs = T * k;
     if (T <= 4 || pairs <= E) return {1, 1};
-    if (T <= 8 || pairs <= 4 * E) return {2, 1};
+    if (T <= 8 || pairs <= (T <= 16 ? 4 : 3) * E) return {2, 1};
     if (T <= 16 || pairs <= 10 * E) return {4, 1};
     return {4, pairs <= 24 * E ? 2 : 4};
 }
