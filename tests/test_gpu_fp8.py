@@ -263,3 +263,18 @@ def test_nan_token_of_split_inputs(T, d, n):
     B.w4a4_fp8_linear(x, layer, Y, ws)
     keep = torch.arange(T, device="cuda") != T // 2
     assert bool(torch.isnan(Y[T // 2]).all()) and torch.equal(Y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T,d,n", [(50, 8200, 4111), (3, 16500, 41), (1050, 2300, 300)])
+def test_workspace_used_again_with_other_tokens(T, d, n):
+    """Ranges of an earlier call never reach a later one's sums."""
+    layer = B.w4a4_fp8_pack_weights(torch.randn(n, d, device="cuda") * 0.02)
+    ws, Y = B.alloc_workspace_fp8(T, layer), torch.empty(T, n, device="cuda")
+    xs = [torch.from_numpy(_x(T, d, BF16, 70 + i)).to(BF16).cuda() for i in range(3)]
+    want = []
+    for x in xs:
+        B.w4a4_fp8_linear(x, layer, Y, B.alloc_workspace_fp8(T, layer))
+        want.append(Y.clone())
+    for i in (0, 1, 2, 1, 0, 2, 0, 2, 1):
+        B.w4a4_fp8_linear(xs[i], layer, Y, ws)
+        assert torch.equal(Y, want[i])

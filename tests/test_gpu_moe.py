@@ -242,3 +242,18 @@ def test_divided_down_tiles(T, d, f, E, k, gated):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(again, Y)
+
+
+@pytest.mark.parametrize("T,d,f,E,k", [(1, 260, 1600, 8, 8), (12, 260, 1600, 8, 3), (40, 4100, 1700, 2, 2), (64, 300, 400, 40, 6)])
+def test_workspace_used_again_with_other_tokens(T, d, f, E, k):
+    """Parts of an earlier call never reach a later one's sums."""
+    layer, _, _ = _layer(d, f, E, k, True, True, BF16, 90)
+    ws, Y = B.alloc_workspace_moe(T, layer), torch.empty(T, d, device="cuda")
+    xs = [torch.from_numpy(_tokens(T, d, BF16, 91 + i)).to(BF16).cuda() for i in range(3)]
+    want = []
+    for x in xs:
+        B.w4a4_moe_forward(x, layer, Y, B.alloc_workspace_moe(T, layer))
+        want.append(Y.clone())
+    for i in (0, 1, 2, 1, 0, 2, 0, 2, 1):
+        B.w4a4_moe_forward(xs[i], layer, Y, ws)
+        assert torch.equal(Y, want[i])
