@@ -18,10 +18,12 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits, int kind) {
 // fl32(x / s) without a division per element.  Binary32 x: the double product x * RN64(1 / s)
 // rounded to binary32; it lies within 2^-52 (relative) of x / s, and a quotient of two binary32
 // numbers stays further than that from every binary32 rounding midpoint, so the rounding lands on
-// the same value.  bf16 x: q = x r, then q + (x - q s) r with r = RN32(1 / s), three full-rate
-// operations; equal to the quotient on every bf16 significand and every significand of s (all 2^31
-// pairs compared).  Quotients below 2^-11 may differ where a remainder leaves the normal range;
-// they are the code 0 either way, as s >= 2^-60.
+// the same value.  bf16 x: q = x r, then q - (q s - x) r with r = RN32(1 / s), three full-rate
+// operations; equal to the quotient for every bf16 significand and every significand of s (2^30
+// pairs, compared at two exponents each).  The remainder is taken as q s - x, because x - q s is +0
+// for a zero of either sign and would turn a quotient of -0 into +0.  Quotients below 2^-11 may
+// differ where a remainder leaves the normal range; they are the code of a zero of their sign either
+// way, as s >= 2^-60.
 struct InverseF32 {
     double r;
     __device__ explicit InverseF32(float s) : r(1.0 / (double)s) {}
@@ -32,7 +34,7 @@ struct InverseBf16 {
     __device__ explicit InverseBf16(float s) : r(1.0f / s) {}
     __device__ float of(float x, float s) const {
         const float q = x * r;
-        return __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+        return __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);
     }
 };
 template <typename X> struct InverseOf { typedef InverseF32 type; };

@@ -278,3 +278,22 @@ def test_workspace_used_again_with_other_tokens(T, d, n):
     for i in (0, 1, 2, 1, 0, 2, 0, 2, 1):
         B.w4a4_fp8_linear(xs[i], layer, Y, ws)
         assert torch.equal(Y, want[i])
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_zeros_keep_their_signs(dtype, kind):
+    """The code of -0, and of a negative value that rounds to zero, is 0x80 for every input type,
+    in activations and weights."""
+    x = np.random.default_rng(80).choice(np.float32([0.0, -0.0, 2.0 ** -120, -2.0 ** -120, 1e-40, -1e-40]), (48, 300))
+    if dtype == BF16:
+        x = R.bf16(x)
+    x[::3, 5] = 1.0                      # blocks of zeros beside an ordinary value
+    X = torch.from_numpy(x).to(dtype).cuda()
+    p = B.w4a4_fp8_pack_weights(X, kind)
+    c, _ = R.quantize_blocks(x, kind)
+    assert np.array_equal(p.views()["codes"][0].cpu().numpy(), c) and (c == 0x80).any() and (c == 0).any()
+    ws = B.alloc_workspace_fp8(48, p)
+    B.w4a4_fp8_quantize_activations(X, p, ws)
+    q, _ = R.quantize_rows(x, kind)
+    assert np.array_equal(B.workspace_fp8_views(ws, 48, p)["A_q"].cpu().numpy(), q) and (q[:, :300] == 0x80).any()
