@@ -60,6 +60,9 @@ __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__
     if (g == 0) as[kb * t_ld + t] = s;
 }
 
+// The product's counters, where the quantization of the same call does not clear them.
+__global__ __launch_bounds__(FP8_COUNTERS) void fp8_clear_kernel(int32_t* __restrict__ count) { count[threadIdx.x] = 0; }
+
 // Weights: one workgroup per 128 x 128 block; thread = (row, half of the block's inputs).
 template <typename W>
 __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, int64_t d_in, int64_t d_out, int64_t nkb,
@@ -153,6 +156,11 @@ hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_
     else
         hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, items, kind, aq, as, t_ld,
                            count);
+    return hipGetLastError();
+}
+
+hipError_t launch_fp8_clear(int32_t* count, hipStream_t st) {
+    hipLaunchKernelGGL(fp8_clear_kernel, dim3(1), dim3(FP8_COUNTERS), 0, st, count);
     return hipGetLastError();
 }
 

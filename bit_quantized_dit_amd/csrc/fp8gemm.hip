@@ -455,7 +455,6 @@ __global__ __launch_bounds__(512, RT == 1 ? 1 : NT == 2 ? 4 : 2) void fp8_gemv_k
         if (tid == 0) done = __hip_atomic_fetch_add(count + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (done != (int)gridDim.z - 1) return;
-        if (tid == 0) count[tile] = 0;                     // for the next call
         y = v4f{0, 0, 0, 0};
         if (tid < RT * NT * 64)
             for (uint32_t u = 0; u < gridDim.z; ++u)

@@ -71,8 +71,8 @@ hipError_t launch_dyn_gather(const uint16_t* W_t, const int32_t* O, int64_t d_in
 hipError_t launch_dyn_transpose(const float* W, int64_t d_in, int64_t d_out, uint16_t* W_t, hipStream_t st);
 
 // FP8 block-scaled layer (fp8.hip, fp8gemm.hip): activation codes and scales ([k_pad/128]
-// rows of t_ld scales), weight quantization, the reordering of a checkpoint's codes, the
-// product
+// rows of t_ld scales; `count`, where given: counters to clear), weight quantization, the
+// reordering of a checkpoint's codes, the product
 hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_in, int kind, uint8_t* aq, float* as,
                                int64_t t_ld, int32_t* count, hipStream_t st);
 hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d, uint8_t* codes, float* scales,
@@ -90,6 +90,8 @@ struct Fp8Plan {
     size_t part_bytes;
 };
 Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t k_pad);
+hipError_t launch_fp8_clear(int32_t* count, hipStream_t st);
+// `count` has to be zero where the plan has counters
 hipError_t launch_fp8_gemm(const uint8_t* aq, const float* as, int64_t T, int64_t t_ld, const w4a4_fp8_packed& d, void* out,
                            int y_dtype, float* part, int32_t* count, hipStream_t st);
 

@@ -410,15 +410,18 @@ typedef struct w4a4_fp8_ws_layout {
                          unwritten                                                         */
     size_t partial;   /* fp32 partial sums of K ranges (written and read back within a
                          call; empty when the plan does not split)                         */
-    size_t count;     /* int32 ranges done, zero between calls (of a few tokens' plan that
-                         splits; set by the quantization)                                  */
+    size_t count;     /* int32 ranges done (of a few tokens' plan that splits; cleared by
+                         every call that multiplies)                                       */
     size_t total;
 } w4a4_fp8_ws_layout;
 int w4a4_fp8_workspace_layout(int64_t T, const w4a4_fp8_packed* desc, w4a4_fp8_ws_layout* out);
 int w4a4_fp8_workspace_size(int64_t T, const w4a4_fp8_packed* desc, size_t* bytes);
 
 /* Activation codes and scales of X (device [T][d_in] fp32 or bf16, row-major contiguous)
- * into ws.  desc->n_mat must be 1, here and in the calls below.  Async. */
+ * into ws.  desc->n_mat must be 1, here and in the calls below.  Where they lie depends on T
+ * and d_in only, and they on scale_kind too: one call serves every layer of that d_in and
+ * scale_kind (gate and up, or query, key and value projections), in a workspace that is large
+ * enough for each of them.  Async. */
 int w4a4_fp8_quantize_activations(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc,
                                   void* ws, size_t ws_bytes, void* stream);
 /* The product on quantized activations in ws.  Y device [T][d_out], fp32 or bf16 (the

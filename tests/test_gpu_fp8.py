@@ -297,3 +297,26 @@ def test_zeros_keep_their_signs(dtype, kind):
     B.w4a4_fp8_quantize_activations(X, p, ws)
     q, _ = R.quantize_rows(x, kind)
     assert np.array_equal(B.workspace_fp8_views(ws, 48, p)["A_q"].cpu().numpy(), q) and (q[:, :300] == 0x80).any()
+
+
+@pytest.mark.parametrize("T,d,ns", [(3, 16500, (5000, 41, 300)), (20, 8200, (6000, 300, 4111)), (40, 8300, (9000, 21)), (1050, 2300, (300, 1003))])
+def test_codes_of_one_call_serve_several_layers(T, d, ns):
+    """Quantized with one layer, multiplied with others of the same d_in: plans that split and plans
+    that do not, counters at other places of the workspace or where another layer has partial sums."""
+    layers = [B.w4a4_fp8_pack_weights(torch.randn(n, d, device="cuda") * 0.02) for n in ns]
+    x = torch.from_numpy(_x(T, d, BF16, 90)).to(BF16).cuda()
+    want = []
+    for p in layers:
+        y = torch.empty(T, p.d_out, device="cuda")
+        B.w4a4_fp8_linear(x, p, y, B.alloc_workspace_fp8(T, p))
+        want.append(y)
+    need = max(B.w4a4_fp8_workspace_size(T, p) for p in layers)
+    for fill in (255, 1):
+        for by in range(len(layers)):
+            print(f"fp8 shared codes T={T} d={d} quantized with {ns[by]}", flush=True)
+            ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+            B.w4a4_fp8_quantize_activations(x, layers[by], ws)
+            for i in list(range(len(layers))) * 2:
+                y = torch.full((T, ns[i]), float("nan"), device="cuda")
+                B.w4a4_fp8_gemm_prequantized(ws, T, layers[i], y)
+                assert torch.equal(y, want[i])
