@@ -191,6 +191,21 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _written_on(buf: torch.Tensor, stream) -> torch.Tensor:
+    """buf, just allocated (on the current stream), for a call that writes it on `stream`: that
+    stream first waits for what the current one still has to do with the memory (an earlier
+    owner's work, a fill), and the allocator keeps the memory until `stream` is done with it."""
+    if stream is not None:
+        if not hasattr(stream, "wait_stream"):         # a raw handle
+            h = int(getattr(stream, "cuda_stream", stream))
+            stream = torch.cuda.ExternalStream(h, buf.device) if h else torch.cuda.default_stream(buf.device)
+        current = torch.cuda.current_stream(buf.device)
+        if stream != current:
+            stream.wait_stream(current)
+            buf.record_stream(stream)
+    return buf
+
+
 def _x_dtype(X: torch.Tensor) -> int:
     if X.dtype == torch.float32:
         return W4A4_X_F32
@@ -298,7 +313,7 @@ def w4a4_column_absmax(X: torch.Tensor, out: torch.Tensor | None = None, stream=
         raise ValueError(f"X must be 2-D, got {tuple(X.shape)}")
     rows, cols = X.shape
     if out is None:
-        out = torch.empty(cols, dtype=torch.int32, device=X.device)
+        out = _written_on(torch.empty(cols, dtype=torch.int32, device=X.device), stream)
     _dev(out, "out")
     if out.dtype not in (torch.int32, torch.uint32) or out.numel() != cols or out.device != X.device:
         raise ValueError(f"out must be a 32-bit integer tensor of {cols} elements on {X.device}")
@@ -353,7 +368,7 @@ def w4a4_pack_weights_dyn(W: torch.Tensor, s: np.ndarray, k: int, layout: int, s
     s = np.ascontiguousarray(s, dtype=np.float32)
     n = ctypes.c_size_t(0)
     _check("w4a4_packed_dyn_size", lib().w4a4_packed_dyn_size(d_in, d_out, int(k), int(layout), ctypes.byref(n)))
-    blob = torch.zeros(max(n.value, 256), dtype=torch.uint8, device=W.device)
+    blob = _written_on(torch.zeros(max(n.value, 256), dtype=torch.uint8, device=W.device), stream)
     desc = W4A4PackedDyn()
     st = lib().w4a4_pack_weights_dyn(_ptr(W), d_in, d_out, s.ctypes.data_as(ctypes.c_void_p), int(k), int(layout),
                                      _ptr(blob), blob.numel(), ctypes.byref(desc), _stream(stream))
@@ -425,7 +440,7 @@ def w4a4_search_alpha_k(X_cal: torch.Tensor, W: torch.Tensor, alphas, ks, layout
     al = np.ascontiguousarray(np.asarray(alphas, dtype=np.float32))
     ka = np.ascontiguousarray(np.asarray(ks, dtype=np.int32))
     nbytes = w4a4_search_scratch_size(T_cal, d_in, d_out, ka, layout)
-    scratch = torch.empty(nbytes, dtype=torch.uint8, device=X_cal.device)
+    scratch = _written_on(torch.empty(nbytes, dtype=torch.uint8, device=X_cal.device), stream)
     err = np.zeros(al.size * ka.size, np.float64)
     best = np.zeros(2, np.int32)
     vp = lambda arr: arr.ctypes.data_as(ctypes.c_void_p)
@@ -452,7 +467,7 @@ def w4a4_pack_weights(W: torch.Tensor, s: np.ndarray, O: np.ndarray, layout: int
     O = np.ascontiguousarray(O, dtype=np.int32)
     k = int(O.size)
     nbytes = w4a4_packed_size(d_in, d_out, k, layout)
-    blob = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=W.device)
+    blob = _written_on(torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=W.device), stream)
     desc = W4A4Packed()
     Optr = O.ctypes.data_as(ctypes.c_void_p) if k else None
     st = lib().w4a4_pack_weights(_ptr(W), d_in, d_out, s.ctypes.data_as(ctypes.c_void_p), Optr, k,
@@ -674,7 +689,7 @@ def w4a4_fp8_pack_weights(W: torch.Tensor, scale_kind: int = W4A4_FP8_SCALE_F32,
     if W.dim() not in (2, 3):
         raise ValueError(f"W must be [d_out, d_in] or [n_mat, d_out, d_in], got {tuple(W.shape)}")
     n_mat, (d_out, d_in) = (W.shape[0] if W.dim() == 3 else 1), W.shape[-2:]
-    blob = torch.empty(w4a4_fp8_packed_size(n_mat, d_in, d_out), dtype=torch.uint8, device=W.device)
+    blob = _written_on(torch.empty(w4a4_fp8_packed_size(n_mat, d_in, d_out), dtype=torch.uint8, device=W.device), stream)
     desc = W4A4Fp8Packed()
     _check("w4a4_fp8_pack_weights",
            lib().w4a4_fp8_pack_weights(_ptr(W), dt, n_mat, d_in, d_out, int(scale_kind), _ptr(blob), blob.numel(),
@@ -700,7 +715,7 @@ def w4a4_fp8_pack_codes(codes: torch.Tensor, scales: torch.Tensor, stream=None) 
     if tuple(scales.shape) != want:
         raise ValueError(f"scales must be {want}, got {tuple(scales.shape)}")
     kind = W4A4_FP8_SCALE_F32 if scales.dtype == torch.float32 else W4A4_FP8_SCALE_E8M0
-    blob = torch.empty(w4a4_fp8_packed_size(n_mat, d_in, d_out), dtype=torch.uint8, device=codes.device)
+    blob = _written_on(torch.empty(w4a4_fp8_packed_size(n_mat, d_in, d_out), dtype=torch.uint8, device=codes.device), stream)
     desc = W4A4Fp8Packed()
     _check("w4a4_fp8_pack_codes",
            lib().w4a4_fp8_pack_codes(_ptr(codes), _ptr(scales), n_mat, d_in, d_out, kind, _ptr(blob), blob.numel(),

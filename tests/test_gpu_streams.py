@@ -42,3 +42,39 @@ def test_two_streams_match_sequential():
         assert bool(torch.equal(a[3].view(torch.int32), ya.view(torch.int32))), f"stream A, repetition {rep}"
         assert bool(torch.equal(b[3].view(torch.int32), yb.view(torch.int32))), f"stream B, repetition {rep}"
     _banner("  5 repetitions bit-identical to the sequential calls")
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_packing_on_another_stream(raw):
+    """Packed on a stream while the current one still works in memory that it has freed since: that
+    work is not disturbed, and the packed buffer's memory is not given out again before the stream
+    is done with it."""
+    _banner(f"packing on another stream, raw handle {raw}")
+    W = torch.randn(2048, 4096, device="cuda")
+    want = B.w4a4_fp8_pack_weights(W).blob.clone()
+    a = torch.randn(4096, 4096, device="cuda", dtype=torch.bfloat16)
+    c = torch.empty_like(a)
+
+    def busy():
+        for _ in range(60):
+            torch.mm(a, a, out=c)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.full((want.numel(),), 7, dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(old)
+    torch.cuda.synchronize()
+    busy()
+    out.copy_(old)
+    del old
+    p = B.w4a4_fp8_pack_weights(W, stream=s.cuda_stream if raw else s)
+    torch.cuda.synchronize()
+    assert bool((out == 7).all()) and torch.equal(p.blob, want)
+    with torch.cuda.stream(s):
+        busy()
+    p = B.w4a4_fp8_pack_weights(W, stream=s.cuda_stream if raw else s)
+    ptr = p.blob.data_ptr()
+    del p
+    new = torch.empty_like(out)
+    assert new.data_ptr() != ptr
+    torch.cuda.synchronize()
