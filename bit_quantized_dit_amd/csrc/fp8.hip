@@ -25,17 +25,31 @@ __device__ __forceinline__ uint4 encode_piece(const float* x, float s, const Inv
     return make_uint4(a.x, a.y, b.x, b.y);
 }
 
+// A launch counts its work items in 32 bits, which 64 GiB of codes already exceed; longer work runs
+// as launches of this many workgroups, which the kernels number from `first` on (a GiB of codes or
+// more each, so that their starts do not count).
+constexpr int64_t SLICE = 1 << 18;
+template <typename F>
+hipError_t in_slices(int64_t workgroups, const F& launch) {
+    for (int64_t first = 0; first < workgroups; first += SLICE) {
+        launch(dim3((uint32_t)(workgroups - first < SLICE ? workgroups - first : SLICE)), first);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // Activations.  A wavefront takes 16 tokens x one block of 128 inputs, one run of the packed order:
 // lane l holds the 32 inputs that it has in the matrix instructions (token l % 16, inputs
 // 32 q + 8 (l / 16) .. + 7), so that the two stores write one KiB each.
 template <typename X>
 __global__ __launch_bounds__(256) void fp8_actquant_kernel(const X* __restrict__ x, int64_t T, int64_t d_in, int64_t nkb,
-                                                           int64_t items, int kind, uint8_t* __restrict__ aq,
+                                                           int64_t first, int64_t items, int kind, uint8_t* __restrict__ aq,
                                                            float* __restrict__ as, int64_t t_ld, int32_t* __restrict__ count) {
-    if (count && blockIdx.x == 0)   // the product's counters
+    if (count && first + blockIdx.x == 0)   // the product's counters
         for (int i = threadIdx.x; i < FP8_COUNTERS; i += 256) count[i] = 0;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t item = (first + blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (item >= items) return;
     const int64_t tg = item / nkb, kb = item - tg * nkb;
     const int64_t t = tg * 16 + r;
@@ -66,10 +80,10 @@ __global__ __launch_bounds__(FP8_COUNTERS) void fp8_clear_kernel(int32_t* __rest
 // Weights: one workgroup per 128 x 128 block; thread = (row, half of the block's inputs).
 template <typename W>
 __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, int64_t d_in, int64_t d_out, int64_t nkb,
-                                                       int64_t nnb, int64_t n_pad, int kind, uint8_t* __restrict__ codes,
-                                                       float* __restrict__ scales) {
+                                                       int64_t nnb, int64_t n_pad, int64_t first, int kind,
+                                                       uint8_t* __restrict__ codes, float* __restrict__ scales) {
     __shared__ uint32_t wmax[4];
-    const int64_t b = blockIdx.x;
+    const int64_t b = first + blockIdx.x;
     const int64_t mat = b / (nnb * nkb), nb = (b / nkb) % nnb, kb = b % nkb;
     const int64_t row = nb * 128 + (threadIdx.x >> 1);
     const int64_t p0 = kb * 128 + (threadIdx.x & 1) * 64;
@@ -105,9 +119,9 @@ __global__ __launch_bounds__(256) void fp8_pack_kernel(const W* __restrict__ w, 
 
 // Codes of a checkpoint, row-major, into the packed order: one thread per 16-byte piece.
 __global__ __launch_bounds__(256) void fp8_reorder_kernel(const uint8_t* __restrict__ src, int64_t d_in, int64_t d_out,
-                                                          int64_t nkb, int64_t n_pad, int64_t pieces, int vec,
-                                                          uint8_t* __restrict__ codes) {
-    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                          int64_t nkb, int64_t n_pad, int64_t first, int64_t pieces,
+                                                          int vec, uint8_t* __restrict__ codes) {
+    const int64_t q = (first + blockIdx.x) * 256 + threadIdx.x;
     if (q >= pieces) return;
     const int l = (int)(q & 63), h = (int)((q >> 6) & 1);
     const int64_t run = q >> 7;                       // 16 rows x 128 inputs
@@ -132,9 +146,9 @@ __global__ __launch_bounds__(256) void fp8_reorder_kernel(const uint8_t* __restr
     *reinterpret_cast<uint4*>(codes + q * 16) = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
 }
 
-__global__ __launch_bounds__(256) void fp8_scales_kernel(const void* __restrict__ src, int64_t n, int kind,
+__global__ __launch_bounds__(256) void fp8_scales_kernel(const void* __restrict__ src, int64_t first, int64_t n, int kind,
                                                          float* __restrict__ scales) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;
     if (i >= n) return;
     if (kind == W4A4_FP8_SCALE_F32) {
         scales[i] = reinterpret_cast<const float*>(src)[i];
@@ -149,14 +163,14 @@ __global__ __launch_bounds__(256) void fp8_scales_kernel(const void* __restrict_
 hipError_t launch_fp8_actquant(const void* X, int x_dtype, int64_t T, int64_t d_in, int kind, uint8_t* aq, float* as,
                                int64_t t_ld, int32_t* count, hipStream_t st) {
     const int64_t nkb = (d_in + 127) / 128, items = (T + 15) / 16 * nkb;
-    const dim3 grid((uint32_t)((items + 3) / 4));
-    if (x_dtype == W4A4_X_BF16)
-        hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, items, kind, aq, as, t_ld,
-                           count);
-    else
-        hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, items, kind, aq, as, t_ld,
-                           count);
-    return hipGetLastError();
+    return in_slices((items + 3) / 4, [&](dim3 grid, int64_t first) {
+        if (x_dtype == W4A4_X_BF16)
+            hipLaunchKernelGGL(fp8_actquant_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)X, T, d_in, nkb, first, items, kind,
+                               aq, as, t_ld, count);
+        else
+            hipLaunchKernelGGL(fp8_actquant_kernel<float>, grid, dim3(256), 0, st, (const float*)X, T, d_in, nkb, first, items, kind, aq, as,
+                               t_ld, count);
+    });
 }
 
 hipError_t launch_fp8_clear(int32_t* count, hipStream_t st) {
@@ -167,27 +181,28 @@ hipError_t launch_fp8_clear(int32_t* count, hipStream_t st) {
 hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d, uint8_t* codes, float* scales,
                            hipStream_t st) {
     const int64_t nkb = d.k_pad / 128, nnb = (d.d_out + 127) / 128;
-    const dim3 grid((uint32_t)(d.n_mat * nnb * nkb));
-    if (w_dtype == W4A4_X_BF16)
-        hipLaunchKernelGGL(fp8_pack_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)W, d.d_in, d.d_out, nkb, nnb,
-                           d.n_pad, d.scale_kind, codes, scales);
-    else
-        hipLaunchKernelGGL(fp8_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)W, d.d_in, d.d_out, nkb, nnb,
-                           d.n_pad, d.scale_kind, codes, scales);
-    return hipGetLastError();
+    return in_slices(d.n_mat * nnb * nkb, [&](dim3 grid, int64_t first) {
+        if (w_dtype == W4A4_X_BF16)
+            hipLaunchKernelGGL(fp8_pack_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t*)W, d.d_in, d.d_out, nkb, nnb, d.n_pad,
+                               first, d.scale_kind, codes, scales);
+        else
+            hipLaunchKernelGGL(fp8_pack_kernel<float>, grid, dim3(256), 0, st, (const float*)W, d.d_in, d.d_out, nkb, nnb, d.n_pad, first,
+                               d.scale_kind, codes, scales);
+    });
 }
 
 hipError_t launch_fp8_reorder(const uint8_t* src, const void* src_scales, const w4a4_fp8_packed& d, uint8_t* codes,
                               float* scales, hipStream_t st) {
     const int64_t nkb = d.k_pad / 128, pieces = d.n_mat * d.n_pad * d.k_pad / 16;
-    hipLaunchKernelGGL(fp8_reorder_kernel, dim3((uint32_t)((pieces + 255) / 256)), dim3(256), 0, st, src, d.d_in, d.d_out, nkb,
-                       d.n_pad, pieces, d.d_in % 8 == 0 ? 1 : 0, codes);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = in_slices((pieces + 255) / 256, [&](dim3 grid, int64_t first) {
+        hipLaunchKernelGGL(fp8_reorder_kernel, grid, dim3(256), 0, st, src, d.d_in, d.d_out, nkb, d.n_pad, first, pieces,
+                           d.d_in % 8 == 0 ? 1 : 0, codes);
+    });
     if (e != hipSuccess) return e;
     const int64_t n = d.n_mat * ((d.d_out + 127) / 128) * nkb;
-    hipLaunchKernelGGL(fp8_scales_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, src_scales, n, d.scale_kind,
-                       scales);
-    return hipGetLastError();
+    return in_slices((n + 255) / 256, [&](dim3 grid, int64_t first) {
+        hipLaunchKernelGGL(fp8_scales_kernel, grid, dim3(256), 0, st, src_scales, first, n, d.scale_kind, scales);
+    });
 }
 
 }  // namespace w4a4

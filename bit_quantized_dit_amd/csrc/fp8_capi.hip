@@ -10,7 +10,11 @@ using namespace w4a4;
 
 namespace {
 
-constexpr int64_t kMaxBlocks = ((int64_t)1 << 31) - 1;   // workgroups of a launch
+constexpr int64_t kMaxRuns = ((int64_t)1 << 31) - 1;      // runs of 16 rows x 128 inputs: 4 TiB of codes
+constexpr int64_t kMaxT = (int64_t)1 << 33;
+// 256 x 256 tiles of outputs: a launch counts its work items, 512 a tile, in 32 bits (4096: room for
+// the parts of a last round)
+constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 4096;
 
 bool valid_x(int t) { return t == W4A4_X_F32 || t == W4A4_X_BF16; }
 bool valid_y(int t) { return t == W4A4_Y_F32 || t == W4A4_Y_BF16; }
@@ -19,8 +23,7 @@ bool valid_kind(int k) { return k == W4A4_FP8_SCALE_F32 || k == W4A4_FP8_SCALE_E
 int check_dims(int64_t n_mat, int64_t d_in, int64_t d_out) {
     if (n_mat <= 0 || d_in <= 0 || d_out <= 0) return W4A4_ERR_INVALID;
     if (d_in > W4A4_FP8_MAX_D || d_out > W4A4_FP8_MAX_D || n_mat > 65535) return W4A4_ERR_SHAPE;
-    // packing runs one workgroup per 4 KiB of codes or 128 x 128 block
-    if (n_mat * (round_up(d_out, 16) / 16) * (round_up(d_in, 128) / 128) > kMaxBlocks) return W4A4_ERR_SHAPE;
+    if (n_mat * (round_up(d_out, 16) / 16) * (round_up(d_in, 128) / 128) > kMaxRuns) return W4A4_ERR_SHAPE;
     return W4A4_OK;
 }
 
@@ -50,10 +53,7 @@ int check_layer(int64_t T, const w4a4_fp8_packed* d) {
     const int st = check_packed(d);
     if (st) return st;
     if (d->n_mat != 1) return W4A4_ERR_INVALID;
-    // one workgroup per 128 x 128 outputs, one wavefront per 16 tokens x 128 inputs
-    if (T > kMaxBlocks * 4 || (T + 127) / 128 * ((d->d_out + 127) / 128) > kMaxBlocks ||
-        ((T + 15) / 16 * (d->k_pad / 128) + 3) / 4 > kMaxBlocks)
-        return W4A4_ERR_SHAPE;
+    if (T > kMaxT || (T + 255) / 256 * ((d->d_out + 255) / 256) > kMaxTiles) return W4A4_ERR_SHAPE;
     return W4A4_OK;
 }
 

@@ -178,3 +178,12 @@ def test_plans(L):
         assert out.count - out.partial == tiles * floats * 4, (T, d_in, d_out)
         assert out.total - out.count == (2048 if T <= 64 and tiles else 0)
     assert L.w4a4_fp8_workspace_layout(0, _packed(1, 13824, 5120), out) == 0 and out.total == 0
+
+
+def test_sizes_that_a_launch_cannot_count(L):
+    """Refused with a status of their own before anything reaches the device."""
+    out = B.W4A4Fp8WsLayout()
+    assert L.w4a4_fp8_workspace_layout(1 << 30, _packed(1, 1, 256), out) == 0
+    assert L.w4a4_fp8_workspace_layout(1 << 31, _packed(1, 1, 256), out) == 2
+    assert L.w4a4_fp8_workspace_layout((1 << 33) + 1, _packed(1, 1, 1), out) == 2
+    assert B.w4a4_fp8_packed_size(4096, 1 << 20, 16) == (1 << 36) + (1 << 27)

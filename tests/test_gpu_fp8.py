@@ -320,3 +320,28 @@ def test_codes_of_one_call_serve_several_layers(T, d, ns):
                 y = torch.full((T, ns[i]), float("nan"), device="cuda")
                 B.w4a4_fp8_gemm_prequantized(ws, T, layers[i], y)
                 assert torch.equal(y, want[i])
+
+
+def test_work_of_several_launches():
+    """Checkpoint codes, weights and activations of more workgroups than one launch takes."""
+    codes = torch.randint(0, 256, (3, 20480, 18000), dtype=torch.uint8, device="cuda")
+    print("fp8 several launches: codes", flush=True)
+    p = B.w4a4_fp8_pack_codes(codes, torch.ones(3, 160, 141, device="cuda"))
+    assert torch.equal(p.views()["codes"], codes)
+    del p, codes
+    W = torch.randn(300, 16, 1 << 17, device="cuda", dtype=BF16)
+    print("fp8 several launches: weights", flush=True)
+    v, w = B.w4a4_fp8_pack_weights(W).views(), B.w4a4_fp8_pack_weights(W[200:].contiguous()).views()
+    assert torch.equal(v["codes"][200:], w["codes"]) and torch.equal(v["scales"][200:], w["scales"])
+    del v, w, W
+    T = (1 << 24) + 100
+    x = torch.randn(T, 1, device="cuda")
+    layer = B.w4a4_fp8_pack_weights(torch.randn(1, 1, device="cuda"))
+    Y = torch.empty(T, 1, device="cuda")
+    print("fp8 several launches: activations", flush=True)
+    B.w4a4_fp8_linear(x, layer, Y, B.alloc_workspace_fp8(T, layer))
+    for t0 in range(0, T, 1 << 22):
+        part = x[t0:t0 + (1 << 22)].contiguous()
+        y = torch.empty_like(part)
+        B.w4a4_fp8_linear(part, layer, y, B.alloc_workspace_fp8(part.shape[0], layer))
+        assert torch.equal(Y[t0:t0 + (1 << 22)], y)
