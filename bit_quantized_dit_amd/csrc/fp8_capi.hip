@@ -71,31 +71,31 @@ w4a4_fp8_ws_layout ws_layout(int64_t T, const w4a4_fp8_packed* d) {
     return w;
 }
 
-int check_quantize(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* d, const void* ws, size_t ws_bytes) {
+int check_quantize(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* d, const void* ws, size_t ws_bytes,
+                   w4a4_fp8_ws_layout* w) {
     const int st = check_layer(T, d);
     if (st) return st;
     if (!X || !ws || !valid_x(x_dtype)) return W4A4_ERR_INVALID;
     if (misaligned(X) || misaligned(ws)) return W4A4_ERR_ALIGN;
-    return ws_bytes < ws_layout(T, d).total ? W4A4_ERR_SHAPE : W4A4_OK;
+    *w = ws_layout(T, d);
+    return ws_bytes < w->total ? W4A4_ERR_SHAPE : W4A4_OK;
 }
 
 // The product's counters, which have to be zero when it starts; null where its plan has none.
-int32_t* counters(int64_t T, const w4a4_fp8_packed* d, void* ws) {
-    const w4a4_fp8_ws_layout w = ws_layout(T, d);
+int32_t* counters(const w4a4_fp8_ws_layout& w, void* ws) {
     return w.total > w.count ? (int32_t*)((uint8_t*)ws + w.count) : nullptr;
 }
 // The codes and scales of checked arguments; clears `count` too.
-int quantize(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* d, void* ws, int32_t* count, hipStream_t stream) {
-    const w4a4_fp8_ws_layout w = ws_layout(T, d);
+int quantize(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* d, const w4a4_fp8_ws_layout& w, void* ws, int32_t* count,
+             hipStream_t stream) {
     uint8_t* b = (uint8_t*)ws;
     return dev_status(launch_fp8_actquant(X, x_dtype, T, d->d_in, d->scale_kind, b + w.a_q, (float*)(b + w.a_s), t_ld_of(T), count, stream));
 }
 // The product of checked arguments.
-int multiply(void* ws, int64_t T, const w4a4_fp8_packed* d, void* Y, int y_dtype, hipStream_t stream) {
-    const w4a4_fp8_ws_layout w = ws_layout(T, d);
+int multiply(const w4a4_fp8_ws_layout& w, void* ws, int64_t T, const w4a4_fp8_packed* d, void* Y, int y_dtype, hipStream_t stream) {
     uint8_t* b = (uint8_t*)ws;
     return dev_status(launch_fp8_gemm(b + w.a_q, (const float*)(b + w.a_s), T, t_ld_of(T), *d, Y, y_dtype, (float*)(b + w.partial),
-                                      (int32_t*)(b + w.count), stream));
+                                      counters(w, ws), stream));
 }
 
 int describe(int64_t n_mat, int64_t d_in, int64_t d_out, int kind, void* blob, size_t blob_bytes, w4a4_fp8_packed* out) {
@@ -206,9 +206,10 @@ int w4a4_fp8_workspace_size(int64_t T, const w4a4_fp8_packed* desc, size_t* byte
 
 int w4a4_fp8_quantize_activations(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc, void* ws, size_t ws_bytes,
                                   void* stream) {
-    const int st = check_quantize(X, x_dtype, T, desc, ws, ws_bytes);
+    w4a4_fp8_ws_layout w;
+    const int st = check_quantize(X, x_dtype, T, desc, ws, ws_bytes, &w);
     if (st || T == 0) return st;
-    return quantize(X, x_dtype, T, desc, ws, nullptr, (hipStream_t)stream);
+    return quantize(X, x_dtype, T, desc, w, ws, nullptr, (hipStream_t)stream);
 }
 
 int w4a4_fp8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_fp8_packed* desc, void* Y, int y_dtype,
@@ -217,24 +218,26 @@ int w4a4_fp8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_
     if (st) return st;
     if (!Y || !ws || !valid_y(y_dtype)) return W4A4_ERR_INVALID;
     if (misaligned(Y) || misaligned(ws)) return W4A4_ERR_ALIGN;
-    if (ws_bytes < ws_layout(T, desc).total) return W4A4_ERR_SHAPE;
+    const w4a4_fp8_ws_layout w = ws_layout(T, desc);
+    if (ws_bytes < w.total) return W4A4_ERR_SHAPE;
     if (T == 0) return W4A4_OK;
     // the codes may come from a call for another layer, whose workspace has its counters elsewhere or none
-    if (int32_t* const count = counters(T, desc, ws)) {
+    if (int32_t* const count = counters(w, ws)) {
         const hipError_t e = launch_fp8_clear(count, (hipStream_t)stream);
         if (e != hipSuccess) return dev_status(e);
     }
-    return multiply(ws, T, desc, Y, y_dtype, (hipStream_t)stream);
+    return multiply(w, ws, T, desc, Y, y_dtype, (hipStream_t)stream);
 }
 
 int w4a4_fp8_linear(const void* X, int x_dtype, int64_t T, const w4a4_fp8_packed* desc, void* Y, int y_dtype, void* ws,
                     size_t ws_bytes, void* stream) {
     if (!Y || !valid_y(y_dtype)) return W4A4_ERR_INVALID;
     if (misaligned(Y)) return W4A4_ERR_ALIGN;
-    const int st = check_quantize(X, x_dtype, T, desc, ws, ws_bytes);
+    w4a4_fp8_ws_layout w;
+    const int st = check_quantize(X, x_dtype, T, desc, ws, ws_bytes, &w);
     if (st || T == 0) return st;
-    const int q = quantize(X, x_dtype, T, desc, ws, counters(T, desc, ws), (hipStream_t)stream);
-    return q ? q : multiply(ws, T, desc, Y, y_dtype, (hipStream_t)stream);
+    const int q = quantize(X, x_dtype, T, desc, w, ws, counters(w, ws), (hipStream_t)stream);
+    return q ? q : multiply(w, ws, T, desc, Y, y_dtype, (hipStream_t)stream);
 }
 
 int w4a4_moe_workspace_layout(int64_t T, const w4a4_moe* moe, w4a4_moe_ws_layout* out) {
