@@ -345,3 +345,88 @@ def test_work_of_several_launches():
         y = torch.empty_like(part)
         B.w4a4_fp8_linear(part, layer, y, B.alloc_workspace_fp8(part.shape[0], layer))
         assert torch.equal(Y[t0:t0 + (1 << 22)], y)
+
+
+@pytest.mark.parametrize("kind,yt", [(0, BF16), (1, BF16), (0, F32), (1, F32)])
+def test_whole_tiles_and_a_split_last_round(kind, yt):
+    """17 x 17 large tiles, ragged both ways: 256 run whole and 33 in two ranges of their inputs."""
+    w = (np.random.default_rng(120).standard_normal((4300, 1100), np.float32) * np.float32(0.02))
+    x = _x(4100, 1100, BF16, 121)
+    x[4099, 1099] = np.nan               # in the last range of a split tile
+    y = _check(x, BF16, w, kind, yt)
+    assert np.isnan(y[4099]).all() and np.isfinite(y[:4099]).all()
+
+
+# Small tiles whole and with split inputs, large tiles whole, large tiles whole and split.
+TILES = [(1100, 700, 300), (1100, 1300, 300), (4100, 300, 4300), (4100, 1100, 4300)]
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("T,d,n", TILES)
+def test_special_values_in_tiles(T, d, n, kind):
+    """Zero blocks, blocks at the scale's floor, the largest values, NaN and infinite tokens and weights
+    through the FP8 instructions, scaled by them or after them."""
+    x = _x(T, d, F32, 130)
+    w = (np.random.default_rng(131).standard_normal((n, d), np.float32) * np.float32(0.02))
+    x[0, :128], x[0, 128:256] = 0, 1e-42
+    x[1] = 0
+    x[2] = np.float32(2.0 ** -130)
+    x[3, 5], x[T - 1, 130] = 3.0e38, -3.0e38
+    w[:128, :128] = 0
+    y = _check(x, F32, w, kind, BF16)
+    assert np.isfinite(y).all() and not y[1:3].any()
+    x[7, 200], x[T // 2, 1], x[T - 2, d - 1] = np.nan, np.inf, -np.inf
+    w[140, 129] = np.nan
+    y2 = _check(x, F32, w, kind, BF16)
+    tok, out = np.ones(T, bool), np.ones(n, bool)
+    tok[[7, T // 2, T - 2]], out[128:256] = False, False
+    assert np.array_equal(y2[np.ix_(tok, out)], y[np.ix_(tok, out)]) and np.isnan(y2[~tok]).all() and np.isnan(y2[:, ~out]).all()
+
+
+@pytest.mark.parametrize("T", [20, 1100])
+def test_checkpoint_of_every_code_and_wide_scales(T):
+    """NaN codes make their own outputs NaN and no other; E8M0 scales from 2^-60 to 2^60 and NaN."""
+    rng = np.random.default_rng(140)
+    n, d = 300, 700
+    codes = rng.integers(0, 256, (n, d)).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0x38
+    codes[17, 333], codes[290, 5] = 0x7F, 0xFF
+    e8 = rng.integers(67, 188, (3, 6)).astype(np.uint8)
+    e8[1, 2] = 255
+    sc = np.where(e8 == 255, np.nan, 2.0 ** (e8.astype(np.float64) - 127)).astype(np.float32)
+    p = B.w4a4_fp8_pack_codes(torch.from_numpy(codes).cuda(), torch.from_numpy(e8).cuda())
+    x = _x(T, d, BF16, 141)
+    rq, rs = R.quantize_rows(x, 1)
+    for yt in (F32, BF16):
+        print(f"fp8 checkpoint T={T} y={yt}", flush=True)
+        Y = torch.empty(T, n, dtype=yt, device="cuda")
+        B.w4a4_fp8_linear(torch.from_numpy(x).to(BF16).cuda(), p, Y, B.alloc_workspace_fp8(T, p))
+        ref, tol = R.product(R.dequant_rows(rq, rs)[:, :d], R.dequant_blocks(codes, sc), yt == BF16 and T > 64)
+        R.close(Y.double().cpu().numpy(), ref, tol + (R.BF16_U * (np.abs(ref) + tol) if yt == BF16 else 0), "Y")
+        nan = np.isnan(ref)
+        assert nan[:, [17, 290]].all() and nan[:, 128:256].all() and not np.delete(nan, [17, 290] + list(range(128, 256)), 1).any()
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("d", [128, 1024, 13824])
+@pytest.mark.parametrize("heavy", [False, True])
+def test_error_of_the_fp8_instructions(d, heavy, kind):
+    """bf16 outputs of many tokens: what the FP8 instructions drop, seen in the share of outputs that are not the
+    bf16 number nearest to the exact one.  An error of rms e (relative to the outputs' rms) moves an output across a
+    rounding midpoint with probability at most |error| / ulp <= 256 |error| / |y|, on average over normal outputs at
+    most 0.8 a (1.06 - ln a) with a = 256 e: 2% for e = 1.4e-5 (normal inputs), 5% for e = 4e-5 (inputs with heavy
+    channels).  d = 13824 runs 108 blocks through one accumulator (256 whole tiles)."""
+    T, n = 4096, 4096
+    X = torch.from_numpy(_x(T, d, BF16, 150, heavy)).to(BF16).cuda()
+    layer = B.w4a4_fp8_pack_weights(torch.randn(n, d, device="cuda", generator=torch.Generator("cuda").manual_seed(151)) * 0.02, kind)
+    ws, Y = B.alloc_workspace_fp8(T, layer), torch.empty(T, n, dtype=BF16, device="cuda")
+    print(f"fp8 error d={d} heavy={heavy} kind={kind}", flush=True)
+    B.w4a4_fp8_linear(X, layer, Y, ws)
+    v, p = B.workspace_fp8_views(ws, T, layer), layer.views()
+    rows = slice(3, None, 16)
+    a = R.dequant_rows(v["A_q"][rows].cpu().numpy(), v["A_s"][rows].cpu().numpy())[:, :d]
+    y = a @ R.dequant_blocks(p["codes"][0].cpu().numpy(), p["scales"][0].cpu().numpy()).T
+    near = torch.from_numpy(y).to(torch.float32).to(BF16)
+    share = float((Y[rows].cpu() != near).double().mean())
+    print(f"not the nearest: {share:.4%}", flush=True)
+    assert share <= (0.05 if heavy else 0.02)

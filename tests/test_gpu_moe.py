@@ -257,3 +257,48 @@ def test_workspace_used_again_with_other_tokens(T, d, f, E, k):
     for i in (0, 1, 2, 1, 0, 2, 0, 2, 1):
         B.w4a4_moe_forward(xs[i], layer, Y, ws)
         assert torch.equal(Y, want[i])
+
+
+# Many tokens in passes of four tokens (T k <= E) and eight (T k <= 3 E), found by slots (T k < E <= 256)
+# or by counting; down steps for 17 to 64 and 65 to 128 tokens, whole tiles and divided ones; the
+# most experts, pairs and segments that a call may have.
+NARROW = [(40, 130, 72, 64, 1), (40, 260, 1600, 64, 4), (64, 130, 72, 300, 4), (24, 264, 500, 64, 6), (100, 200, 100, 128, 1),
+          (100, 260, 1600, 128, 3), (65, 128, 900, 256, 8), (128, 40, 24, 1024, 8), (128, 40, 24, 1024, 24), (128, 40, 24, 1024, 32),
+          (20, 136, 64, 256, 12)]
+
+
+@pytest.mark.parametrize("skew", [False, True])
+@pytest.mark.parametrize("T,d,f,E,k", NARROW)
+def test_narrow_passes_of_many_tokens(T, d, f, E, k, skew):
+    """skew: one expert takes every token, in as many passes as they need."""
+    gated, renorm = T % 8 != 0, E % 3 != 0
+    router = (np.random.default_rng(T + k).standard_normal((E, d)) * 2 / np.sqrt(d)).astype(np.float32)
+    x = _tokens(T, d, BF16, 100)
+    if skew:
+        router[:, 0], x[:, 0] = 0, 1
+        router[E // 2, 0] = 30
+    layer, r, mats = _layer(d, f, E, k, gated, renorm, BF16, 101, router=router)
+    Y, v = _check(x, BF16, layer, r, mats, F32)
+    assert not skew or (v["ids"][:, 0] == E // 2).all()
+    X, ws, again = torch.from_numpy(x).to(BF16).cuda(), B.alloc_workspace_moe(T, layer), torch.empty_like(Y)
+    for _ in range(3):
+        again.fill_(float("nan"))
+        B.w4a4_moe_forward(X, layer, again, ws)
+        assert torch.equal(again, Y)
+    x[T // 3, 2] = np.nan
+    Y, v = _check(x, BF16, layer, r, mats, BF16)
+    assert v["ids"][T // 3].tolist() == list(range(k)) and bool(torch.isnan(Y[T // 3]).all()) and not bool(torch.isnan(Y[T // 3 + 1]).any())
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("T,E,k", [(2, 12, 3), (30, 12, 3), (40, 64, 1)])
+def test_infinite_tokens(T, E, k, gated):
+    """Infinities of both signs go through the formula (infinite and NaN h, a NaN row) and touch no
+    other token; logits that are all -Inf tie."""
+    router = (np.random.default_rng(110).standard_normal((E, 192)) / 7).astype(np.float32)
+    router[:, 20] = np.abs(router[:, 20]) + np.float32(0.01)
+    layer, r, mats = _layer(192, 64, E, k, gated, True, BF16, 111, router=router)
+    x = _tokens(T, 192, BF16, 112)
+    x[0, 17], x[1, 20] = np.inf, -np.inf
+    Y, v = _check(x, BF16, layer, r, mats, F32)
+    assert v["ids"][1].tolist() == list(range(k)) and bool(torch.isnan(Y[:2]).all()) and not bool(torch.isnan(Y[2:]).any())
