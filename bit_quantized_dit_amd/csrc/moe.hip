@@ -759,15 +759,16 @@ void down(const DownArgs& a, int wgs, hipStream_t st) {
 template <int XI>
 void run_down(const DownArgs& a, hipStream_t st) {
     if (a.T <= 16) return down<16, 8, XI, 1>(a, 512, st);
+    if (a.T > 64) return down<MAX_T, 8, XI, 1>(a, 256, st);
     if constexpr (XI == 4) {
         // two row tiles for one read of h, where its 16 tokens' rows are twice the codes of one (64
         // tokens, 6 of 64 experts, 1536 -> 5120: 145 to 120 us), where there are more tiles than workgroups
         // (37 tokens, 333 -> 1000: 11.4 us with two, 10.0 with one)
-        if (a.T <= 64 && a.d > 4096) return down<64, 16, XI, 2>(a, 256, st);
-        if (a.T <= 64) return down<64, 16, XI, 1>(a, 256, st);
+        if (a.d > 4096) return down<64, 16, XI, 2>(a, 256, st);
+        down<64, 16, XI, 1>(a, 256, st);
+    } else {
+        down<64, 8, XI, 1>(a, 512, st);
     }
-    if (a.T <= 64) return down<64, 8, XI, 1>(a, 512, st);
-    down<MAX_T, 8, XI, 1>(a, 256, st);
 }
 
 }  // namespace
