@@ -302,3 +302,10 @@ def test_infinite_tokens(T, E, k, gated):
     x[0, 17], x[1, 20] = np.inf, -np.inf
     Y, v = _check(x, BF16, layer, r, mats, F32)
     assert v["ids"][1].tolist() == list(range(k)) and bool(torch.isnan(Y[:2]).all()) and not bool(torch.isnan(Y[2:]).any())
+
+
+@pytest.mark.parametrize("xt,rt", [(F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("T,d", [(1, 256), (1, 131), (6, 131)])
+def test_tokens_and_router_of_different_types(T, d, xt, rt):
+    layer, r, mats = _layer(d, 48, 20, 4, True, False, rt, 120)
+    _check(_tokens(T, d, xt, 121), xt, layer, r, mats, BF16)
