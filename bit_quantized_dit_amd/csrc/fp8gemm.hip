@@ -18,7 +18,8 @@
 // products of a few inputs up with the largest one and drop what falls about 13 bits below
 // it: on Gaussian codes a block's sum is off by 1.4e-5 of its norm, with one heavy input by
 // 4e-5 (measured against exact sums).  For bf16 outputs that is a fiftieth of the final
-// rounding and the FP8 instructions run.  fp32 outputs, and few tokens (where the arithmetic
+// rounding and the FP8 instructions run: 1 to 3% of the outputs round to a neighbour of the bf16
+// number nearest to the exact sum, no more where E8M0's accumulators run through 108 blocks.  fp32 outputs, and few tokens (where the arithmetic
 // is free), take the codes widened to bf16, which is exact: bf16 products are exact in
 // binary32 and their sums are off by 1e-8.
 //
@@ -134,12 +135,15 @@ __device__ __forceinline__ void store_tiles(const v4f (&acc)[FT][FF], uint8_t* s
 // Tiles that would leave most CUs idle in a last round run as sp.n ranges of their blocks, whose
 // sums go to memory; fp8_reduce_kernel adds them in order.
 //
-// Measured: 57600 x 5120 -> 13824, bf16 outputs, 3.41 ms (2.39 PFLOP/s; the library's product with one
-// scale for each whole operand takes 2.76).  What shares a CU's LDS bounds it: the same loop takes 2.7 ms
-// without the copies into LDS, 2.1 without the fragment reads, 3.25 with a quarter of the scaling.
-// A second barrier and the copies in two halves changed nothing (3.64 against 3.62).  E8M0 scales in the
-// instruction: 4096 x 13824 -> 5120 in 263 us (library 210).  fp32 outputs run at the bf16
-// instructions' rate: 4096 x 5120 -> 13824 in 499 us, 1.16 PFLOP/s (library bf16 1.24).
+// Measured (this kernel alone, traced, clocks settled: the first twenty calls after a pause take a tenth
+// longer): 57600 x 5120 -> 13824, bf16 outputs, 3.39 ms (2.40 PFLOP/s; the library's product with one
+// scale for each whole operand takes 2.75).  What shares a CU's LDS bounds it: the same loop took 2.7 ms of
+// 3.4 without the copies into LDS, 2.1 without the fragment reads, 3.25 with a quarter of the scaling.
+// A second barrier and the copies in two halves changed nothing (0.5%).  E8M0 scales in the
+// instruction: 4096 x 13824 -> 5120 in 216 us (library 210).  fp32 outputs: 4096 x 5120 -> 13824 in
+// 457 us, 1.27 PFLOP/s, which is what the 16-row bf16 instruction gives alone (1.3; the 32-row form gives 2.3,
+// the library's bf16 product 1.24).  Registers: 222 with fp32 scales, 201 with E8M0; 256 and 12
+// bytes of scratch a lane with fp32 outputs.
 struct Split {
     float* part;
     uint32_t full, n;

@@ -21,11 +21,12 @@
 // Measured (us a call; "codes" is the time that the chosen experts' codes alone take at the 6.4 TB/s that a kernel
 // which only reads reaches on long arrays):
 //   1 token,   5120 x 1536 gated, 8 of 64 experts        42   (codes 30)
-//   8 tokens,  2048 x 768 gated, 8 of 128 experts        63   (codes 38)
-//   16 tokens, 5120 x 13824 GELU, 2 of 8 experts        195   (codes 177)
-//   64 tokens, 5120 x 1536 gated, 6 of 64 experts       262   (codes 235)
-// In the first two the three launches' starts and the first loads' latencies are the rest; in the last two
-// the memory is busy for about 90% of the up kernel and 80% of the down kernel.
+//   8 tokens,  2048 x 768 gated, 8 of 128 experts        61   (codes 38)
+//   16 tokens, 5120 x 13824 GELU, 2 of 8 experts        184   (codes 175)
+//   64 tokens, 5120 x 1536 gated, 6 of 64 experts       259   (codes 236)
+// (on a slower card of the same kind 43, 64, 196, 258).  In the first two the three launches' starts and
+// the first loads' latencies are the rest; in the last two the up kernel reads at 99% of that
+// rate and the down kernel at 86 to 95%.
 #include "fp8_device.h"
 #include "w4a4_internal.h"
 
@@ -727,9 +728,12 @@ void run_logits(const void* X_, const w4a4_moe& m, int T, bool copy, float* logi
 // that it has on average: a second pass reads the codes again, a wider one reads more of the other
 // operand than there is.  Passes of 4, 8, 16 and 32 tokens, us a call, 2048 x 768 gated, 8 of 64 experts:
 //   8 tokens 58, 56, 57, 62;  16: 70, 62, 62, 67;  32: 95, 73, 67, 72;  64: 146, 104, 77, 80;
-// 64 tokens, 8 of 32 experts: 125, 86, 65, 58; 16 tokens, 5120 x 13824, 2 of 8 experts, 8 or 16 a pass: 196, 223; 40
-// tokens, 5120 x 1024 gated, 6 of 64 experts: 188, 181 (above 16 tokens, 16 a pass go with the down step's
-// two row tiles).
+// 64 tokens, 8 of 32 experts: 125, 86, 65, 58.  Between three and four tokens an expert, 8 or 16 a pass:
+// above 16 tokens, where the down step then has 16 wavefronts a workgroup, 16 (24 tokens, 2048 x 768, 9 of 64 experts: 69, 63; 32 tokens, 8 of 64: 75, 65; 40 tokens,
+// 5120 x 1536, 6 of 64: 252, 246; 20 tokens, 4096 x 1024, 3 of 16: 52, 48; but 40 tokens, 1024 x 512, 3
+// of 32: 32, 35, and 32 tokens, 2880 x 2880, 4 of 32: 150, 158), up to 16 tokens, where it has 8
+// either way, 8 (16 tokens, 5120 x 13824 GELU, 2 of 8: 196, 223; 16 tokens, 5120 x 1536, 8 of 32:
+// 133, 140; 10 tokens, 5120 x 13824, 3 of 8: 274, 285; but 16 tokens, 2048 x 768, 4 of 16: 32, 30).
 struct Pass {
     int xi, nt;
 };

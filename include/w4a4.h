@@ -354,10 +354,12 @@ int w4a4_linear_noalloc(const void* X, int x_dtype, int64_t T, const w4a4_packed
  *   - Sums, and the products with the scales, are binary32, and fp32 outputs are those
  *     sums.  For bf16 outputs of more than 64 tokens the matrix instructions may take the
  *     codes as FP8 and drop what is 13 bits below the largest product beside it: 1.4e-5 to 4e-5
- *     of a sum, a fiftieth of the outputs' own rounding.  The product of two scales
+ *     of the outputs' root mean square, a fiftieth of their own rounding (1 to 3% of the
+ *     outputs round to a neighbour of the nearest bf16 number).  The product of two scales
  *     s_x s_w is taken first: with scales of a checkpoint it has to be a normal number.
  *   - The inputs are zero padded to k_pad = roundup(d_in, 128); 1 <= d_in <=
- *     W4A4_FP8_MAX_D, 1 <= d_out <= W4A4_FP8_MAX_D, any number of tokens.
+ *     W4A4_FP8_MAX_D, 1 <= d_out <= W4A4_FP8_MAX_D, any number of tokens whose outputs a
+ *     launch can count (2^33 tokens, 2^39 outputs; W4A4_ERR_SHAPE above).
  * The conventions at the top of this file hold: caller-owned buffers, 16-byte aligned
  * device pointers, T = 0 a no-op, no allocation or synchronisation, graph capture.
  * Calls are bit-reproducible for a given shape. */
