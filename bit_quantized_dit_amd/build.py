@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a4.so")
 SOURCES = ["capi.hip", "calib.hip", "pack.hip", "actprep.hip", "gemm.hip", "gelu.hip", "search.hip", "dynamic.hip",
-           "fp8_capi.hip", "fp8.hip", "fp8gemm.hip", "moe.hip"]
+           "fp8_capi.hip", "fp8.hip", "fp8gemm.hip", "moe.hip", "int8_capi.hip", "int8.hip", "int8gemm.hip",
+           "kv_capi.hip", "kv.hip", "kvattn.hip"]
 
 # Numerics-relevant flags: IEEE binary32 division, fp32 subnormals kept, no FMA
 # contraction, no fast-math; packed-fp32 instructions disabled.

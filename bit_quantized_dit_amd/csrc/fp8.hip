@@ -191,15 +191,19 @@ hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d,
     });
 }
 
+hipError_t launch_reorder_codes(const uint8_t* src, int64_t n_mat, int64_t d_in, int64_t d_out, uint8_t* codes, hipStream_t st) {
+    const int64_t nkb = (d_in + 127) / 128, n_pad = (d_out + 15) / 16 * 16, pieces = n_mat * n_pad * nkb * 8;
+    return in_slices((pieces + 255) / 256, [&](dim3 grid, int64_t first) {
+        hipLaunchKernelGGL(fp8_reorder_kernel, grid, dim3(256), 0, st, src, d_in, d_out, nkb, n_pad, first, pieces,
+                           d_in % 8 == 0 ? 1 : 0, codes);
+    });
+}
+
 hipError_t launch_fp8_reorder(const uint8_t* src, const void* src_scales, const w4a4_fp8_packed& d, uint8_t* codes,
                               float* scales, hipStream_t st) {
-    const int64_t nkb = d.k_pad / 128, pieces = d.n_mat * d.n_pad * d.k_pad / 16;
-    const hipError_t e = in_slices((pieces + 255) / 256, [&](dim3 grid, int64_t first) {
-        hipLaunchKernelGGL(fp8_reorder_kernel, grid, dim3(256), 0, st, src, d.d_in, d.d_out, nkb, d.n_pad, first, pieces,
-                           d.d_in % 8 == 0 ? 1 : 0, codes);
-    });
+    const hipError_t e = launch_reorder_codes(src, d.n_mat, d.d_in, d.d_out, codes, st);
     if (e != hipSuccess) return e;
-    const int64_t n = d.n_mat * ((d.d_out + 127) / 128) * nkb;
+    const int64_t n = d.n_mat * ((d.d_out + 127) / 128) * (d.k_pad / 128);
     return in_slices((n + 255) / 256, [&](dim3 grid, int64_t first) {
         hipLaunchKernelGGL(fp8_scales_kernel, grid, dim3(256), 0, st, src_scales, first, n, d.scale_kind, scales);
     });

@@ -79,6 +79,8 @@ hipError_t launch_fp8_pack(const void* W, int w_dtype, const w4a4_fp8_packed& d,
                            hipStream_t st);
 hipError_t launch_fp8_reorder(const uint8_t* src, const void* src_scales, const w4a4_fp8_packed& d, uint8_t* codes,
                               float* scales, hipStream_t st);
+// row-major bytes [n_mat][d_out][d_in] into the packed order (any 8-bit codes)
+hipError_t launch_reorder_codes(const uint8_t* src, int64_t n_mat, int64_t d_in, int64_t d_out, uint8_t* codes, hipStream_t st);
 // Plan of the product (host logic): tiles [0, full) whole, each later one as `split` ranges of the
 // inputs, whose fp32 sums take part_bytes of workspace.  `few`: the few-token kernel, which splits all
 // its tiles or none and counts the ranges done in FP8_COUNTERS counters.
@@ -103,5 +105,30 @@ struct MoeBuffers {
 };
 hipError_t launch_moe(const void* X, int x_dtype, int64_t T, const w4a4_moe& m, const MoeBuffers& b, void* Y, int y_dtype,
                       hipStream_t st);
+
+// INT8 layer (int8.hip, int8gemm.hip): codes and scales of rows (tokens, or weight rows with the
+// rows and scales past the last one zeroed up to a multiple of 16), the product
+hipError_t launch_int8_quant(const void* X, int x_dtype, int64_t rows, int64_t d_in, bool zero_past, uint8_t* q, float* s,
+                             int32_t* count, hipStream_t st);
+hipError_t launch_int8_scales(const float* src, int64_t n, int64_t n_pad, float* dst, hipStream_t st);
+constexpr int INT8_COUNTERS = 512;
+struct Int8Plan {
+    int64_t tiles, full;
+    int32_t split, rt;
+    bool few, big;
+    size_t part_bytes;
+};
+Int8Plan int8_plan(int64_t T, int64_t N, int64_t k_pad);
+hipError_t launch_int8_clear(int32_t* count, hipStream_t st);
+hipError_t launch_int8_gemm(const uint8_t* aq, const float* as, int64_t T, const w4a4_int8_packed& d, void* out, int y_dtype,
+                            int32_t* part, int32_t* count, hipStream_t st);
+
+// 4-bit key/value cache (kv.hip, kvattn.hip)
+hipError_t launch_kv_append(const w4a4_kv_rows& K, const w4a4_kv_rows& V, int64_t n_rows, const w4a4_kv_batch& b,
+                            const w4a4_kv_cache& c, hipStream_t st);
+hipError_t launch_kv_read(int64_t n_rows, const w4a4_kv_batch& b, const w4a4_kv_cache& c, void* K, void* V, int y_dtype, hipStream_t st);
+size_t kv_attention_ws(int64_t n_rows, const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads);
+hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads,
+                               float scale, bool causal, int64_t window, uint16_t* O, void* ws, hipStream_t st);
 
 }  // namespace w4a4

@@ -43,7 +43,11 @@ EXPORTS = ("w4a4_status_string", "w4a4_column_absmax", "w4a4_calibrate_scales", 
            "w4a4_linear_noalloc",
            "w4a4_fp8_packed_size", "w4a4_fp8_pack_weights", "w4a4_fp8_pack_codes", "w4a4_fp8_workspace_layout",
            "w4a4_fp8_workspace_size", "w4a4_fp8_quantize_activations", "w4a4_fp8_gemm_prequantized", "w4a4_fp8_linear",
-           "w4a4_moe_workspace_layout", "w4a4_moe_workspace_size", "w4a4_moe_forward")
+           "w4a4_moe_workspace_layout", "w4a4_moe_workspace_size", "w4a4_moe_forward",
+           "w4a4_int8_packed_size", "w4a4_int8_pack_weights", "w4a4_int8_pack_codes", "w4a4_int8_workspace_layout",
+           "w4a4_int8_workspace_size", "w4a4_int8_quantize_activations", "w4a4_int8_gemm_prequantized", "w4a4_int8_linear",
+           "w4a4_kv_cache_size", "w4a4_kv_cache_describe", "w4a4_kv_append", "w4a4_kv_read",
+           "w4a4_kv_attention_workspace_size", "w4a4_kv_attention")
 
 
 class W4A4Packed(ctypes.Structure):
@@ -95,6 +99,31 @@ class W4A4Moe(ctypes.Structure):
 class W4A4MoeWsLayout(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_size_t), ("xb", ctypes.c_size_t), ("ids", ctypes.c_size_t), ("p", ctypes.c_size_t),
                 ("h", ctypes.c_size_t), ("place", ctypes.c_size_t), ("count", ctypes.c_size_t), ("part", ctypes.c_size_t), ("total", ctypes.c_size_t)]
+
+
+class W4A4Int8Packed(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64), ("k_pad", ctypes.c_int64), ("n_pad", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class W4A4Int8WsLayout(ctypes.Structure):
+    _fields_ = [("a_q", ctypes.c_size_t), ("a_s", ctypes.c_size_t), ("partial", ctypes.c_size_t), ("count", ctypes.c_size_t),
+                ("total", ctypes.c_size_t)]
+
+
+class W4A4KvCache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int64), ("page_tokens", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("d_pad", ctypes.c_int32), ("block_bytes", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
+class W4A4KvBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int64), ("max_rows", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("pages", ctypes.c_void_p)]
+
+
+class W4A4KvRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class W4A4Error(RuntimeError):
@@ -154,6 +183,20 @@ def lib() -> ctypes.CDLL:
             "w4a4_moe_workspace_layout": (ci, [i64, P(W4A4Moe), P(W4A4MoeWsLayout)]),
             "w4a4_moe_workspace_size": (ci, [i64, P(W4A4Moe), P(sz)]),
             "w4a4_moe_forward": (ci, [vp, ci, i64, P(W4A4Moe), vp, ci, vp, sz, vp]),
+            "w4a4_int8_packed_size": (ci, [i64, i64, P(sz)]),
+            "w4a4_int8_pack_weights": (ci, [vp, ci, i64, i64, vp, sz, P(W4A4Int8Packed), vp]),
+            "w4a4_int8_pack_codes": (ci, [vp, vp, i64, i64, vp, sz, P(W4A4Int8Packed), vp]),
+            "w4a4_int8_workspace_layout": (ci, [i64, P(W4A4Int8Packed), P(W4A4Int8WsLayout)]),
+            "w4a4_int8_workspace_size": (ci, [i64, P(W4A4Int8Packed), P(sz)]),
+            "w4a4_int8_quantize_activations": (ci, [vp, ci, i64, P(W4A4Int8Packed), vp, sz, vp]),
+            "w4a4_int8_gemm_prequantized": (ci, [vp, sz, i64, P(W4A4Int8Packed), vp, ci, vp]),
+            "w4a4_int8_linear": (ci, [vp, ci, i64, P(W4A4Int8Packed), vp, ci, vp, sz, vp]),
+            "w4a4_kv_cache_size": (ci, [i64, i32, i32, i32, P(sz)]),
+            "w4a4_kv_cache_describe": (ci, [i64, i32, i32, i32, vp, sz, P(W4A4KvCache)]),
+            "w4a4_kv_append": (ci, [P(W4A4KvRows), P(W4A4KvRows), i64, P(W4A4KvBatch), P(W4A4KvCache), vp]),
+            "w4a4_kv_read": (ci, [i64, P(W4A4KvBatch), P(W4A4KvCache), vp, vp, ci, vp]),
+            "w4a4_kv_attention_workspace_size": (ci, [i64, P(W4A4KvBatch), P(W4A4KvCache), i32, P(sz)]),
+            "w4a4_kv_attention": (ci, [P(W4A4KvRows), i64, P(W4A4KvBatch), P(W4A4KvCache), i32, f32, ci, i64, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -854,3 +897,278 @@ def w4a4_moe_forward(X: torch.Tensor, layer: MoeLayer, Y: torch.Tensor, ws: torc
     st = lib().w4a4_moe_forward(_ptr(X), _x_dtype(X), T, ctypes.byref(layer.desc), _ptr(Y), dt, _ptr(ws), ws.numel(),
                                 _stream(stream))
     _check("w4a4_moe_forward", st)
+
+
+# --------------------------------------------------------------------------- INT8 layer
+
+def _here(t: torch.Tensor, name: str) -> None:
+    """The library launches on the current device."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+class PackedInt8:
+    """INT8 weights with a scale per output channel.  Keeps the device blob alive."""
+
+    def __init__(self, blob: torch.Tensor, desc: W4A4Int8Packed):
+        self.blob, self.desc = blob, desc
+
+    @property
+    def d_in(self) -> int: return self.desc.d_in
+    @property
+    def d_out(self) -> int: return self.desc.d_out
+    @property
+    def k_pad(self) -> int: return self.desc.k_pad
+    @property
+    def n_pad(self) -> int: return self.desc.n_pad
+
+    def views(self) -> dict:
+        """Copies of the packed arrays: codes int8 [d_out, d_in] (row-major) and scales float32 [d_out]."""
+        d = self.desc
+        off = d.scales - self.blob.data_ptr()
+        codes = untile_fp8(self.blob[:d.n_pad * d.k_pad], d.n_pad, d.k_pad).view(torch.int8)
+        return {"codes": codes[:d.d_out, :d.d_in].contiguous(), "scales": self.blob[off:off + 4 * d.d_out].view(torch.float32).clone()}
+
+
+def w4a4_int8_packed_size(d_in: int, d_out: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("w4a4_int8_packed_size", lib().w4a4_int8_packed_size(d_in, d_out, ctypes.byref(n)))
+    return n.value
+
+
+def w4a4_int8_pack_weights(W: torch.Tensor, stream=None) -> PackedInt8:
+    """W: float32 or bfloat16 [d_out, d_in]."""
+    _dev(W, "W")
+    _here(W, "W")
+    dt = _x_dtype(W)
+    if W.dim() != 2:
+        raise ValueError(f"W must be [d_out, d_in], got {tuple(W.shape)}")
+    d_out, d_in = W.shape
+    blob = _written_on(torch.empty(w4a4_int8_packed_size(d_in, d_out), dtype=torch.uint8, device=W.device), stream)
+    desc = W4A4Int8Packed()
+    _check("w4a4_int8_pack_weights",
+           lib().w4a4_int8_pack_weights(_ptr(W), dt, d_in, d_out, _ptr(blob), blob.numel(), ctypes.byref(desc), _stream(stream)))
+    return PackedInt8(blob, desc)
+
+
+def w4a4_int8_pack_codes(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> PackedInt8:
+    """Weights that are quantized already: codes int8 [d_out, d_in], scales float32 [d_out]."""
+    _dev(codes, "codes")
+    _dev(scales, "scales")
+    _here(codes, "codes")
+    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+        raise TypeError(f"codes must be int8 and scales float32, got {codes.dtype} and {scales.dtype}")
+    if codes.dim() != 2 or tuple(scales.shape) != (codes.shape[0],) or codes.device != scales.device:
+        raise ValueError("codes must be [d_out, d_in] and scales [d_out] on one device")
+    d_out, d_in = codes.shape
+    blob = _written_on(torch.empty(w4a4_int8_packed_size(d_in, d_out), dtype=torch.uint8, device=codes.device), stream)
+    desc = W4A4Int8Packed()
+    _check("w4a4_int8_pack_codes",
+           lib().w4a4_int8_pack_codes(_ptr(codes), _ptr(scales), d_in, d_out, _ptr(blob), blob.numel(), ctypes.byref(desc),
+                                      _stream(stream)))
+    return PackedInt8(blob, desc)
+
+
+def w4a4_int8_workspace_layout(T: int, packed: PackedInt8) -> W4A4Int8WsLayout:
+    out = W4A4Int8WsLayout()
+    _check("w4a4_int8_workspace_layout",
+           lib().w4a4_int8_workspace_layout(T, ctypes.byref(packed.desc), ctypes.byref(out)))
+    return out
+
+
+def w4a4_int8_workspace_size(T: int, packed: PackedInt8) -> int:
+    n = ctypes.c_size_t(0)
+    _check("w4a4_int8_workspace_size", lib().w4a4_int8_workspace_size(T, ctypes.byref(packed.desc), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_workspace_int8(T: int, packed: PackedInt8, device="cuda") -> torch.Tensor:
+    return torch.empty(max(w4a4_int8_workspace_size(T, packed), 256), dtype=torch.uint8, device=device)
+
+
+def workspace_int8_views(ws: torch.Tensor, T: int, packed: PackedInt8) -> dict:
+    """Copies of the quantized activations inside ws: A_q int8 [T, k_pad] (row-major) and A_s float32 [T]."""
+    L = w4a4_int8_workspace_layout(T, packed)
+    rows = (T + 15) // 16 * 16
+    return {"A_q": untile_fp8(ws[L.a_q:L.a_q + rows * packed.k_pad], rows, packed.k_pad)[:T].view(torch.int8),
+            "A_s": ws[L.a_s:L.a_s + 4 * T].view(torch.float32).clone()}
+
+
+def w4a4_int8_quantize_activations(X: torch.Tensor, packed: PackedInt8, ws: torch.Tensor, stream=None) -> None:
+    T = _acts(X, packed.d_in)
+    _here(X, "X")
+    _wsbuf(ws, X)
+    if T == 0:      # an empty tensor has no address
+        return
+    st = lib().w4a4_int8_quantize_activations(_ptr(X), _x_dtype(X), T, ctypes.byref(packed.desc), _ptr(ws), ws.numel(),
+                                              _stream(stream))
+    _check("w4a4_int8_quantize_activations", st)
+
+
+def w4a4_int8_gemm_prequantized(ws: torch.Tensor, T: int, packed: PackedInt8, Y: torch.Tensor, stream=None) -> None:
+    _dev(Y, "Y")
+    _here(Y, "Y")
+    dt = _y_dtype(Y, T, packed.d_out, Y)
+    _wsbuf(ws, Y)
+    if T == 0:
+        return
+    st = lib().w4a4_int8_gemm_prequantized(_ptr(ws), ws.numel(), T, ctypes.byref(packed.desc), _ptr(Y), dt, _stream(stream))
+    _check("w4a4_int8_gemm_prequantized", st)
+
+
+def w4a4_int8_linear(X: torch.Tensor, packed: PackedInt8, Y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    T = _acts(X, packed.d_in)
+    _here(X, "X")
+    dt = _y_dtype(Y, T, packed.d_out, X)
+    _wsbuf(ws, X)
+    if T == 0:      # an empty tensor has no address
+        return
+    st = lib().w4a4_int8_linear(_ptr(X), _x_dtype(X), T, ctypes.byref(packed.desc), _ptr(Y), dt, _ptr(ws), ws.numel(),
+                                _stream(stream))
+    _check("w4a4_int8_linear", st)
+
+
+# --------------------------------------------------------------------------- 4-bit key/value cache
+
+class KvCache:
+    """A paged cache of MXFP4 keys and values: the device buffer (kept alive here) and its descriptor."""
+
+    def __init__(self, data: torch.Tensor, desc: W4A4KvCache):
+        self.data, self.desc = data, desc
+
+    @property
+    def n_pages(self) -> int: return self.desc.n_pages
+    @property
+    def page_tokens(self) -> int: return self.desc.page_tokens
+    @property
+    def n_heads(self) -> int: return self.desc.n_heads
+    @property
+    def head_dim(self) -> int: return self.desc.head_dim
+
+
+def w4a4_kv_cache_size(n_pages: int, page_tokens: int, n_heads: int, head_dim: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("w4a4_kv_cache_size", lib().w4a4_kv_cache_size(n_pages, page_tokens, n_heads, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def kv_cache(n_pages: int, page_tokens: int, n_heads: int, head_dim: int, device="cuda") -> KvCache:
+    """A cache of n_pages pages (not cleared: every token is written before it is read)."""
+    nbytes = w4a4_kv_cache_size(n_pages, page_tokens, n_heads, head_dim)
+    data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    desc = W4A4KvCache()
+    _check("w4a4_kv_cache_describe",
+           lib().w4a4_kv_cache_describe(n_pages, page_tokens, n_heads, head_dim, _ptr(data), nbytes, ctypes.byref(desc)))
+    return KvCache(data, desc)
+
+
+class KvBatch:
+    """A call's sequences: descriptor, and the tensors it points to (kept alive here)."""
+
+    def __init__(self, desc: W4A4KvBatch, keep: tuple):
+        self.desc, self.keep = desc, keep
+
+    @property
+    def device(self) -> torch.device: return self.keep[0].device
+
+
+def kv_batch(q_start: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor, max_rows: int) -> KvBatch:
+    """q_start int32 [n_seqs + 1], lens int32 [n_seqs], pages int32 [n_seqs, max_pages], on the
+    device; max_rows: the largest number of rows that any sequence may have.  The kernels
+    read the three when they run, so that they may change between calls."""
+    for t, name in ((q_start, "q_start"), (lens, "lens"), (pages, "pages")):
+        _dev(t, name)
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32, got {t.dtype}")
+        if t.device != q_start.device:
+            raise ValueError(f"{name} is on {t.device}, expected {q_start.device}")
+    n = lens.numel()
+    if lens.dim() != 1 or tuple(q_start.shape) != (n + 1,) or pages.dim() != 2 or pages.shape[0] != n or pages.shape[1] == 0:
+        raise ValueError(f"q_start must be [n + 1], lens [n], pages [n, max_pages], got {tuple(q_start.shape)}, {tuple(lens.shape)}, "
+                         f"{tuple(pages.shape)}")
+    if int(max_rows) < 0:
+        raise ValueError("max_rows must not be negative")
+    desc = W4A4KvBatch(n, int(max_rows), pages.shape[1], q_start.data_ptr(), lens.data_ptr(), pages.data_ptr())
+    return KvBatch(desc, (q_start, lens, pages))
+
+
+def _kv_here(batch: KvBatch, cache: KvCache, t: torch.Tensor, name: str) -> None:
+    _here(t, name)
+    for other, what in ((batch.device, "the batch"), (cache.data.device, "the cache")):
+        if other != t.device:
+            raise ValueError(f"{name} is on {t.device}, {what} on {other}")
+
+
+def _kv_rows(X: torch.Tensor, n_heads: int, head_dim: int, name: str) -> W4A4KvRows:
+    """X [rows, n_heads, head_dim], channels contiguous, rows and heads at any stride."""
+    if not X.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    dt = _x_dtype(X)
+    if X.dim() != 3 or tuple(X.shape[1:]) != (n_heads, head_dim):
+        raise ValueError(f"{name} must be [rows, {n_heads}, {head_dim}], got {tuple(X.shape)}")
+    if head_dim > 1 and X.stride(2) != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    return W4A4KvRows(X.data_ptr(), X.stride(0), X.stride(1), dt, 0)
+
+
+def w4a4_kv_append(K: torch.Tensor, V: torch.Tensor, batch: KvBatch, cache: KvCache, stream=None) -> None:
+    k, v = _kv_rows(K, cache.n_heads, cache.head_dim, "K"), _kv_rows(V, cache.n_heads, cache.head_dim, "V")
+    if K.shape[0] != V.shape[0] or K.dtype != V.dtype or K.device != V.device:
+        raise ValueError("K and V must have as many rows, one dtype and one device")
+    _kv_here(batch, cache, K, "K")
+    if K.shape[0] == 0:      # an empty tensor has no address
+        return
+    _check("w4a4_kv_append", lib().w4a4_kv_append(ctypes.byref(k), ctypes.byref(v), K.shape[0], ctypes.byref(batch.desc),
+                                                  ctypes.byref(cache.desc), _stream(stream)))
+
+
+def w4a4_kv_read(batch: KvBatch, cache: KvCache, K: torch.Tensor, V: torch.Tensor, stream=None) -> None:
+    """K, V: float32 or bfloat16 [rows, n_heads, head_dim], contiguous, written."""
+    for t, name in ((K, "K"), (V, "V")):
+        _dev(t, name)
+        if t.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        if t.dim() != 3 or tuple(t.shape[1:]) != (cache.n_heads, cache.head_dim):
+            raise ValueError(f"{name} must be [rows, {cache.n_heads}, {cache.head_dim}], got {tuple(t.shape)}")
+    if K.shape[0] != V.shape[0] or K.dtype != V.dtype or K.device != V.device:
+        raise ValueError("K and V must have as many rows, one dtype and one device")
+    _kv_here(batch, cache, K, "K")
+    if K.shape[0] == 0:
+        return
+    dt = W4A4_Y_F32 if K.dtype == torch.float32 else W4A4_Y_BF16
+    _check("w4a4_kv_read", lib().w4a4_kv_read(K.shape[0], ctypes.byref(batch.desc), ctypes.byref(cache.desc), _ptr(K), _ptr(V), dt,
+                                              _stream(stream)))
+
+
+def w4a4_kv_attention_workspace_size(n_rows: int, batch: KvBatch, n_q_heads: int, cache: KvCache) -> int:
+    n = ctypes.c_size_t(0)
+    _check("w4a4_kv_attention_workspace_size",
+           lib().w4a4_kv_attention_workspace_size(n_rows, ctypes.byref(batch.desc), ctypes.byref(cache.desc), n_q_heads, ctypes.byref(n)))
+    return n.value
+
+
+def alloc_workspace_kv(n_rows: int, batch: KvBatch, n_q_heads: int, cache: KvCache, device="cuda") -> torch.Tensor:
+    return torch.empty(max(w4a4_kv_attention_workspace_size(n_rows, batch, n_q_heads, cache), 256), dtype=torch.uint8, device=device)
+
+
+def w4a4_kv_attention(Q: torch.Tensor, batch: KvBatch, cache: KvCache, O: torch.Tensor, ws: torch.Tensor, scale: float | None = None,
+                      causal: bool = True, window: int = 0, stream=None) -> None:
+    """Q [rows, n_q_heads, head_dim] float32 or bfloat16; O bfloat16, contiguous, of Q's shape;
+    scale None: 1 / sqrt(head_dim)."""
+    if Q.dim() != 3:
+        raise ValueError(f"Q must be [rows, n_q_heads, {cache.head_dim}], got {tuple(Q.shape)}")
+    n, heads, d = Q.shape
+    q = _kv_rows(Q, heads, cache.head_dim, "Q")
+    _dev(O, "O")
+    if O.dtype != torch.bfloat16:
+        raise TypeError(f"O must be bfloat16, got {O.dtype}")
+    if O.shape != Q.shape or O.device != Q.device:
+        raise ValueError(f"O must have Q's shape {tuple(Q.shape)} and device, got {tuple(O.shape)} on {O.device}")
+    _kv_here(batch, cache, Q, "Q")
+    _wsbuf(ws, Q)
+    if n == 0:
+        return
+    sc = cache.head_dim ** -0.5 if scale is None else float(scale)
+    _check("w4a4_kv_attention",
+           lib().w4a4_kv_attention(ctypes.byref(q), n, ctypes.byref(batch.desc), ctypes.byref(cache.desc), heads, sc, int(bool(causal)),
+                                   int(window), _ptr(O), _ptr(ws), ws.numel(), _stream(stream)))

@@ -493,6 +493,166 @@ int w4a4_moe_workspace_size(int64_t T, const w4a4_moe* moe, size_t* bytes);
 int w4a4_moe_forward(const void* X, int x_dtype, int64_t T, const w4a4_moe* moe, void* Y, int y_dtype,
                      void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * INT8 linear layer: 8-bit integer codes with one scale per token and one per output
+ * channel (the projections around the attention below).
+ *
+ *     Y[t][n] = s_x[t] s_w[n] sum_p q_x[t][p] q_w[n][p]
+ *
+ *   - s = max(fl32(a / 127), 2^-60) with a the largest magnitude of the token (of the weight
+ *     row); q = rne(fl32(x / s)), nearest integer, ties to even, |q| <= 127.  A NaN or Inf
+ *     gives s = NaN and zero codes: the token's (the channel's) outputs are NaN, no others.
+ *   - The integer sums are exact (32 bits; d_in <= W4A4_INT8_MAX_D_IN keeps any codes, -128
+ *     included, within them).  An output is fl32(fl32(s_x s_w) fl32(sum)), rounded once more
+ *     for bf16, so calls are bit-reproducible whatever the shape.
+ *   - Limits: 1 <= d_in <= W4A4_INT8_MAX_D_IN, 1 <= d_out <= W4A4_INT8_MAX_D_OUT, up to 2^26
+ *     tokens and 2^39 outputs (W4A4_ERR_SHAPE above).
+ * The conventions at the top of this file hold. */
+#define W4A4_INT8_MAX_D_IN 131072
+#define W4A4_INT8_MAX_D_OUT 1048576
+
+typedef struct w4a4_int8_packed {
+    int64_t d_in, d_out;
+    int64_t k_pad;           /* roundup(d_in, 128)                                          */
+    int64_t n_pad;           /* roundup(d_out, 16)                                          */
+    const uint8_t* codes;    /* device, two's complement, in the order of w4a4_fp8_packed.codes
+                                (n_mat = 1); rows past d_out and inputs past d_in are zero  */
+    const float* scales;     /* device [n_pad], zero past d_out                             */
+} w4a4_int8_packed;
+
+/* Bytes of the device blob. */
+int w4a4_int8_packed_size(int64_t d_in, int64_t d_out, size_t* bytes);
+/* Quantize W (device [d_out][d_in], fp32 or bf16) into `blob` (device, blob_bytes >=
+ * w4a4_int8_packed_size) and fill *desc.  Async on `stream`. */
+int w4a4_int8_pack_weights(const void* W, int w_dtype, int64_t d_in, int64_t d_out, void* blob, size_t blob_bytes,
+                           w4a4_int8_packed* desc, void* stream);
+/* The same from a checkpoint: codes device int8 [d_out][d_in], scales device fp32 [d_out],
+ * taken as they are.  Async on `stream`. */
+int w4a4_int8_pack_codes(const int8_t* codes, const float* scales, int64_t d_in, int64_t d_out, void* blob,
+                         size_t blob_bytes, w4a4_int8_packed* desc, void* stream);
+
+/* Offsets (bytes) inside a workspace for T tokens. */
+typedef struct w4a4_int8_ws_layout {
+    size_t a_q;       /* activation codes in the order of w4a4_int8_packed.codes, tokens as rows;
+                         rows past T unwritten                                              */
+    size_t a_s;       /* fp32 [T] activation scales                                         */
+    size_t partial;   /* int32 partial sums of ranges of the inputs (written and read back
+                         within a call; empty when the plan does not split)                 */
+    size_t count;     /* int32 ranges done (of a few tokens' plan that splits; cleared by
+                         every call that multiplies)                                        */
+    size_t total;
+} w4a4_int8_ws_layout;
+int w4a4_int8_workspace_layout(int64_t T, const w4a4_int8_packed* desc, w4a4_int8_ws_layout* out);
+int w4a4_int8_workspace_size(int64_t T, const w4a4_int8_packed* desc, size_t* bytes);
+
+/* Activation codes and scales of X (device [T][d_in] fp32 or bf16, row-major contiguous) into
+ * ws.  They and where they lie depend on T and d_in only: one call serves every layer of that
+ * d_in (query, key and value projections), in a workspace large enough for each.  Async. */
+int w4a4_int8_quantize_activations(const void* X, int x_dtype, int64_t T, const w4a4_int8_packed* desc, void* ws,
+                                   size_t ws_bytes, void* stream);
+/* The product on quantized activations in ws.  Y device [T][d_out] fp32 or bf16.  Async. */
+int w4a4_int8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4_int8_packed* desc, void* Y, int y_dtype,
+                                void* stream);
+/* Both.  Async. */
+int w4a4_int8_linear(const void* X, int x_dtype, int64_t T, const w4a4_int8_packed* desc, void* Y, int y_dtype, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Key/value cache in 4 bits, and attention over it.
+ *
+ * Cache.  Every token's keys and values are MXFP4 as at the top of this file, in groups of 32
+ * consecutive channels of one head (the last one cut by the head's width): E2M1 codes and an
+ * E8M0 scale.  The cache is a pool of n_pages pages of page_tokens tokens; a sequence's tokens
+ * stand in the pages that its row of a table names.  Page p, head h, 16 tokens r hold one
+ * contiguous block of `block_bytes`
+ *     data + ((p * n_heads + h) * (page_tokens / 16) + r) * block_bytes,
+ * with g = d_pad / 32 groups, sg = roundup(g, 4) (g itself for g <= 2):
+ *     [0, 256 g)          key codes: dword ((d/8)%4 * 16 + t%16) * g + d/32 holds channels d .. d+7
+ *                         (d a multiple of 8) of token t, channel d+i in nibble i
+ *     [256 g, 512 g)      value codes: byte ((t%16)/4 * 16 + d%16) * 4 g + d/32 * 4 + t%4 holds
+ *                         channel d (d%32 < 16) in its low nibble and d + 16 in its high one
+ *     [512 g, + 16 sg)    key scales: byte t%16 * sg + d/32
+ *     [.., + 16 sg)       value scales: byte (t%16)/4 * 4 sg + d/32 * 4 + t%4
+ * Channels past head_dim are zero.  Nothing in a cache has to be cleared before its first use.
+ *
+ * Batch.  q_start[b] .. q_start[b+1] are the rows of the call's inputs (of n_rows in all) that
+ * belong to sequence b; lens[b] is its number of cached tokens, the rows of this call included.
+ * Row i of n stands at position lens[b] - n + i.  The three arrays are device memory that the
+ * kernels read when they run (a captured call follows their contents); max_rows, the largest number of rows that any
+ * sequence may have, is the host's.  Rows outside every sequence are neither read nor written.
+ * What the host cannot check the kernels do:
+ *   - q_start is clamped to 0 .. n_rows; of a sequence with more than max_rows rows only the
+ *     first max_rows are computed (all its rows count for the positions);
+ *   - lens is clamped to 0 .. max_pages * page_tokens;
+ *   - a position below zero is not stored, reads back as zero, and its row sees nothing;
+ *   - a page number outside 0 .. n_pages - 1 is a page that is not there: its tokens are not
+ *     stored, read back as zero, and no row sees them.
+ * No two rows of a call may name the same token of the cache.
+ *
+ * Attention.  n_q_heads query heads, a multiple of n_heads; head j reads key/value head
+ * j / (n_q_heads / n_heads).  With q = bf16_rne(Q) and the cached keys and values k, v,
+ *     O[row][j] = bf16_rne(sum_t p_t v_t / sum_t p_t),   p_t = exp(scale (q . k_t) - m)
+ * over the tokens t that the row sees: all lens[b] of them, or (causal) t <= the row's own
+ * position, or (causal, window > 0) also t > position - window.  A row that sees nothing, or no score above
+ * -Inf, is zero.  Tokens that a row does not see do not change it, whatever they hold.  A NaN or Inf
+ * in a group of a visible key makes the row NaN, in a group of a visible value its 32 channels.
+ *   - Scores, maxima, sums and outputs are binary32.  The p_t are rounded to bf16 (for sequences of
+ *     up to W4A4_KV_FEW_ROWS rows a head group: to two bf16 terms, 16 bits) where they are multiplied with the values.
+ *   - Results depend on the sequences, not on where their pages are; the order of sums depends on
+ *     shape and lengths only, so calls are bit-reproducible.
+ *
+ * Limits: head_dim 1 .. 256 (d_pad = roundup(head_dim, 32) up to 128, roundup(head_dim, 64)
+ * above), page_tokens a multiple of 16 up to 2^20, n_heads and n_q_heads up to 4096, n_pages
+ * below 2^31, max_pages * page_tokens up to 2^31 - 256, up to 65535 sequences and 2^26 rows, and
+ * n_seqs * (max_rows / 16 + 2) * (n_heads / 4 + 1) and n_seqs * n_heads * (max_rows * ratio / 128 + 2)
+ * (ratio = n_q_heads / n_heads) below 2^23 (the workgroups of a launch); W4A4_ERR_SHAPE above.
+ * K, V, Q may be slices of a larger array: row and head strides are in elements, channels are
+ * contiguous, and their pointers need only be aligned to an element. */
+#define W4A4_KV_FEW_ROWS 64
+
+typedef struct w4a4_kv_cache {
+    int64_t n_pages;
+    int32_t page_tokens, n_heads, head_dim;
+    int32_t d_pad;
+    int64_t block_bytes;     /* of 16 tokens of one head                                    */
+    uint8_t* data;           /* device, w4a4_kv_cache_size bytes, 16-byte aligned           */
+} w4a4_kv_cache;
+/* Bytes of a cache, and its descriptor (host work only). */
+int w4a4_kv_cache_size(int64_t n_pages, int32_t page_tokens, int32_t n_heads, int32_t head_dim, size_t* bytes);
+int w4a4_kv_cache_describe(int64_t n_pages, int32_t page_tokens, int32_t n_heads, int32_t head_dim, void* data,
+                           size_t data_bytes, w4a4_kv_cache* out);
+
+typedef struct w4a4_kv_batch {
+    int64_t n_seqs, max_rows, max_pages;
+    const int32_t* q_start;  /* device [n_seqs + 1], not decreasing                         */
+    const int32_t* lens;     /* device [n_seqs]                                             */
+    const int32_t* pages;    /* device [n_seqs][max_pages]                                  */
+} w4a4_kv_batch;
+
+/* A [n_rows][heads][head_dim] input with its strides in elements. */
+typedef struct w4a4_kv_rows {
+    const void* data;
+    int64_t row_stride, head_stride;
+    int32_t dtype;           /* W4A4_X_F32 or W4A4_X_BF16                                   */
+    int32_t reserved;
+} w4a4_kv_rows;
+
+/* Quantize the rows of K and V into their places of the cache.  Async. */
+int w4a4_kv_append(const w4a4_kv_rows* K, const w4a4_kv_rows* V, int64_t n_rows, const w4a4_kv_batch* batch,
+                   const w4a4_kv_cache* cache, void* stream);
+/* The rows' keys and values out of the cache: K, V device [n_rows][n_heads][head_dim], both of
+ * y_dtype (every code's value is a bf16 and an fp32 number).  Async. */
+int w4a4_kv_read(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache, void* K, void* V, int y_dtype,
+                 void* stream);
+/* Bytes of an attention call's workspace: partial results of long sequences' ranges. */
+int w4a4_kv_attention_workspace_size(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache,
+                                     int32_t n_q_heads, size_t* bytes);
+/* O device bf16 [n_rows][n_q_heads][head_dim]; scale > 0; causal 0 or 1; window >= 0 (0: none;
+ * only with causal).  Async. */
+int w4a4_kv_attention(const w4a4_kv_rows* Q, int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache,
+                      int32_t n_q_heads, float scale, int causal, int64_t window, uint16_t* O, void* ws, size_t ws_bytes,
+                      void* stream);
+
 #ifdef __cplusplus
 }
 #endif
