@@ -31,33 +31,101 @@ struct AttnArgs {
     const void* q;
     int64_t q_row, q_head;
     uint16_t* out;
-    float *part_o, *part_ml;      // [unit][split][rows_cap][d_pad], [unit][split][rows_cap][2]
+    float *part_o, *part_ml;      // [slot][rows_cap][d_pad], [slot][rows_cap][2]
+    int64_t* ranges;              // [n_seqs]: a sequence's first slot * 2^20 + its number of ranges
     int64_t window;
     float scale;                  // scale * log2(e)
-    int32_t ratio, causal, nsplit, rows_cap;
+    int32_t ratio, causal, target, rows_cap;
 };
 
-// The steps of ST tokens that rows m0 .. m1 - 1 of a sequence see, cut into equal ranges.
+// The steps of ST tokens that rows m0 .. m1 - 1 of a sequence see.
 template <int ST> struct Steps {
-    int32_t start, n, chunk, active;
+    int32_t start, n;
     __device__ Steps(const AttnArgs& a, const KvSeq& s, int32_t m0, int32_t m1) {
         const int64_t i0 = m0 / a.ratio, i1 = (m1 - 1) / a.ratio;
         int64_t lo = a.causal && a.window ? s.first + i0 - a.window + 1 : 0, hi = a.causal ? s.first + i1 + 1 : s.len;
         lo = lo < 0 ? 0 : lo / ST * ST;
         n = m1 > m0 && hi > lo ? (int32_t)((hi - lo + ST - 1) / ST) : 0;
         start = (int32_t)lo;
-        constexpr int LEAST = 256 / ST;
-        chunk = (n + a.nsplit - 1) / a.nsplit;
-        chunk = chunk < LEAST ? LEAST : chunk;
-        active = n > chunk ? (n + chunk - 1) / chunk : 1;
+    }
+};
+
+// Long sequences are cut into ranges of about the same number of steps, whatever sequence they
+// belong to, so that a ragged batch keeps all CUs busy to the end: with `target` workgroups in mind a
+// range has total / target steps, at least LEAST.  The lengths are the device's, so every
+// workgroup finds its range by itself: a wavefront sums the sequences' steps, 64 at a time,
+// and looks its number up among their ranges.  Ranges of sequences that have several leave their results in
+// slots, of which there are fewer than 2 target (a sequence of n steps > C has at most n / C + 1 < 2 n / C).
+struct Range {
+    int64_t b, slot;      // slot of the sequence's first range (heads lie side by side)
+    int32_t k, count;     // which of how many ranges; count 0: there is nothing to do
+};
+__device__ __forceinline__ int32_t scan64(int32_t v) {      // inclusive, over the wavefront
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        const int32_t u = __shfl_up(v, o);
+        v += lane >= o ? u : 0;
+    }
+    return v;
+}
+template <int ST, int LEAST> struct Ranges {
+    int32_t chunk;
+    __device__ static int32_t steps(const AttnArgs& a, int64_t b, bool& live) {
+        live = false;
+        if (b >= a.kv.n_seqs) return 0;
+        const KvSeq s = kv_seq(a.kv, b);
+        live = s.done > 0;
+        return live ? Steps<ST>(a, s, 0, s.done * a.ratio).n : 0;
+    }
+    __device__ explicit Ranges(const AttnArgs& a) : chunk(0x7FFFFFFF) {
+        if (!a.target) return;
+        int64_t total = 0;
+        bool live;
+        for (int64_t b = threadIdx.x & 63; b < a.kv.n_seqs; b += 64) total += steps(a, b, live);
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
+        const int64_t c = (total * a.kv.n_heads + a.target - 1) / a.target;
+        chunk = (int32_t)(c < LEAST ? LEAST : c);
+    }
+    __device__ Range find(const AttnArgs& a, int64_t item) const {
+        Range r = {0, 0, 0, 0};
+        if (!a.target) {
+            r.b = item;
+            r.count = item < a.kv.n_seqs;
+            return r;
+        }
+        int64_t before = 0, slots = 0;
+        for (int64_t b0 = 0; b0 < a.kv.n_seqs; b0 += 64) {
+            bool live;
+            const int lane = threadIdx.x & 63;
+            const int32_t n = steps(a, b0 + lane, live);
+            const int32_t c = live ? (n > chunk ? (n + chunk - 1) / chunk : 1) : 0, m = c > 1 ? c : 0;
+            const int32_t sc = scan64(c), sm = scan64(m);
+            const uint64_t hit = __ballot(item < before + sc);
+            if (hit) {
+                const int w = __builtin_ctzll(hit);
+                const int32_t cw = __shfl(c, w);
+                r.b = b0 + w;
+                r.count = cw;
+                r.k = (int32_t)(item - (before + __shfl(sc, w) - cw));
+                r.slot = slots + __shfl(sm, w) - (cw > 1 ? cw : 0);
+                return r;
+            }
+            before += __shfl(sc, 63);
+            slots += __shfl(sm, 63);
+        }
+        return r;
     }
 };
 
 template <int N> __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
     __builtin_memcpy(w, __builtin_assume_aligned(p, N % 4 == 0 ? 16 : N % 2 == 0 ? 8 : 4), 4 * N);
 }
+// A scale code's byte where a binary32 has its exponent.  The neighbouring bytes stay beside it: the
+// conversions read the exponent field only (compared for every code and several other bits).
 __device__ __forceinline__ float scale_of(uint32_t word, int byte) {
-    return __uint_as_float(byte == 3 ? (word >> 1) & 0x7F800000u : (word << (23 - 8 * byte)) & 0x7F800000u);
+    return __uint_as_float(byte == 3 ? word >> 1 : word << (23 - 8 * byte));
 }
 template <int J> __device__ __forceinline__ uint32_t widen2(uint32_t w, float s) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, J));
@@ -119,26 +187,44 @@ __device__ __forceinline__ void store_out4(uint16_t* row, int d, int D, v4f v) {
 
 // ---------------------------------------------------------------- few rows
 //
-// Up to 16 MT stacked rows: bound by reading the cache.  A wavefront takes every fourth step of
-// 32 tokens of its workgroup's range, codes straight from memory into registers with the next
-// step's in flight; the wavefronts' results meet in LDS.
+// Up to 16 MT stacked rows: bound by reading the cache.  A wavefront takes every NW-th step of
+// 32 tokens of its workgroup's range.  Its two blocks go into a ring of R steps in LDS by copies that
+// need no registers, so that many steps are in flight beside the accumulators; the copies past the
+// last step run with empty ranges, so that every wait counts the same number.  The wavefronts'
+// results meet in LDS.
+constexpr int FEW_LEAST = 16;      // steps of a range: 512 tokens
+template <int G, int MT> struct Few {      // wavefronts of a workgroup, steps of a ring, wavefronts a SIMD (for the register budget)
+    static constexpr int NW = 4, R = 2, OCC = G * MT <= 4 ? 4 : G * MT <= 8 ? 2 : 1;
+    static constexpr int COPIES = (KvBlock<G>::BYTES + 1023) / 1024, STEP = 2 * KvBlock<G>::BYTES, LD = 32 * G + 4;
+    static constexpr int64_t ROUND = 256 * OCC;      // workgroups at a time
+    static constexpr int RING = NW * R * STEP, RED = NW * 16 * LD * 4, LDS = RING > RED ? RING : RED;
+};
+
 template <int G, int MT, bool QB>
-__global__ __launch_bounds__(256) void kv_few_kernel(AttnArgs a) {
+__global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_few_kernel(AttnArgs a) {
     typedef KvBlock<G> L;
-    constexpr int DP = 32 * G, LD = DP + 4, NW = 4;
-    __shared__ __attribute__((aligned(16))) float red[NW][16][LD];
+    typedef Few<G, MT> F;
+    constexpr int DP = 32 * G, LD = F::LD, NW = F::NW, R = F::R;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[F::LDS];      // the rings, then the wavefronts' sums
     __shared__ float red_m[NW][MT][16], red_l[NW][MT][16];
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t unit = blockIdx.x / a.nsplit;
-    const int sp = blockIdx.x % a.nsplit;
-    const int64_t b = unit / a.kv.n_heads;
-    const int h = (int)(unit - b * a.kv.n_heads);
+    const uint32_t item = blockIdx.x / (uint32_t)a.kv.n_heads;
+    const int h = (int)(blockIdx.x - item * (uint32_t)a.kv.n_heads);
+    const Ranges<32, FEW_LEAST> ranges(a);
+    Range rg = ranges.find(a, item);
+    rg.k = __builtin_amdgcn_readfirstlane(rg.k);
+    rg.count = __builtin_amdgcn_readfirstlane(rg.count);
+    if (rg.count == 0) return;
+    const int64_t b = __builtin_amdgcn_readfirstlane((int)rg.b);
     const KvSeq s = kv_seq(a.kv, b);
     const int rows = s.done * a.ratio;
     const Steps<32> st(a, s, 0, rows);
-    if (rows == 0 || sp >= st.active) return;
-    const int s0 = sp * st.chunk, s1 = s0 + st.chunk < st.n ? s0 + st.chunk : st.n;
+    if (rows == 0) return;
+    if (a.target && rg.k == 0 && h == 0 && threadIdx.x == 0) a.ranges[b] = rg.slot << 20 | rg.count;      // for the join
+    // equal parts of the sequence's steps; this wavefront's are s0 + wave, + NW, ..
+    const int s0 = (int)((int64_t)st.n * rg.k / rg.count), s1 = (int)((int64_t)st.n * (rg.k + 1) / rg.count);
+    const int mine = s1 - s0 > wave ? (s1 - s0 - wave + NW - 1) / NW : 0;
 
     // this lane's rows: the operand of each block of 32 channels, and the tokens they see
     v8bf q[MT][G];
@@ -172,137 +258,162 @@ __global__ __launch_bounds__(256) void kv_few_kernel(AttnArgs a) {
         for (int t = 0; t < 2 * G; ++t) acc[mt][t] = v4f{0, 0, 0, 0};
     }
 
-    struct Codes {
-        uint32_t k[2][G], v[2][G], ks[2][(G + 3) / 4], vs[2][G];
-        bool there[2];
+    // Block addresses of 32 steps, two a step, one a lane (zero where a block is not there).
+    uint64_t addr = 0;
+    auto lookup = [&](int k) __attribute__((always_inline)) {
+        const int mk = k + (lane >> 1);
+        addr = mk < mine ? (uint64_t)(uintptr_t)kv_block(a.kv, b, (uint32_t)(st.start / 16 + 2 * (s0 + wave + mk * NW) + (lane & 1)), h) : 0;
     };
-    Codes buf[2];
-    // block addresses of 32 steps at a time, two a step, one a lane
-    for (int k0 = s0 + wave; k0 < s1; k0 += 32 * NW) {
-        const int mine = k0 + (lane >> 1) * NW;
-        uint64_t addr = 0;
-        if (mine < s1) addr = (uint64_t)(uintptr_t)kv_block(a.kv, b, (uint32_t)(st.start / 16 + 2 * mine + (lane & 1)), h);
-        auto fetch = [&](Codes& x, int k) __attribute__((always_inline)) {
+    const uint32_t ring = (uint32_t)(uintptr_t)smem + (uint32_t)wave * R * F::STEP;
+    uint64_t there_bits = 0;      // whether each block of these steps is there
+    auto copy = [&](int k, uint32_t slot) __attribute__((always_inline)) {      // step k of this wavefront into a slot of its ring
+        if ((k & 31) == 0) {
+            lookup(k);
+            there_bits = __ballot(addr != 0);
+        }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t al = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)addr, 2 * k + u);
-                const uint32_t ah = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(addr >> 32), 2 * k + u);
-                const uint8_t* p = (const uint8_t*)(uintptr_t)((uint64_t)ah << 32 | al);
-                x.there[u] = p != nullptr;
-                p = p ? p : a.kv.data;
-                load_words<G>(p + lane * 4 * G, x.k[u]);
-                load_words<G>(p + L::V + lane * 4 * G, x.v[u]);
-                load_words<G>(p + L::VS + g * 4 * L::SG, x.vs[u]);
-                if constexpr (G == 1) x.ks[u][0] = p[L::KS + c];
-                else if constexpr (G == 2) x.ks[u][0] = *reinterpret_cast<const uint16_t*>(p + L::KS + c * 2);
-                else load_words<(G + 3) / 4>(p + L::KS + c * L::SG, x.ks[u]);
+        for (int u = 0; u < 2; ++u) {
+            const int from = 2 * (k & 31) + u;
+            const uint32_t al = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)addr, from);
+            const uint32_t ah = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(addr >> 32), from);
+            const uint64_t p = (uint64_t)ah << 32 | al;
+            const v4i srd = make_srd((const void*)(uintptr_t)p, p ? L::BYTES : 0u);
+#pragma unroll
+            for (int i = 0; i < F::COPIES; ++i) {
+                const int off = i * 1024 + lane * 16;
+                if (off < L::BYTES) dma16(srd, ring + slot * F::STEP + u * L::BYTES + i * 1024, off, 0);
             }
-        };
-        auto compute = [&](Codes& x, int pos) __attribute__((always_inline)) {      // pos: the step's first token
-            const bool full = pos + 31 <= all_hi && pos >= last_from && x.there[0] && x.there[1];
-            v4f sc[MT][2];
+        }
+    };
+    // One step from token `pos` on; `there` tells which of its two blocks are in the cache.  Where some row
+    // does not see all of its tokens, their scores become -Inf; value scale codes that no weight
+    // of zero may be multiplied with are made harmless first, and values that are NaN go by a list of their own.
+    auto step = [&](uint8_t* x, int pos, uint32_t there) __attribute__((always_inline)) {
+        const bool full = there == 3u && pos + 31 <= all_hi && pos >= last_from;      // uniform
+        uint32_t nan = 0;
+        if (!full) {
+            constexpr int WORDS = 4 * L::SG;      // of a block's value scales: tokens 4 (i / sg) .., group i % sg
+            if (lane < 2 * WORDS) {
+                uint32_t* const w = reinterpret_cast<uint32_t*>(x + lane / WORDS * L::BYTES + L::VS) + lane % WORDS;
+                if (wild(*w)) *w = tame(*w, nan);
+            }
+            asm volatile("" ::: "memory");
+        }
+        v4f sc[MT][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) sc[mt][0] = sc[mt][1] = v4f{0, 0, 0, 0};
+        for (int mt = 0; mt < MT; ++mt) sc[mt][0] = sc[mt][1] = v4f{0, 0, 0, 0};
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            uint32_t kw[G], ks[(G + 3) / 4];
+            const uint8_t* const p = x + u * L::BYTES;
+            load_words<G>(p + lane * 4 * G, kw);
+            if constexpr (G == 1) ks[0] = p[L::KS + c];
+            else if constexpr (G == 2) ks[0] = *reinterpret_cast<const uint16_t*>(p + L::KS + c * 2);
+            else load_words<(G + 3) / 4>(p + L::KS + c * L::SG, ks);
 #pragma unroll
-                for (int d = 0; d < G; ++d) {
-                    const v8bf kf = widen_key(x.k[u][d], scale_of(x.ks[u][d / 4], d & 3));
+            for (int d = 0; d < G; ++d) {
+                const v8bf kf = widen_key(kw[d], scale_of(ks[d / 4], d & 3));
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) sc[mt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[mt][d], sc[mt][u], 0, 0, 0);
-                }
-            uint32_t bad[MT];      // groups whose values are NaN for this lane's row
+                for (int mt = 0; mt < MT; ++mt) sc[mt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[mt][d], sc[mt][u], 0, 0, 0);
+            }
+        }
+        uint32_t vw[2][G], vs[2][G];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) bad[mt] = 0;
-            if (!full) {
-                uint32_t seen[MT][2];      // bit i: token 4 g + i of the block is seen by the row
+        for (int u = 0; u < 2; ++u) {
+            load_words<G>(x + u * L::BYTES + L::V + lane * 4 * G, vw[u]);
+            load_words<G>(x + u * L::BYTES + L::VS + g * 4 * L::SG, vs[u]);
+        }
+        if (!full) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        seen[mt][u] = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int t = pos + 16 * u + 4 * g + i;
-                            const bool see = t >= lo[mt] && t <= hi[mt] && x.there[u];
-                            seen[mt][u] |= see ? 1u << i : 0u;
-                            sc[mt][u][i] = see ? sc[mt][u][i] : -__builtin_inff();
-                        }
-                    }
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int d = 0; d < G; ++d) {
-                        uint32_t nan;
-                        x.vs[u][d] = tame(x.vs[u][d], nan);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) bad[mt] |= (nan & seen[mt][u]) ? 1u << d : 0u;
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = pos + 16 * u + 4 * g + i;
+                        if (t < lo[mt] || t > hi[mt] || !(there >> u & 1)) sc[mt][u][i] = -__builtin_inff();
                     }
+        }
+        v8bf ph[MT], pl[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(sc[mt][0][0], sc[mt][0][1]), __builtin_fmaxf(sc[mt][0][2], sc[mt][0][3])),
+                                        __builtin_fmaxf(__builtin_fmaxf(sc[mt][1][0], sc[mt][1][1]), __builtin_fmaxf(sc[mt][1][2], sc[mt][1][3])));
+            top *= a.scale;
+            if (__any(top > mx[mt] + M_SLACK)) {
+                top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+                const float m = __builtin_fmaxf(mx[mt], top), f = __builtin_amdgcn_exp2f(mx[mt] - m);
+                mx[mt] = m;
+                sum[mt] *= f;
+#pragma unroll
+                for (int t = 0; t < 2 * G; ++t) acc[mt][t] *= f;
             }
-            v8bf ph[MT], pl[MT];
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][i >> 2][i & 3], a.scale, -mx[mt]));
+                sum[mt] += p[i];
+            }
+            uint32_t wh[4], wl[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wh[i] = pk_bf16(p[2 * i], p[2 * i + 1]);
+                wl[i] = pk_bf16(p[2 * i] - __uint_as_float(wh[i] << 16), p[2 * i + 1] - __uint_as_float(wh[i] & 0xFFFF0000u));
+            }
+            ph[mt] = join8(wh[0], wh[1], wh[2], wh[3]);
+            pl[mt] = join8(wl[0], wl[1], wl[2], wl[3]);
+        }
+#pragma unroll
+        for (int d = 0; d < G; ++d) {
+            v8bf v0, v1;
+            widen_value(vw[0][d], vs[0][d], vw[1][d], vs[1][d], v0, v1);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(sc[mt][0][0], sc[mt][0][1]), __builtin_fmaxf(sc[mt][0][2], sc[mt][0][3])),
-                                            __builtin_fmaxf(__builtin_fmaxf(sc[mt][1][0], sc[mt][1][1]), __builtin_fmaxf(sc[mt][1][2], sc[mt][1][3])));
-                top *= a.scale;
-                if (__any(top > mx[mt] + M_SLACK)) {
-                    top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-                    top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                    const float m = __builtin_fmaxf(mx[mt], top), f = __builtin_amdgcn_exp2f(mx[mt] - m);
-                    mx[mt] = m;
-                    sum[mt] *= f;
-#pragma unroll
-                    for (int t = 0; t < 2 * G; ++t) acc[mt][t] *= f;
-                }
-                float p[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][i >> 2][i & 3], a.scale, -mx[mt]));
-                    sum[mt] += p[i];
-                }
-                uint32_t ph_[4], pl_[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ph_[i] = pk_bf16(p[2 * i], p[2 * i + 1]);
-                    pl_[i] = pk_bf16(p[2 * i] - __uint_as_float(ph_[i] << 16), p[2 * i + 1] - __uint_as_float(ph_[i] & 0xFFFF0000u));
-                }
-                ph[mt] = join8(ph_[0], ph_[1], ph_[2], ph_[3]);
-                pl[mt] = join8(pl_[0], pl_[1], pl_[2], pl_[3]);
-            }
-#pragma unroll
-            for (int d = 0; d < G; ++d) {
-                v8bf v0, v1;
-                widen_value(x.v[0][d], x.vs[0][d], x.v[1][d], x.vs[1][d], v0, v1);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    acc[mt][2 * d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, ph[mt], acc[mt][2 * d], 0, 0, 0);
-                    acc[mt][2 * d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pl[mt], acc[mt][2 * d], 0, 0, 0);
-                    acc[mt][2 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, ph[mt], acc[mt][2 * d + 1], 0, 0, 0);
-                    acc[mt][2 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl[mt], acc[mt][2 * d + 1], 0, 0, 0);
-                }
-            }
-            if (!full) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    bad[mt] |= (uint32_t)__shfl_xor((int)bad[mt], 16);
-                    bad[mt] |= (uint32_t)__shfl_xor((int)bad[mt], 32);
-#pragma unroll
-                    for (int d = 0; d < G; ++d)
-                        if (bad[mt] >> d & 1) acc[mt][2 * d] = acc[mt][2 * d + 1] = acc[mt][2 * d] + __uint_as_float(0x7FC00000u);
-                }
-            }
-        };
-        const int left = (s1 - k0 + NW - 1) / NW, steps = left < 32 ? left : 32;
-        fetch(buf[0], 0);
-        for (int k = 0; k < steps; k += 2) {
-            if (k + 1 < steps) fetch(buf[1], k + 1);
-            compute(buf[0], st.start + (k0 + k * NW) * 32);
-            if (k + 1 < steps) {
-                if (k + 2 < steps) fetch(buf[0], k + 2);
-                compute(buf[1], st.start + (k0 + (k + 1) * NW) * 32);
+                acc[mt][2 * d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, ph[mt], acc[mt][2 * d], 0, 0, 0);
+                acc[mt][2 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, ph[mt], acc[mt][2 * d + 1], 0, 0, 0);
+                acc[mt][2 * d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pl[mt], acc[mt][2 * d], 0, 0, 0);
+                acc[mt][2 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl[mt], acc[mt][2 * d + 1], 0, 0, 0);
             }
         }
+        if (!full) {      // rare: for every NaN that a row sees, its group of channels
+            for (uint64_t left = __ballot(nan != 0); left; left &= left - 1) {
+                const int from = __builtin_ctzll(left), w = from % (4 * L::SG), u = from / (4 * L::SG);
+                const uint32_t bits = (uint32_t)__builtin_amdgcn_readlane((int)nan, from);
+                const int t0 = pos + 16 * u + 4 * (w / L::SG), d = w % L::SG;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    bool hit = false;
+                    for (int j = 0; j < 4; ++j) hit |= (bits >> j & 1) && (there >> u & 1) && t0 + j >= lo[mt] && t0 + j <= hi[mt];
+#pragma unroll
+                    for (int e = 0; e < G; ++e)
+                        if (hit && e == d) acc[mt][2 * e][0] = acc[mt][2 * e][1] = acc[mt][2 * e][2] = acc[mt][2 * e][3] = acc[mt][2 * e + 1][0] =
+                            acc[mt][2 * e + 1][1] = acc[mt][2 * e + 1][2] = acc[mt][2 * e + 1][3] = __uint_as_float(0x7FC00000u);
+                }
+            }
+        }
+    };
+    uint64_t there = 0;      // of the steps whose copies are under way, two bits a step, the next one lowest
+    auto there_of = [&](int k) { return (uint32_t)(there_bits >> (2 * (k & 31))) & 3u; };
+#pragma unroll
+    for (int k = 0; k < R - 1; ++k) {
+        copy(k, k);
+        there |= (uint64_t)there_of(k) << (2 * k);
     }
+    uint32_t slot = 0;
+    for (int k = 0; k < mine; ++k) {
+        // the slot read last is free: its reads are in registers
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy(k + R - 1, slot == 0 ? R - 1 : slot - 1);
+        there |= (uint64_t)there_of(k + R - 1) << (2 * (R - 1));
+        asm volatile("s_waitcnt vmcnt(%0)" ::"i"((R - 1) * 2 * F::COPIES) : "memory");
+        step(smem + (wave * R + slot) * F::STEP, st.start + (s0 + wave + k * NW) * 32, (uint32_t)there & 3u);
+        there >>= 2;
+        slot = slot == R - 1 ? 0 : slot + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();      // the rings are free
+    float(*const red)[16][LD] = reinterpret_cast<float(*)[16][LD]>(smem);
 
     // the wavefronts' results: one maximum, then the sums of 16 rows at a time
 #pragma unroll
@@ -325,7 +436,7 @@ __global__ __launch_bounds__(256) void kv_few_kernel(AttnArgs a) {
 #pragma unroll
         for (int t = 0; t < 2 * G; ++t) *reinterpret_cast<v4f*>(&red[wave][c][16 * t + 4 * g]) = acc[mt][t] * f;
         __syncthreads();
-        for (int e = threadIdx.x; e < 16 * (DP / 4); e += 256) {
+        for (int e = threadIdx.x; e < 16 * (DP / 4); e += NW * 64) {
             const int col = e / (DP / 4), d = e % (DP / 4) * 4, row = mt * 16 + col;
             if (row >= rows) continue;
             float top = red_m[0][mt][col], l = 0.0f;
@@ -337,12 +448,12 @@ __global__ __launch_bounds__(256) void kv_few_kernel(AttnArgs a) {
                 l += red_l[w][mt][col] * __builtin_amdgcn_exp2f(red_m[w][mt][col] - top);
                 o += *reinterpret_cast<const v4f*>(&red[w][col][d]);
             }
-            if (st.active == 1) {
+            if (rg.count == 1) {
                 const int i = row / a.ratio, j = row - i * a.ratio;
                 const float r = l == 0.0f ? 0.0f : 1.0f / l;
                 store_out4(a.out + ((s.row0 + i) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + j) * a.kv.head_dim, d, a.kv.head_dim, o * r);
             } else {
-                const int64_t at = (unit * a.nsplit + sp) * a.rows_cap + row;
+                const int64_t at = ((rg.slot + rg.k) * a.kv.n_heads + h) * a.rows_cap + row;
                 *reinterpret_cast<v4f*>(a.part_o + at * DP + d) = o;
                 if (d == 0) {
                     a.part_ml[2 * at] = top;
@@ -360,8 +471,11 @@ __global__ __launch_bounds__(256) void kv_few_kernel(AttnArgs a) {
 // once, a block of 16 tokens a wavefront, into two LDS buffers that take turns; the codes of the tile after
 // are in flight meanwhile.  Rows of LDS are 16 bytes longer than their data, so that the
 // operand reads of 16 lanes touch every bank once.
+// The ranges that a row tile's steps are cut into, out of nsplit that there is room for.
+__device__ __forceinline__ int many_parts(int n, int nsplit) { return n / 4 < 1 ? 1 : n / 4 < nsplit ? n / 4 : nsplit; }
+
 template <int G, int NW, bool QB>
-__global__ __launch_bounds__(NW * 64) void kv_many_kernel(AttnArgs a, uint32_t row_tiles) {
+__global__ __launch_bounds__(NW * 64, (G <= 4 ? 2 : 1)) void kv_many_kernel(AttnArgs a, uint32_t row_tiles, int32_t nsplit) {
     typedef KvBlock<G> L;
     constexpr int DP = 32 * G, KLD = 64 * G + 16, VLD = 144, KB = 64 * KLD, VB = DP * VLD, BUF = KB + VB, ROWS = 32 * NW;
     constexpr int NB = (G + 1) / 2;                        // value groups a lane converts
@@ -371,8 +485,8 @@ __global__ __launch_bounds__(NW * 64) void kv_many_kernel(AttnArgs a, uint32_t r
     __shared__ uint8_t nans[2][64];                        // a token's groups that are NaN
     const int lane = threadIdx.x & 63, c = lane & 31, h2 = lane >> 5, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int sp = blockIdx.x % a.nsplit;
-    const uint32_t rest = blockIdx.x / a.nsplit;
+    const int sp = blockIdx.x % nsplit;
+    const uint32_t rest = blockIdx.x / nsplit;
     const int tile = (int)(row_tiles - 1 - rest % row_tiles);      // the rows that see most first
     const int64_t unit = rest / row_tiles;
     const int64_t b = unit / a.kv.n_heads;
@@ -383,8 +497,9 @@ __global__ __launch_bounds__(NW * 64) void kv_many_kernel(AttnArgs a, uint32_t r
     if (m0 >= all_rows) return;
     const int rows = (int)(all_rows - m0 < ROWS ? all_rows - m0 : ROWS);
     const Steps<64> st(a, s, (int32_t)m0, (int32_t)(m0 + rows));
-    if (sp >= st.active) return;
-    const int s0 = sp * st.chunk, s1 = s0 + st.chunk < st.n ? s0 + st.chunk : st.n;
+    const int parts = many_parts(st.n, nsplit);
+    if (sp >= parts) return;
+    const int s0 = (int)((int64_t)st.n * sp / parts), s1 = (int)((int64_t)st.n * (sp + 1) / parts);
 
     const int m = (int)m0 + wave * 32 + c, qi = m / a.ratio, qj = m - qi * a.ratio;
     const bool on = wave * 32 + c < rows;
@@ -555,8 +670,8 @@ __global__ __launch_bounds__(NW * 64) void kv_many_kernel(AttnArgs a, uint32_t r
     }
     sum += __shfl_xor(sum, 32);
     if (!on) return;
-    const float r = st.active > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = (unit * a.nsplit + sp) * a.rows_cap + m;
+    const float r = parts > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t at = (unit * nsplit + sp) * a.rows_cap + m;
     uint16_t* const out = a.out + ((s.row0 + qi) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + qj) * a.kv.head_dim;
 #pragma unroll
     for (int d = 0; d < G; ++d)
@@ -564,83 +679,144 @@ __global__ __launch_bounds__(NW * 64) void kv_many_kernel(AttnArgs a, uint32_t r
         for (int u = 0; u < 4; ++u) {
             const v4f v = v4f{acc[d][4 * u] * r, acc[d][4 * u + 1] * r, acc[d][4 * u + 2] * r, acc[d][4 * u + 3] * r};
             const int ch = 32 * d + 8 * u + 4 * h2;
-            if (st.active == 1) store_out4(out, ch, a.kv.head_dim, v);
+            if (parts == 1) store_out4(out, ch, a.kv.head_dim, v);
             else *reinterpret_cast<v4f*>(a.part_o + at * DP + ch) = v;
         }
-    if (st.active > 1 && h2 == 0) {
+    if (parts > 1 && h2 == 0) {
         a.part_ml[2 * at] = mx;
         a.part_ml[2 * at + 1] = sum;
     }
 }
 
-// The ranges' results of one row a wavefront: the common maximum, then the weighted sums.
-template <int G, int ST, int ROWS>
-__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs a) {
-    constexpr int DP = 32 * G;
-    const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t unit = id / a.rows_cap, b = unit / a.kv.n_heads;
-    const int m = (int)(id - unit * a.rows_cap), h = (int)(unit - b * a.kv.n_heads);
-    if (b >= a.kv.n_seqs) return;
+// The ranges' results of one row a workgroup: the common maximum, then the weighted sums; a quarter of
+// a row's lanes take four channels each and every 256 / lanes-th range.  ROWS 0: the ranges of the few-row
+// kernel, else those of tiles of ROWS rows.
+template <int G, int ROWS>
+__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs a, int32_t nsplit) {
+    constexpr int DP = 32 * G, QL = DP / 4, KK = 256 / QL;
+    __shared__ __attribute__((aligned(16))) float red[KK][DP];
+    __shared__ float red_m[KK], red_l[KK];
+    const uint32_t unit = blockIdx.x / (uint32_t)a.rows_cap;
+    const int m = (int)(blockIdx.x - unit * (uint32_t)a.rows_cap);
+    const int64_t b = unit / (uint32_t)a.kv.n_heads;
+    const int h = (int)(unit - (uint32_t)b * (uint32_t)a.kv.n_heads);
     const KvSeq s = kv_seq(a.kv, b);
     const int rows = s.done * a.ratio;
     if (m >= rows) return;
-    const int m0 = ROWS ? m / (ROWS ? ROWS : 1) * ROWS : 0, m1 = ROWS && m0 + ROWS < rows ? m0 + ROWS : rows;
-    const Steps<ST> st(a, s, m0, m1);
-    if (st.active == 1) return;
-    const int64_t at = unit * a.nsplit * a.rows_cap + m;
-    float top = M_NONE, l = 0.0f;
-    for (int k = 0; k < st.active; ++k) top = __builtin_fmaxf(top, a.part_ml[2 * (at + (int64_t)k * a.rows_cap)]);
-    v4f o = v4f{0, 0, 0, 0};
-    for (int k = 0; k < st.active; ++k) {
-        const int64_t p = at + (int64_t)k * a.rows_cap;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - top);
-        l += a.part_ml[2 * p + 1] * f;
-        if (lane < DP / 4) o += *reinterpret_cast<const v4f*>(a.part_o + p * DP + 4 * lane) * f;
+    int count;
+    int64_t at, step;
+    if constexpr (ROWS == 0) {
+        const int64_t r = a.ranges[b];
+        count = (int)(r & 0xFFFFF);
+        at = ((r >> 20) * a.kv.n_heads + h) * a.rows_cap + m;
+        step = (int64_t)a.kv.n_heads * a.rows_cap;
+    } else {
+        const int m0 = m / ROWS * ROWS, m1 = m0 + ROWS < rows ? m0 + ROWS : rows;
+        const Steps<64> st(a, s, m0, m1);
+        count = many_parts(st.n, nsplit);
+        at = (int64_t)unit * nsplit * a.rows_cap + m;
+        step = a.rows_cap;
     }
-    if (4 * lane >= a.kv.head_dim) return;
+    if (count <= 1) return;
+    const int q = threadIdx.x % QL, kk = threadIdx.x / QL;
+    float top = M_NONE, l = 0.0f;
+    v4f o = v4f{0, 0, 0, 0};
+    if (kk < KK) {      // (192 channels: 48 lanes a range, 16 lanes left over)
+#pragma unroll 4
+        for (int k = kk; k < count; k += KK) {
+            const int64_t p = at + k * step;
+            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * p);
+            const v4f v = *reinterpret_cast<const v4f*>(a.part_o + p * DP + 4 * q);
+            const float t = __builtin_fmaxf(top, ml.x), f0 = __builtin_amdgcn_exp2f(top - t), f1 = __builtin_amdgcn_exp2f(ml.x - t);
+            l = l * f0 + ml.y * f1;
+            o = o * f0 + v * f1;
+            top = t;
+        }
+        *reinterpret_cast<v4f*>(&red[kk][4 * q]) = o;
+        if (q == 0) {
+            red_m[kk] = top;
+            red_l[kk] = l;
+        }
+    }
+    __syncthreads();
+    if (kk != 0 || 4 * q >= a.kv.head_dim) return;
+    float all = M_NONE;
+    for (int k = 0; k < KK; ++k) all = __builtin_fmaxf(all, red_m[k]);
+    l = 0.0f;
+    o = v4f{0, 0, 0, 0};
+    for (int k = 0; k < KK; ++k) {
+        const float f = __builtin_amdgcn_exp2f(red_m[k] - all);
+        l += red_l[k] * f;
+        o += *reinterpret_cast<const v4f*>(&red[k][4 * q]) * f;
+    }
     const int i = m / a.ratio, j = m - i * a.ratio;
-    store_out4(a.out + ((s.row0 + i) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + j) * a.kv.head_dim, 4 * lane, a.kv.head_dim,
+    store_out4(a.out + ((s.row0 + i) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + j) * a.kv.head_dim, 4 * q, a.kv.head_dim,
                o * (l == 0.0f ? 0.0f : 1.0f / l));
 }
 
-// How a call runs: the kernel for few rows (16 mt of them at most) or the other one, and the ranges
-// that a sequence's tokens are cut into, so that there are workgroups for every CU.
+// How a call runs: the kernel for few rows (16 mt of them at most) or the other one, and room for the
+// ranges that sequences are cut into, so that there are workgroups for every CU.
 struct Plan {
     int mt;                 // 0: many rows
-    int64_t units, row_tiles;
-    int32_t nsplit, rows_cap;
-    size_t o_bytes, ml_bytes;
+    int64_t units, row_tiles, groups, slots;
+    int32_t target, nsplit, rows_cap;
+    size_t o_bytes, ml_bytes, range_bytes, bytes;
 };
+int64_t few_round(int g, int mt) {
+    int64_t r = 0;
+    kv_groups(32 * g, [&](auto gc) {
+        r = mt == 1 ? Few<gc(), 1>::ROUND : mt == 2 ? Few<gc(), 2>::ROUND : Few<gc(), 4>::ROUND;
+        return hipSuccess;
+    });
+    return r;
+}
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr int MANY_WAVES = 4;
 Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads) {
-    Plan p;
+    Plan p = {};
     const int64_t ratio = n_q_heads / c.n_heads, rows = b.max_rows * ratio, cap = b.max_pages * c.page_tokens;
-    p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= W4A4_KV_FEW_ROWS ? 4 : 0;
+    p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= W4A4_KV_FEW_ROWS && c.d_pad <= 128 ? 4 : 0;
     p.units = b.n_seqs * c.n_heads;
     p.rows_cap = (int32_t)rows;
     p.row_tiles = p.mt ? 1 : (rows + 32 * MANY_WAVES - 1) / (32 * MANY_WAVES);
-    const int64_t groups = p.units * p.row_tiles, target = p.mt ? 2048 : 512;
-    int64_t n = groups ? target / groups : 1;
-    if (n > cap / 256) n = cap / 256;
-    p.nsplit = (int32_t)(n < 1 ? 1 : n > 256 ? 256 : n);
-    p.o_bytes = p.nsplit > 1 ? (size_t)(p.units * p.nsplit * rows) * c.d_pad * 4 : 0;
-    p.ml_bytes = p.nsplit > 1 ? (size_t)(p.units * p.nsplit * rows) * 8 : 0;
+    p.nsplit = 1;
+    if (p.mt) {
+        const int64_t most = p.units * ((cap / 32 + FEW_LEAST) / FEW_LEAST), round = few_round(c.d_pad / 32, p.mt);
+        // One round of workgroups where few sequences leave most of it to full ranges (one row over 57600
+        // tokens, 40 heads: 59 us, in two rounds 62); else two, whose ranges are shorter, so that the
+        // last ones end closer together (64 ragged sequences: 220 us, in one round 240)
+        const int64_t target = p.units <= round / 4 ? round - p.units : 2 * round;
+        p.groups = p.units;
+        if (cap > 32 * FEW_LEAST) {
+            p.target = (int32_t)target;
+            p.groups = most < target + p.units ? most : target + p.units;
+            p.slots = most < 2 * target ? most : 2 * target;
+        }
+    } else {
+        int64_t n = 512 / (p.units * p.row_tiles > 0 ? p.units * p.row_tiles : 1);
+        if (n > cap / 256) n = cap / 256;
+        p.nsplit = (int32_t)(n < 1 ? 1 : n > 256 ? 256 : n);
+        p.groups = p.units * p.row_tiles * p.nsplit;
+        p.slots = p.nsplit > 1 ? p.units * p.nsplit : 0;
+    }
+    p.o_bytes = up256((size_t)(p.slots * rows) * c.d_pad * 4);
+    p.ml_bytes = up256((size_t)(p.slots * rows) * 8);
+    p.range_bytes = p.target ? up256((size_t)b.n_seqs * 8) : 0;
+    p.bytes = p.o_bytes + p.ml_bytes + p.range_bytes;
     return p;
 }
 
 template <int G, int MT>
 void run_few(const AttnArgs& a, const Plan& p, bool qb, hipStream_t st) {
-    const dim3 grid((uint32_t)(p.units * p.nsplit));
-    if (qb) hipLaunchKernelGGL((kv_few_kernel<G, MT, true>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((kv_few_kernel<G, MT, false>), grid, dim3(256), 0, st, a);
+    const dim3 grid((uint32_t)p.groups), threads(Few<G, MT>::NW * 64);
+    if (qb) hipLaunchKernelGGL((kv_few_kernel<G, MT, true>), grid, threads, 0, st, a);
+    else hipLaunchKernelGGL((kv_few_kernel<G, MT, false>), grid, threads, 0, st, a);
 }
 
 }  // namespace
 
 size_t kv_attention_ws(int64_t, const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads) {
-    const Plan p = plan_of(b, c, n_q_heads);
-    return (p.o_bytes + 255) / 256 * 256 + (p.ml_bytes + 255) / 256 * 256;
+    return plan_of(b, c, n_q_heads).bytes;
 }
 
 hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads,
@@ -653,30 +829,31 @@ hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4
     a.q_head = Q.head_stride;
     a.out = O;
     a.part_o = (float*)ws;
-    a.part_ml = (float*)((uint8_t*)ws + (p.o_bytes + 255) / 256 * 256);
+    a.part_ml = (float*)((uint8_t*)ws + p.o_bytes);
+    a.ranges = (int64_t*)((uint8_t*)ws + p.o_bytes + p.ml_bytes);
     a.window = window;
     a.scale = scale * 1.44269504088896340736f;
     a.ratio = n_q_heads / c.n_heads;
     a.causal = causal ? 1 : 0;
-    a.nsplit = p.nsplit;
+    a.target = p.target;
     a.rows_cap = p.rows_cap;
     const bool qb = Q.dtype == W4A4_X_BF16;
     return kv_groups(c.d_pad, [&](auto gc) {
         constexpr int G = gc();
-        const dim3 join((uint32_t)((p.units * p.rows_cap + 3) / 4));
+        const dim3 join((uint32_t)(p.units * p.rows_cap));
         if (p.mt) {
             if (p.mt == 1) run_few<G, 1>(a, p, qb, stream);
             else if (p.mt == 2) run_few<G, 2>(a, p, qb, stream);
-            else run_few<G, 4>(a, p, qb, stream);
+            else if constexpr (G <= 4) run_few<G, 4>(a, p, qb, stream);
         } else {
-            const dim3 grid((uint32_t)(p.units * p.row_tiles * p.nsplit));
-            if (qb) hipLaunchKernelGGL((kv_many_kernel<G, MANY_WAVES, true>), grid, dim3(64 * MANY_WAVES), 0, stream, a, (uint32_t)p.row_tiles);
-            else hipLaunchKernelGGL((kv_many_kernel<G, MANY_WAVES, false>), grid, dim3(64 * MANY_WAVES), 0, stream, a, (uint32_t)p.row_tiles);
+            const dim3 grid((uint32_t)p.groups), threads(64 * MANY_WAVES);
+            if (qb) hipLaunchKernelGGL((kv_many_kernel<G, MANY_WAVES, true>), grid, threads, 0, stream, a, (uint32_t)p.row_tiles, p.nsplit);
+            else hipLaunchKernelGGL((kv_many_kernel<G, MANY_WAVES, false>), grid, threads, 0, stream, a, (uint32_t)p.row_tiles, p.nsplit);
         }
         const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || p.nsplit == 1) return e;
-        if (p.mt) hipLaunchKernelGGL((kv_join_kernel<G, 32, 0>), join, dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((kv_join_kernel<G, 64, 32 * MANY_WAVES>), join, dim3(256), 0, stream, a);
+        if (e != hipSuccess || !p.slots) return e;
+        if (p.mt) hipLaunchKernelGGL((kv_join_kernel<G, 0>), join, dim3(256), 0, stream, a, 1);
+        else hipLaunchKernelGGL((kv_join_kernel<G, 32 * MANY_WAVES>), join, dim3(256), 0, stream, a, p.nsplit);
         return hipGetLastError();
     });
 }

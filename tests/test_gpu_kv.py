@@ -202,7 +202,7 @@ def _check_attention(s, rows, Hq, qt=BF16, causal=True, window=0, scale=None, le
     assert bool((ws[-512:] == 255).all()) and bool((O[n:] == 7).all())
     qb = torch.from_numpy(q).bfloat16().double()
     sc = s.D ** -0.5 if scale is None else scale
-    few = (max(rows) if max_rows is None else max_rows) * (Hq // s.H) <= 64
+    few = (max(rows) if max_rows is None else max_rows) * (Hq // s.H) <= (64 if s.D <= 128 else 32)
     at, err2, var, nr2 = 0, 0.0, 0.0, 0.0
     for i, r in enumerate(rows):
         k, v = s.values(i)
