@@ -467,22 +467,39 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
 
 // ---------------------------------------------------------------- many rows
 //
-// A workgroup owns 32 rows a wavefront and walks tiles of 64 tokens.  The tile's codes are widened
-// once, a block of 16 tokens a wavefront, into two LDS buffers that take turns; the codes of the tile after
-// are in flight meanwhile.  Rows of LDS are 16 bytes longer than their data, so that the
-// operand reads of 16 lanes touch every bank once.
+// A workgroup owns 32 rows a wavefront and walks tiles of 64 tokens.  A tile's codes are widened once,
+// every wavefront its share, into LDS; rows of LDS are 16 bytes longer than their data, so that the
+// operand reads of 16 lanes touch every bank once.  The loop is a pipeline with one barrier a tile: while the
+// matrix unit multiplies tile k's keys, the codes of tile k + 1 are widened; while it multiplies tile
+// k - 1's weights with its values, tile k's scores become weights, a quarter of them as soon as that quarter of the
+// old ones has been used.  The codes of tile k + 2 are on their way meanwhile.  The order of instructions is written
+// out: a matrix instruction, the read of an operand FR steps ahead, a few vector instructions.
+//
+// Weights are taken with the maximum of the tiles before; where their sum shows that a score passed it by
+// far, the maximum is renewed and they are taken again.
+template <int G, int WAVES> struct Many {
+    static constexpr int NW = WAVES, ROWS = 32 * NW, PARTS = NW / 4;      // wavefronts; those that share a block's widening
+    static constexpr int KG = (G + PARTS - 1) / PARTS, VG = (G + 2 * PARTS - 1) / (2 * PARTS);      // groups that a lane widens
+    static constexpr int KLD = 64 * G + 16, VLD = 144, KB = 64 * KLD, VB = 32 * G * VLD;
+    // value buffers: widened a tile ahead and read a tile behind, without a barrier between the two.  Wide heads,
+    // for which four do not fit, and small workgroups, of which two share a CU, take keys and values in turn.
+    static constexpr int VSLOTS = G <= 4 && NW == 8 ? 4 : 2;
+    static constexpr int OCC = G <= 4 ? 2 : 1;
+};
+constexpr float P_MOST = 256.0f;
 // The ranges that a row tile's steps are cut into, out of nsplit that there is room for.
-__device__ __forceinline__ int many_parts(int n, int nsplit) { return n / 4 < 1 ? 1 : n / 4 < nsplit ? n / 4 : nsplit; }
+constexpr int MANY_LEAST = 8;
+__device__ __forceinline__ int many_parts(int n, int nsplit) { return n / MANY_LEAST < 1 ? 1 : n / MANY_LEAST < nsplit ? n / MANY_LEAST : nsplit; }
 
-template <int G, int NW, bool QB>
-__global__ __launch_bounds__(NW * 64, (G <= 4 ? 2 : 1)) void kv_many_kernel(AttnArgs a, uint32_t row_tiles, int32_t nsplit) {
+template <int G, int WAVES, bool QB>
+__global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_kernel(AttnArgs a, uint32_t row_tiles, int32_t nsplit) {
     typedef KvBlock<G> L;
-    constexpr int DP = 32 * G, KLD = 64 * G + 16, VLD = 144, KB = 64 * KLD, VB = DP * VLD, BUF = KB + VB, ROWS = 32 * NW;
-    constexpr int NB = (G + 1) / 2;                        // value groups a lane converts
-    static_assert(NW == 4, "a wavefront widens one of the tile's four blocks");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][BUF];
-    __shared__ uint32_t flags[2][4];                       // of a block: 1 values that are NaN, 2 not there
-    __shared__ uint8_t nans[2][64];                        // a token's groups that are NaN
+    typedef Many<G, WAVES> M;
+    constexpr int DP = 32 * G, ROWS = M::ROWS, KG = M::KG, VG = M::VG, KLD = M::KLD, VLD = M::VLD, N = 4 * G, FR = 4;
+    __shared__ __attribute__((aligned(16))) uint8_t keys[2][M::KB];
+    __shared__ __attribute__((aligned(16))) uint8_t vals[M::VSLOTS][M::VB];
+    __shared__ uint4 flags[M::VSLOTS][M::PARTS];           // by share and block: 1 values that are NaN, 2 not there
+    __shared__ uint8_t nans[M::VSLOTS][M::PARTS][64];      // a token's groups that are NaN
     const int lane = threadIdx.x & 63, c = lane & 31, h2 = lane >> 5, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sp = blockIdx.x % nsplit;
@@ -501,8 +518,52 @@ __global__ __launch_bounds__(NW * 64, (G <= 4 ? 2 : 1)) void kv_many_kernel(Attn
     if (sp >= parts) return;
     const int s0 = (int)((int64_t)st.n * sp / parts), s1 = (int)((int64_t)st.n * (sp + 1) / parts);
 
-    const int m = (int)m0 + wave * 32 + c, qi = m / a.ratio, qj = m - qi * a.ratio;
-    const bool on = wave * 32 + c < rows;
+    const int row = wave * 32 + c, m = (int)m0 + row, qi = m / a.ratio, qj = m - qi * a.ratio;
+    const bool on = row < rows;
+    // tokens that the row sees
+    const int64_t pos = (int64_t)s.first + qi, from = a.causal && a.window ? pos - a.window + 1 : 0;
+    const int32_t lo = from < 0 ? 0 : (int32_t)from, hi = !on ? -1 : a.causal ? (int32_t)pos : s.len - 1;
+    // tokens that all of the wavefront's rows see (where some row is missing: none)
+    const int64_t i0 = ((int)m0 + wave * 32) / a.ratio, i1 = ((int)m0 + wave * 32 + 31) / a.ratio;
+    const int64_t all_hi = wave * 32 + 32 > rows ? -1 : a.causal ? s.first + i0 : s.len - 1;
+    const int64_t all_lo = a.causal && a.window ? s.first + i1 - a.window + 1 : 0;
+
+    v16f acc[G];
+#pragma unroll
+    for (int d = 0; d < G; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+    float mx = M_NONE, sum = 0.0f;
+
+    // This wavefront's share of a tile: of block `blk` the keys of token r16, groups from k0 on, and of the values
+    // of tokens 4 hh .. and 8 + 4 hh .. the groups from v0 on (shares that do not divide overlap).
+    const int blk = wave / M::PARTS, share = wave % M::PARTS, hh = g & 1;
+    const int k0 = share * KG < G - KG ? share * KG : G - KG;
+    const int vi = (2 * share + (g >> 1)) * VG, v0 = vi < G - VG ? vi : G - VG;
+    uint32_t kw[KG], ks[(G + 3) / 4], vw[2][VG], vs[2][VG];
+    bool there = false;
+    uint64_t addr = 0;      // the block's address in 64 tiles, one a lane (zero: not there, or past the last tile)
+    auto fetch = [&](int k) __attribute__((always_inline)) {
+        const int j = (k - s0) & 63;
+        if (j == 0) addr = k + lane < s1 ? (uint64_t)(uintptr_t)kv_block(a.kv, b, (uint32_t)(st.start / 16 + 4 * (k + lane) + blk), h) : 0;
+        const uint32_t al = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)addr, j), ah = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(addr >> 32), j);
+        const uint8_t* p = (const uint8_t*)(uintptr_t)((uint64_t)ah << 32 | al);
+        there = p != nullptr;
+        p = p ? p : a.kv.data;
+#pragma unroll
+        for (int d = 0; d < KG; ++d) kw[d] = *reinterpret_cast<const uint32_t*>(p + lane * 4 * G + 4 * (k0 + d));
+        if constexpr (G == 1) ks[0] = p[L::KS + r16];
+        else if constexpr (G == 2) ks[0] = *reinterpret_cast<const uint16_t*>(p + L::KS + r16 * 2);
+        else load_words<(G + 3) / 4>(p + L::KS + r16 * L::SG, ks);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int d = 0; d < VG; ++d) {
+                vw[u][d] = *reinterpret_cast<const uint32_t*>(p + L::V + ((hh + 2 * u) * 16 + r16) * 4 * G + 4 * (v0 + d));
+                vs[u][d] = *reinterpret_cast<const uint32_t*>(p + L::VS + (hh + 2 * u) * 4 * L::SG + 4 * (v0 + d));
+            }
+    };
+    if (s0 < s1) fetch(s0);      // on its way while the queries are read
     v8bf q[2 * G];
     {
         const int64_t at = on ? (s.row0 + qi) * a.q_row + (int64_t)(h * a.ratio + qj) * a.q_head : 0;
@@ -513,171 +574,242 @@ __global__ __launch_bounds__(NW * 64, (G <= 4 ? 2 : 1)) void kv_many_kernel(Attn
             q[d] = pack_q(x);
         }
     }
-    const int64_t pos = (int64_t)s.first + qi, from = a.causal && a.window ? pos - a.window + 1 : 0;
-    const int32_t lo = from < 0 ? 0 : (int32_t)from, hi = !on ? -1 : a.causal ? (int32_t)pos : s.len - 1;
-    // the wavefront's rows: tokens that any of them sees, and that all of them see
-    const int w0 = wave * 32, w1 = w0 + 32 < rows ? w0 + 32 : rows;
-    const bool idle = w0 >= rows;
-    const int64_t i0 = ((int)m0 + w0) / a.ratio, i1 = ((int)m0 + (idle ? w0 : w1 - 1)) / a.ratio;
-    const int64_t any_hi = idle ? -1 : a.causal ? s.first + i1 : s.len - 1, all_hi = a.causal ? s.first + i0 : s.len - 1;
-    const int64_t any_lo = a.causal && a.window ? s.first + i0 - a.window + 1 : 0, all_lo = a.causal && a.window ? s.first + i1 - a.window + 1 : 0;
-
-    v16f acc[G];
-#pragma unroll
-    for (int d = 0; d < G; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-    float mx = M_NONE, sum = 0.0f;
-
-    // codes of one block: keys of token r16; values of tokens 4 hh .. and 8 + 4 hh .., groups from gb on
-    const int hh = g & 1, gb = (g >> 1) * NB;
-    uint32_t kw[G], ks[(G + 3) / 4], vw[2][NB], vs[2][NB];
-    bool there;
-    auto fetch = [&](int step) __attribute__((always_inline)) {
-        const uint8_t* p = kv_block(a.kv, b, (uint32_t)(st.start / 16 + 4 * step + wave), h);
-        there = p != nullptr;
-        p = p ? p : a.kv.data;
-        load_words<G>(p + lane * 4 * G, kw);
-        if constexpr (G == 1) ks[0] = p[L::KS + r16];
-        else if constexpr (G == 2) ks[0] = *reinterpret_cast<const uint16_t*>(p + L::KS + r16 * 2);
-        else load_words<(G + 3) / 4>(p + L::KS + r16 * L::SG, ks);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int d = 0; d < NB; ++d) {
-                const int gd = gb + d < G ? gb + d : G - 1;
-                vw[u][d] = *reinterpret_cast<const uint32_t*>(p + L::V + ((hh + 2 * u) * 16 + r16) * 4 * G + 4 * gd);
-                vs[u][d] = *reinterpret_cast<const uint32_t*>(p + L::VS + (hh + 2 * u) * 4 * L::SG + 4 * gd);
-            }
-    };
-    auto widen = [&](int slot) __attribute__((always_inline)) {
-        uint8_t* const kd = lds[slot] + (wave * 16 + r16) * KLD + g * 16;
-#pragma unroll
-        for (int d = 0; d < G; ++d) *reinterpret_cast<v8bf*>(kd + d * 64) = widen_key(kw[d], scale_of(ks[d / 4], d & 3));
+    // Before a fetched block is widened: its flag, and scale codes that a weight of zero may not be multiplied with.
+    auto prepare = [&](int slot) __attribute__((always_inline)) {
+        uint32_t flag = there ? 0u : 2u;
         bool odd = false;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int d = 0; d < NB; ++d) odd |= wild(vs[u][d]);
-        uint32_t flag = there ? 0u : 2u;
+            for (int d = 0; d < VG; ++d) odd |= wild(vs[u][d]);
         if (__any(odd)) {      // rare: values that are NaN go by a list of their own
             uint32_t bits[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int d = 0; d < NB; ++d) {
+                for (int d = 0; d < VG; ++d) {
                     uint32_t nan;
                     vs[u][d] = tame(vs[u][d], nan);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) bits[4 * u + j] |= gb + d < G && (nan >> j & 1) ? 1u << (gb + d) : 0u;
+                    for (int j = 0; j < 4; ++j) bits[4 * u + j] |= (nan >> j & 1) ? 1u << (v0 + d) : 0u;
                 }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) bits[k] |= (uint32_t)__shfl_xor((int)bits[k], 32);      // the other half of the groups
+            for (int k = 0; k < 8; ++k) bits[k] |= (uint32_t)__shfl_xor((int)bits[k], 32);      // the other half's groups
             if (r16 == 0 && g < 2)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) nans[slot][wave * 16 + 4 * hh + (k >> 2) * 8 + (k & 3)] = (uint8_t)bits[k];
+                for (int k = 0; k < 8; ++k) nans[slot][share][blk * 16 + 4 * hh + (k >> 2) * 8 + (k & 3)] = (uint8_t)bits[k];
             flag |= 1u;
         }
-        if (lane == 0) flags[slot][wave] = flag;
-        uint8_t* const vd = lds[slot] + KB + r16 * VLD + (2 * wave + hh) * 16;
-#pragma unroll
-        for (int d = 0; d < NB; ++d) {
-            if (gb + d >= G) continue;
-            v8bf v0, v1;
-            widen_value(vw[0][d], vs[0][d], vw[1][d], vs[1][d], v0, v1);
-            *reinterpret_cast<v8bf*>(vd + (gb + d) * 32 * VLD) = v0;
-            *reinterpret_cast<v8bf*>(vd + ((gb + d) * 32 + 16) * VLD) = v1;
+        if (lane == 0) reinterpret_cast<uint32_t*>(&flags[slot][share])[blk] = flag;
+    };
+    // The widening in UNITS parts: a group of keys each, then two tokens of a group of values each.
+    constexpr int UNITS = KG + 4 * VG;
+    uint32_t vlo[4], vhi[4];
+    auto widen = [&](int n, int kslot, int vslot) __attribute__((always_inline)) {
+        if (n < KG) {
+            const int kg = k0 + n;
+            const float f = __uint_as_float((G > 4 && kg >= 4 ? ks[(G + 3) / 4 - 1] : ks[0]) >> (8 * (kg & 3)) << 23);
+            *reinterpret_cast<v8bf*>(keys[kslot] + (blk * 16 + r16) * KLD + g * 16 + kg * 64) = widen_key(kw[n], f);
+            return;
+        }
+        const int d = (n - KG) / 4, i = (n - KG) & 3, u = i >> 1, j = 2 * (i & 1);
+        const uint32_t w = vw[u][d], x = vs[u][d];
+        const uint32_t p0 = j ? widen2<2>(w, scale_of(x, 2)) : widen2<0>(w, scale_of(x, 0));
+        const uint32_t p1 = j ? widen2<3>(w, scale_of(x, 3)) : widen2<1>(w, scale_of(x, 1));
+        vlo[i] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
+        vhi[i] = __builtin_amdgcn_perm(p1, p0, 0x07060302u);
+        if (i == 3) {
+            uint8_t* const vd = vals[vslot] + ((v0 + d) * 32 + r16) * VLD + (2 * blk + hh) * 16;
+            *reinterpret_cast<v8bf*>(vd) = join8(vlo[0], vlo[1], vlo[2], vlo[3]);
+            *reinterpret_cast<v8bf*>(vd + 16 * VLD) = join8(vhi[0], vhi[1], vhi[2], vhi[3]);
         }
     };
 
-    if (s0 < s1) {
-        fetch(s0);
-        widen(0);
-        if (s0 + 1 < s1) fetch(s0 + 1);
-    }
-    for (int k = s0; k < s1; ++k) {
-        const int slot = (k - s0) & 1;
-        __syncthreads();
-        const int64_t t0 = st.start + (int64_t)k * 64;
-        const uint32_t fl = flags[slot][0] | flags[slot][1] | flags[slot][2] | flags[slot][3];
+    v16f sc[2];           // a tile's scores, 32 tokens each
+    uint32_t pw[16];      // weights
+    float tile_sum = 0.0f;
+    // weights 2 i, 2 i + 1
+    auto weigh = [&](int i) __attribute__((always_inline)) {
+        const float pa = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 3][2 * (i & 7)], a.scale, -mx));
+        const float pb = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 3][2 * (i & 7) + 1], a.scale, -mx));
+        tile_sum = i == 0 ? pa + pb : tile_sum + (pa + pb);
+        pw[i] = pk_bf16(pa, pb);
+        asm volatile("" : "+v"(pw[i]), "+v"(tile_sum));      // here, between the matrix instructions
+    };
+    // Whether the weights just taken may be used; if not, they are taken again with a new maximum.
+    auto settle = [&]() __attribute__((always_inline)) {
+        if (__any(!(tile_sum <= P_MOST))) {
+            float top = sc[0][0];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {      // 32 tokens
-            const int64_t p0 = t0 + 32 * half;
-            if (p0 > any_hi || p0 + 31 < any_lo) continue;
-            v16f sc;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sc[i] = 0.0f;
-            const uint8_t* const kp = lds[slot] + (half * 32 + c) * KLD + h2 * 16;
-#pragma unroll
-            for (int d = 0; d < 2 * G; ++d)
-                sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const v8bf*>(kp + d * 32), q[d], sc, 0, 0, 0);
-            if (p0 + 31 > all_hi || p0 < all_lo || (fl & 2)) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int32_t t = (int32_t)p0 + 8 * (i >> 2) + 4 * h2 + (i & 3);
-                    const bool see = t >= lo && t <= hi && !(flags[slot][2 * half + (i >> 3)] & 2);
-                    sc[i] = see ? sc[i] : -__builtin_inff();
-                }
-            }
-            float top = sc[0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, sc[i]);
+            for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i >> 4][i & 15]);
             top *= a.scale;
-            if (__any(top > mx + M_SLACK)) {
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                const float mn = __builtin_fmaxf(mx, top), f = __builtin_amdgcn_exp2f(mx - mn);
-                mx = mn;
-                sum *= f;
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            const float n = __builtin_fmaxf(mx, top), f = __builtin_amdgcn_exp2f(mx - n);
+            mx = n;
+            sum *= f;
 #pragma unroll
-                for (int d = 0; d < G; ++d) acc[d] *= f;
-            }
-            uint32_t pw[8];
+            for (int d = 0; d < G; ++d) acc[d] *= f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float pa = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i], a.scale, -mx));
-                const float pb = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i + 1], a.scale, -mx));
-                sum += pa;
-                sum += pb;
-                pw[i] = pk_bf16(pa, pb);
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const v8bf pf = join8(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]);
-                const uint8_t* const vp = lds[slot] + KB + c * VLD + ((half * 2 + u) * 2 + h2) * 16;
-#pragma unroll
-                for (int d = 0; d < G; ++d)
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const v8bf*>(vp + d * 32 * VLD), pf, acc[d], 0, 0, 0);
-            }
-            if (fl & 1) {
-                uint32_t bad = 0;
-                for (int t = 0; t < 32; ++t) {
-                    if (!(flags[slot][2 * half + (t >> 4)] & 1)) continue;
-                    const int32_t tp = (int32_t)p0 + t;
-                    bad |= tp >= lo && tp <= hi && !(flags[slot][2 * half + (t >> 4)] & 2) ? nans[slot][half * 32 + t] : 0u;
-                }
-#pragma unroll
-                for (int d = 0; d < G; ++d)
-                    if (bad >> d & 1) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[d][i] = __uint_as_float(0x7FC00000u);
-                    }
-            }
+            for (int i = 0; i < 16; ++i) weigh(i);
         }
-        if (k + 1 < s1) {
-            widen(slot ^ 1);
-            if (k + 2 < s1) fetch(k + 2);
+        sum += tile_sum;
+    };
+    v8bf fr[FR];
+    const int key_at = c * KLD + h2 * 16, val_at = c * VLD + h2 * 16;
+    auto key_operand = [&](int kslot, int i) __attribute__((always_inline)) {      // step i: channels 16 (i / 2) .., tokens 32 (i % 2) ..
+        return *reinterpret_cast<const v8bf*>(keys[kslot] + key_at + (i & 1) * 32 * KLD + (i >> 1) * 32);
+    };
+    auto value_operand = [&](int slot, int i) __attribute__((always_inline)) {      // step i: tokens 16 (i / G) .., channels 32 (i % G) ..
+        return *reinterpret_cast<const v8bf*>(vals[slot] + val_at + (i % G) * 32 * VLD + i / G * 32);
+    };
+    auto key_step = [&](int i) __attribute__((always_inline)) {
+        if (i < 2) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sc[i][e] = 0.0f;
+        }
+        sc[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % FR], q[i >> 1], sc[i & 1], 0, 0, 0);
+    };
+    auto value_step = [&](int i) __attribute__((always_inline)) {
+        const int u = i / G;
+        acc[i % G] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % FR], join8(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]), acc[i % G], 0, 0, 0);
+    };
+    // A tile's flags by block; bit 0 of any, bit 1 of any.
+    auto flags_of = [&](int slot) __attribute__((always_inline)) {
+        uint4 f = flags[slot][0];
+        if constexpr (M::PARTS > 1) {
+            const uint4 o = flags[slot][1];
+            f = make_uint4(f.x | o.x, f.y | o.y, f.z | o.z, f.w | o.w);
+        }
+        return f;
+    };
+    // rare: for every NaN that the lane's row sees, its group of channels
+    auto spread_nans = [&](int slot, int64_t p0) __attribute__((always_inline)) {
+        const uint4 f = flags_of(slot);
+        if (!((f.x | f.y | f.z | f.w) & 1)) return;
+        const uint32_t fb[4] = {f.x, f.y, f.z, f.w};
+        uint32_t bad = 0;
+        for (int t = 0; t < 64; ++t) {
+            const int32_t tp = (int32_t)p0 + t;
+            if ((fb[t >> 4] & 2) || tp < lo || tp > hi) continue;
+            for (int w = 0; w < M::PARTS; ++w)
+                if (reinterpret_cast<const uint32_t*>(&flags[slot][w])[t >> 4] & 1) bad |= nans[slot][w][t];
+        }
+#pragma unroll
+        for (int d = 0; d < G; ++d)
+            if (bad >> d & 1) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[d][i] = __uint_as_float(0x7FC00000u);
+            }
+    };
+    // The scores of tokens that a row does not see.
+    auto hide = [&](int k, int slot) __attribute__((always_inline)) {
+        const int64_t p0 = st.start + (int64_t)k * 64;
+        const uint4 f = flags_of(slot);
+        if (p0 + 63 <= all_hi && p0 >= all_lo && !((f.x | f.y | f.z | f.w) & 2)) return;
+        const uint32_t gone = (f.x >> 1 & 1) | (f.y & 2) | (f.z & 2) << 1 | (f.w & 2) << 2;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int32_t t = (int32_t)p0 + 8 * (i >> 2) + 4 * h2 + (i & 3);
+            if (t < lo || t > hi || (gone >> (i >> 3) & 1)) sc[i >> 4][i & 15] = -__builtin_inff();
+        }
+    };
+    auto widen_all = [&](int kslot, int slot) __attribute__((always_inline)) {
+        prepare(slot);
+#pragma unroll
+        for (int e = 0; e < UNITS; ++e) widen(e, kslot, slot);
+    };
+    constexpr int VS = M::VSLOTS - 1;      // a mask
+    if (s0 < s1) {
+        widen_all(0, 0);
+        fetch(s0 + 1);
+        __syncthreads();
+    }
+    if constexpr (M::VSLOTS == 4) {
+        // Tile s0 + j: its scores, then its weights, beside them (unless it is the first) tile j - 1's weights and values.
+        auto body = [&](auto first, int j) __attribute__((always_inline)) {
+            constexpr bool FIRST = first();
+            prepare((j + 1) & VS);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                key_step(i);
+                if (i + FR < N) fr[i % FR] = key_operand(j & 1, i + FR);
+                else if constexpr (!FIRST) fr[i % FR] = value_operand((j - 1) & VS, i + FR - N);
+#pragma unroll
+                for (int e = UNITS * i / N; e < UNITS * (i + 1) / N; ++e) widen(e, (j + 1) & 1, (j + 1) & VS);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(s0 + j + 2);
+            __syncthreads();
+            hide(s0 + j, j & VS);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (!FIRST) {
+                    value_step(i);
+                    if (i + FR < N) fr[i % FR] = value_operand((j - 1) & VS, i + FR);
+                }
+                if (i + FR >= N) fr[i % FR] = key_operand((j + 1) & 1, i + FR - N);
+                // the weights of 16 tokens are free after their G steps
+                if (i >= G) {
+#pragma unroll
+                    for (int e = 4 * (i - G) / G; e < 4 * (i + 1 - G) / G; ++e) weigh(e);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 12; e < 16; ++e) weigh(e);
+            if constexpr (!FIRST) spread_nans((j - 1) & VS, st.start + (int64_t)(s0 + j - 1) * 64);
+            settle();
+        };
+        if (s0 < s1) {
+#pragma unroll
+            for (int i = 0; i < FR; ++i) fr[i] = key_operand(0, i);
+            body(std::true_type(), 0);
+            const int n = s1 - s0;
+            for (int j = 1; j < n; ++j) body(std::false_type(), j);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                fr[i % FR] = value_operand((n - 1) & VS, i);
+                value_step(i);
+            }
+            spread_nans((n - 1) & VS, st.start + (int64_t)(s1 - 1) * 64);
+        }
+    } else {
+        for (int j = 0; j < s1 - s0; ++j) {
+            if (j) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < FR; ++i) fr[i] = key_operand(j & 1, i);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                key_step(i);
+                if (i + FR < N) fr[i % FR] = key_operand(j & 1, i + FR);
+                else fr[i % FR] = value_operand(j & VS, i + FR - N);
+            }
+            hide(s0 + j, j & VS);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) weigh(e);
+            settle();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                value_step(i);
+                if (i + FR < N) fr[i % FR] = value_operand(j & VS, i + FR);
+            }
+            spread_nans(j & VS, st.start + (int64_t)(s0 + j) * 64);
+            widen_all((j + 1) & 1, (j + 1) & VS);
+            fetch(s0 + j + 2);
         }
     }
     sum += __shfl_xor(sum, 32);
     if (!on) return;
-    const float r = parts > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float f = parts > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
     const int64_t at = (unit * nsplit + sp) * a.rows_cap + m;
     uint16_t* const out = a.out + ((s.row0 + qi) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + qj) * a.kv.head_dim;
 #pragma unroll
     for (int d = 0; d < G; ++d)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const v4f v = v4f{acc[d][4 * u] * r, acc[d][4 * u + 1] * r, acc[d][4 * u + 2] * r, acc[d][4 * u + 3] * r};
+            const v4f v = v4f{acc[d][4 * u] * f, acc[d][4 * u + 1] * f, acc[d][4 * u + 2] * f, acc[d][4 * u + 3] * f};
             const int ch = 32 * d + 8 * u + 4 * h2;
             if (parts == 1) store_out4(out, ch, a.kv.head_dim, v);
             else *reinterpret_cast<v4f*>(a.part_o + at * DP + ch) = v;
@@ -688,11 +820,33 @@ __global__ __launch_bounds__(NW * 64, (G <= 4 ? 2 : 1)) void kv_many_kernel(Attn
     }
 }
 
-// The ranges' results of one row a workgroup: the common maximum, then the weighted sums; a quarter of
-// a row's lanes take four channels each and every 256 / lanes-th range.  ROWS 0: the ranges of the few-row
-// kernel, else those of tiles of ROWS rows.
-template <int G, int ROWS>
-__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs a, int32_t nsplit) {
+// The ranges' results of a row: the common maximum, and the weighted sums.  `step` lies between two ranges' rows.
+template <int DP>
+__device__ __forceinline__ void join_ranges(const AttnArgs& a, int64_t at, int64_t step, int from, int count, int stride, int q, float& top, float& l, v4f& o) {
+    top = M_NONE;
+    l = 0.0f;
+    o = v4f{0, 0, 0, 0};
+#pragma unroll 4
+    for (int k = from; k < count; k += stride) {
+        const int64_t p = at + k * step;
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * p);
+        const v4f v = *reinterpret_cast<const v4f*>(a.part_o + p * DP + 4 * q);
+        const float t = __builtin_fmaxf(top, ml.x), f0 = __builtin_amdgcn_exp2f(top - t), f1 = __builtin_amdgcn_exp2f(ml.x - t);
+        l = l * f0 + ml.y * f1;
+        o = o * f0 + v * f1;
+        top = t;
+    }
+}
+__device__ __forceinline__ void store_joined(const AttnArgs& a, const KvSeq& s, int h, int m, int q, float l, v4f o) {
+    if (4 * q >= a.kv.head_dim) return;
+    const int i = m / a.ratio, j = m - i * a.ratio;
+    store_out4(a.out + ((s.row0 + i) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + j) * a.kv.head_dim, 4 * q, a.kv.head_dim,
+               o * (l == 0.0f ? 0.0f : 1.0f / l));
+}
+
+// Of few rows, one a workgroup: d_pad / 4 lanes take four channels each and every KK-th range.
+template <int G>
+__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs a) {
     constexpr int DP = 32 * G, QL = DP / 4, KK = 256 / QL;
     __shared__ __attribute__((aligned(16))) float red[KK][DP];
     __shared__ float red_m[KK], red_l[KK];
@@ -701,37 +855,15 @@ __global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs a, int32_t nsplit
     const int64_t b = unit / (uint32_t)a.kv.n_heads;
     const int h = (int)(unit - (uint32_t)b * (uint32_t)a.kv.n_heads);
     const KvSeq s = kv_seq(a.kv, b);
-    const int rows = s.done * a.ratio;
-    if (m >= rows) return;
-    int count;
-    int64_t at, step;
-    if constexpr (ROWS == 0) {
-        const int64_t r = a.ranges[b];
-        count = (int)(r & 0xFFFFF);
-        at = ((r >> 20) * a.kv.n_heads + h) * a.rows_cap + m;
-        step = (int64_t)a.kv.n_heads * a.rows_cap;
-    } else {
-        const int m0 = m / ROWS * ROWS, m1 = m0 + ROWS < rows ? m0 + ROWS : rows;
-        const Steps<64> st(a, s, m0, m1);
-        count = many_parts(st.n, nsplit);
-        at = (int64_t)unit * nsplit * a.rows_cap + m;
-        step = a.rows_cap;
-    }
+    if (m >= s.done * a.ratio) return;
+    const int64_t r = a.ranges[b];
+    const int count = (int)(r & 0xFFFFF);
     if (count <= 1) return;
     const int q = threadIdx.x % QL, kk = threadIdx.x / QL;
-    float top = M_NONE, l = 0.0f;
-    v4f o = v4f{0, 0, 0, 0};
+    float top, l;
+    v4f o;
     if (kk < KK) {      // (192 channels: 48 lanes a range, 16 lanes left over)
-#pragma unroll 4
-        for (int k = kk; k < count; k += KK) {
-            const int64_t p = at + k * step;
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * p);
-            const v4f v = *reinterpret_cast<const v4f*>(a.part_o + p * DP + 4 * q);
-            const float t = __builtin_fmaxf(top, ml.x), f0 = __builtin_amdgcn_exp2f(top - t), f1 = __builtin_amdgcn_exp2f(ml.x - t);
-            l = l * f0 + ml.y * f1;
-            o = o * f0 + v * f1;
-            top = t;
-        }
+        join_ranges<DP>(a, ((r >> 20) * a.kv.n_heads + h) * a.rows_cap + m, (int64_t)a.kv.n_heads * a.rows_cap, kk, count, KK, q, top, l, o);
         *reinterpret_cast<v4f*>(&red[kk][4 * q]) = o;
         if (q == 0) {
             red_m[kk] = top;
@@ -739,46 +871,69 @@ __global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs a, int32_t nsplit
         }
     }
     __syncthreads();
-    if (kk != 0 || 4 * q >= a.kv.head_dim) return;
-    float all = M_NONE;
-    for (int k = 0; k < KK; ++k) all = __builtin_fmaxf(all, red_m[k]);
+    if (kk != 0) return;
+    top = M_NONE;
+    for (int k = 0; k < KK; ++k) top = __builtin_fmaxf(top, red_m[k]);
     l = 0.0f;
     o = v4f{0, 0, 0, 0};
     for (int k = 0; k < KK; ++k) {
-        const float f = __builtin_amdgcn_exp2f(red_m[k] - all);
+        const float f = __builtin_amdgcn_exp2f(red_m[k] - top);
         l += red_l[k] * f;
         o += *reinterpret_cast<const v4f*>(&red[k][4 * q]) * f;
     }
-    const int i = m / a.ratio, j = m - i * a.ratio;
-    store_out4(a.out + ((s.row0 + i) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + j) * a.kv.head_dim, 4 * q, a.kv.head_dim,
-               o * (l == 0.0f ? 0.0f : 1.0f / l));
+    store_joined(a, s, h, m, q, l, o);
+}
+
+// Of many rows, tiles of ROWS of them, KK a workgroup: d_pad / 4 lanes take a row's few ranges.
+template <int G, int ROWS>
+__global__ __launch_bounds__(256) void kv_join_many_kernel(AttnArgs a, int32_t nsplit) {
+    constexpr int DP = 32 * G, QL = DP / 4, KK = 256 / QL;
+    const uint32_t groups = ((uint32_t)a.rows_cap + KK - 1) / KK, unit = blockIdx.x / groups;
+    const int q = threadIdx.x % QL, m = (int)((blockIdx.x - unit * groups) * KK + threadIdx.x / QL);
+    const int64_t b = unit / (uint32_t)a.kv.n_heads;
+    const int h = (int)(unit - (uint32_t)b * (uint32_t)a.kv.n_heads);
+    const KvSeq s = kv_seq(a.kv, b);
+    const int64_t rows = (int64_t)s.done * a.ratio;
+    if (m >= rows || threadIdx.x / QL >= KK) return;
+    const int m0 = m / ROWS * ROWS, m1 = (int)(m0 + ROWS < rows ? m0 + ROWS : rows);
+    const Steps<64> st(a, s, m0, m1);
+    const int count = many_parts(st.n, nsplit);
+    if (count <= 1) return;
+    float top, l;
+    v4f o;
+    join_ranges<DP>(a, (int64_t)unit * nsplit * a.rows_cap + m, a.rows_cap, 0, count, 1, q, top, l, o);
+    store_joined(a, s, h, m, q, l, o);
 }
 
 // How a call runs: the kernel for few rows (16 mt of them at most) or the other one, and room for the
 // ranges that sequences are cut into, so that there are workgroups for every CU.
 struct Plan {
-    int mt;                 // 0: many rows
+    int mt, waves;          // mt 0: many rows, of a workgroup of so many wavefronts
     int64_t units, row_tiles, groups, slots;
     int32_t target, nsplit, rows_cap;
     size_t o_bytes, ml_bytes, range_bytes, bytes;
 };
 int64_t few_round(int g, int mt) {
     int64_t r = 0;
-    kv_groups(32 * g, [&](auto gc) {
+    (void)kv_groups(32 * g, [&](auto gc) {
         r = mt == 1 ? Few<gc(), 1>::ROUND : mt == 2 ? Few<gc(), 2>::ROUND : Few<gc(), 4>::ROUND;
         return hipSuccess;
     });
     return r;
 }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-constexpr int MANY_WAVES = 4;
-Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads) {
+// (a window leaves less to cut: never more ranges than without)
+Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, int64_t window) {
     Plan p = {};
-    const int64_t ratio = n_q_heads / c.n_heads, rows = b.max_rows * ratio, cap = b.max_pages * c.page_tokens;
+    const int64_t ratio = n_q_heads / c.n_heads, rows = b.max_rows * ratio, all = b.max_pages * c.page_tokens;
+    const int64_t cap = window && window + b.max_rows < all ? window + b.max_rows : all;
     p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= W4A4_KV_FEW_ROWS && c.d_pad <= 128 ? 4 : 0;
     p.units = b.n_seqs * c.n_heads;
     p.rows_cap = (int32_t)rows;
-    p.row_tiles = p.mt ? 1 : (rows + 32 * MANY_WAVES - 1) / (32 * MANY_WAVES);
+    // eight wavefronts share a tile's widening where that leaves every CU a workgroup
+    p.waves = c.d_pad <= 128 && p.units * ((rows + 255) / 256) >= 256 ? 8 : 4;
+    const int64_t tile = 32 * p.waves;
+    p.row_tiles = p.mt ? 1 : (rows + tile - 1) / tile;
     p.nsplit = 1;
     if (p.mt) {
         const int64_t most = p.units * ((cap / 32 + FEW_LEAST) / FEW_LEAST), round = few_round(c.d_pad / 32, p.mt);
@@ -793,9 +948,13 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads) 
             p.slots = most < 2 * target ? most : 2 * target;
         }
     } else {
-        int64_t n = 512 / (p.units * p.row_tiles > 0 ? p.units * p.row_tiles : 1);
-        if (n > cap / 256) n = cap / 256;
-        p.nsplit = (int32_t)(n < 1 ? 1 : n > 256 ? 256 : n);
+        // as many ranges as leave the last round of workgroups fullest
+        const int64_t groups = p.units * p.row_tiles, seen = window ? window + tile / ratio + 1 : all;
+        const int64_t most = (seen < all ? seen : all) / (64 * MANY_LEAST), round = p.waves == 4 && c.d_pad <= 128 ? 512 : 256;
+        int64_t best = 1;
+        for (int64_t n = 2; n <= most && n <= 64 && groups * n <= 2048; ++n)
+            if (((groups * n + round - 1) / round) * best * 20 < ((groups * best + round - 1) / round) * n * 19) best = n;      // worth the join: 5%
+        p.nsplit = (int32_t)best;
         p.groups = p.units * p.row_tiles * p.nsplit;
         p.slots = p.nsplit > 1 ? p.units * p.nsplit : 0;
     }
@@ -813,15 +972,22 @@ void run_few(const AttnArgs& a, const Plan& p, bool qb, hipStream_t st) {
     else hipLaunchKernelGGL((kv_few_kernel<G, MT, false>), grid, threads, 0, st, a);
 }
 
+template <int G, int WAVES>
+void run_many(const AttnArgs& a, const Plan& p, bool qb, hipStream_t st) {
+    const dim3 grid((uint32_t)p.groups), threads(64 * WAVES);
+    if (qb) hipLaunchKernelGGL((kv_many_kernel<G, WAVES, true>), grid, threads, 0, st, a, (uint32_t)p.row_tiles, p.nsplit);
+    else hipLaunchKernelGGL((kv_many_kernel<G, WAVES, false>), grid, threads, 0, st, a, (uint32_t)p.row_tiles, p.nsplit);
+}
+
 }  // namespace
 
 size_t kv_attention_ws(int64_t, const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads) {
-    return plan_of(b, c, n_q_heads).bytes;
+    return plan_of(b, c, n_q_heads, 0).bytes;
 }
 
 hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads,
                                float scale, bool causal, int64_t window, uint16_t* O, void* ws, hipStream_t stream) {
-    const Plan p = plan_of(b, c, n_q_heads);
+    const Plan p = plan_of(b, c, n_q_heads, window);
     AttnArgs a;
     a.kv = kv_args(n_rows, b, c);
     a.q = Q.data;
@@ -840,20 +1006,23 @@ hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4
     const bool qb = Q.dtype == W4A4_X_BF16;
     return kv_groups(c.d_pad, [&](auto gc) {
         constexpr int G = gc();
-        const dim3 join((uint32_t)(p.units * p.rows_cap));
         if (p.mt) {
             if (p.mt == 1) run_few<G, 1>(a, p, qb, stream);
             else if (p.mt == 2) run_few<G, 2>(a, p, qb, stream);
             else if constexpr (G <= 4) run_few<G, 4>(a, p, qb, stream);
         } else {
-            const dim3 grid((uint32_t)p.groups), threads(64 * MANY_WAVES);
-            if (qb) hipLaunchKernelGGL((kv_many_kernel<G, MANY_WAVES, true>), grid, threads, 0, stream, a, (uint32_t)p.row_tiles, p.nsplit);
-            else hipLaunchKernelGGL((kv_many_kernel<G, MANY_WAVES, false>), grid, threads, 0, stream, a, (uint32_t)p.row_tiles, p.nsplit);
+            if constexpr (G <= 4) {
+                if (p.waves == 8) run_many<G, 8>(a, p, qb, stream);
+            }
+            if (p.waves == 4) run_many<G, 4>(a, p, qb, stream);
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !p.slots) return e;
-        if (p.mt) hipLaunchKernelGGL((kv_join_kernel<G, 0>), join, dim3(256), 0, stream, a, 1);
-        else hipLaunchKernelGGL((kv_join_kernel<G, 32 * MANY_WAVES>), join, dim3(256), 0, stream, a, p.nsplit);
+        constexpr int KK = 256 / (8 * G);      // rows of a workgroup
+        const dim3 join((uint32_t)(p.mt ? p.units * p.rows_cap : p.units * ((p.rows_cap + KK - 1) / KK)));
+        if (p.mt) hipLaunchKernelGGL((kv_join_kernel<G>), join, dim3(256), 0, stream, a);
+        else if (p.waves == 4) hipLaunchKernelGGL((kv_join_many_kernel<G, 128>), join, dim3(256), 0, stream, a, p.nsplit);
+        else if constexpr (G <= 4) hipLaunchKernelGGL((kv_join_many_kernel<G, 256>), join, dim3(256), 0, stream, a, p.nsplit);
         return hipGetLastError();
     });
 }
