@@ -85,6 +85,30 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t p, int64_t co
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = p + i < cols ? bf16_to_f32(row[p + i]) : 0.0f;
 }
+// 8 neighbouring values of a row of any alignment, as they lie in memory; zero past its end.
+template <typename X> struct Row8;
+template <> struct Row8<float> {
+    float v[8];
+    __device__ void load(const float* row, int64_t p, int64_t cols) { load8(row, p, cols, v); }
+    __device__ float at(int i) const { return v[i]; }
+};
+template <> struct Row8<uint16_t> {
+    uint32_t w[4];
+    __device__ void load(const uint16_t* row, int64_t p, int64_t cols) {
+        typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+        if (p + 8 <= cols) {
+            const v4 v = *reinterpret_cast<const v4*>(row + p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = v[j];
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = (p + 2 * j < cols ? (uint32_t)row[p + 2 * j] : 0u) | (p + 2 * j + 1 < cols ? (uint32_t)row[p + 2 * j + 1] << 16 : 0u);
+    }
+    __device__ float at(int i) const { return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16); }
+};
+
 // Values that workgroups of different XCDs pass each other go past the XCDs' caches, value by value: a
 // release or acquire fence would write back or drop a whole L2 (and made these kernels up to 8
 // times slower).

@@ -20,30 +20,6 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
     return amax_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __builtin_fmaxf(__uint_as_float(amax_bits) / 127.0f, 0x1p-60f);
 }
 
-// 8 neighbouring values of a row of any alignment, as they lie in memory; zero past its end.
-template <typename X> struct Row8;
-template <> struct Row8<float> {
-    float v[8];
-    __device__ void load(const float* row, int64_t p, int64_t cols) { load8(row, p, cols, v); }
-    __device__ float at(int i) const { return v[i]; }
-};
-template <> struct Row8<uint16_t> {
-    uint32_t w[4];
-    __device__ void load(const uint16_t* row, int64_t p, int64_t cols) {
-        typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
-        if (p + 8 <= cols) {
-            const v4 v = *reinterpret_cast<const v4*>(row + p);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = v[j];
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = (p + 2 * j < cols ? (uint32_t)row[p + 2 * j] : 0u) | (p + 2 * j + 1 < cols ? (uint32_t)row[p + 2 * j + 1] << 16 : 0u);
-    }
-    __device__ float at(int i) const { return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16); }
-};
-
 // The 32 values of a lane in a block: chunk c holds inputs 32 c + 8 g .. + 7.
 template <typename X>
 __device__ __forceinline__ void load_block(Row8<X> (&v)[4], const X* row, int64_t p, int64_t cols) {

@@ -4,10 +4,10 @@
 //   e2m1(x / 2^(c - 127)), nearest, ties to even, saturating at 6
 //
 // Bound by memory (a prompt) or by the launch (a few rows).  A wavefront owns a block of 16 tokens
-// of one head, keys and values: lane 16 g + r loads channels 32 b + 8 g .. + 7 of token r by
-// 16-byte loads, and its eight nibbles are a dword of the key codes as they lie in memory.  The value
-// codes lie four tokens to a dword, since the attention multiplies with values along the tokens;
-// they are turned through LDS.  Blocks that the call covers in part are stored token by token.
+// of one head, keys and values, and goes through its rows in items of 8 channels, neighbouring lanes on
+// neighbouring items, so that rows are read and written in whole lines.  The block's bytes, which lie in the
+// attention's order (value codes four tokens to a dword), pass through LDS.  Blocks that the call covers in
+// part are stored item by item.
 #include "kv_device.h"
 
 namespace w4a4 {
@@ -37,39 +37,25 @@ template <typename X> struct KvIn {
     int64_t row, head;
 };
 
-// Codes and scale codes of this lane's channels; the scale codes, one a byte, in sc.
-template <typename X, int G>
-__device__ __forceinline__ void quantize(const X* row, bool live, int g, int D, uint32_t (&w)[G], uint32_t (&sc)[2]) {
-    float v[G][8];
-    sc[0] = sc[1] = 0;
-#pragma unroll
-    for (int b = 0; b < G; ++b) {
-        if (live) {
-            load8(row, 32 * b + 8 * g, D, v[b]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[b][j] = 0.0f;
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < G; ++b) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[b][j]));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-        const uint32_t c = e8m0_from_absbits(m);
-        w[b] = e2m1_word(v[b], c);
-        sc[b / 4] |= c << (8 * (b & 3));
-    }
+// The value of the lane two further on in its group of four, and the group's largest.
+__device__ __forceinline__ uint32_t quad_swap2(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false); }
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+    return max(v, quad_swap2(v));
+}
+template <typename T> __device__ __forceinline__ void put(uint8_t* p, T v) { __builtin_memcpy(__builtin_assume_aligned(p, sizeof(T)), &v, sizeof(T)); }
+template <typename T> __device__ __forceinline__ T get(const uint8_t* p) {
+    T v;
+    __builtin_memcpy(&v, __builtin_assume_aligned(p, sizeof(T)), sizeof(T));
+    return v;
 }
 
 // A workgroup's wavefronts take four heads of one (sequence, block) pair.
 template <typename X, int G>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs a, KvIn<X> K, KvIn<X> V, uint32_t blocks, uint32_t head_groups) {
     typedef KvBlock<G> L;
-    __shared__ __attribute__((aligned(16))) uint8_t turn[4][256 * G];
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
+    __shared__ __attribute__((aligned(16))) uint8_t images[4][L::BYTES];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t hg = blockIdx.x % head_groups, rest = blockIdx.x / head_groups;
     const uint32_t rr = rest % blocks;
     const int64_t b = rest / blocks;
@@ -79,67 +65,86 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs a, KvIn<X> K, KvI
     if (q * 16 >= end || h >= a.n_heads) return;      // wave-uniform; no barrier below
     uint8_t* const blk = kv_block(a, b, (uint32_t)q, h);
     if (!blk) return;
-    const int32_t pos = q * 16 + r;
-    const bool live = pos >= start && pos < end;
-    const int64_t row = s.row0 + (pos - s.first);
-    const uint32_t mask = (uint32_t)__ballot(live && g == 0);      // bit t: token t is written
+    const bool whole = q * 16 >= start && q * 16 + 16 <= end;
 
-    uint32_t kw[G], vw[G], ks[2], vs[2];
-    quantize<X, G>(K.p + (live ? row * K.row + h * K.head : 0), live, g, a.head_dim, kw, ks);
-    quantize<X, G>(V.p + (live ? row * V.row + h * V.head : 0), live, g, a.head_dim, vw, vs);
-
-    if (live) {
-        uint32_t* const kd = reinterpret_cast<uint32_t*>(blk) + lane * G;
+    // item i of this lane: token r, channels 32 d + 8 c .. + 7
+    Row8<X> x[2][G];
 #pragma unroll
-        for (int c = 0; c < G; ++c) kd[c] = kw[c];
-        if (g == 0) {
-            uint8_t* const sd = blk + L::KS + r * L::SG;
-            if constexpr (G == 1) sd[0] = (uint8_t)ks[0];
-            else if constexpr (G == 2) *reinterpret_cast<uint16_t*>(sd) = (uint16_t)ks[0];
-            else {
-                reinterpret_cast<uint32_t*>(sd)[0] = ks[0];
-                if constexpr (G > 4) reinterpret_cast<uint32_t*>(sd)[1] = ks[1];
-            }
-        }
-        uint8_t* const sv = blk + L::VS + (r >> 2) * 4 * L::SG + (r & 3);
-#pragma unroll
-        for (int c = 0; c < L::SG; ++c)
-            if ((c & 3) == g) sv[c * 4] = (uint8_t)(vs[c / 4] >> (8 * (c & 3)));
-    }
-    // Bytes of (d, d + 16): lanes g < 2 hold d = 8 g + j, lanes g + 2 the other half; each of the two
-    // makes four of the eight bytes.
-    uint8_t* const t = turn[wave];
-#pragma unroll
-    for (int c = 0; c < G; ++c) {
-        const uint32_t other = (uint32_t)__shfl_xor((int)vw[c], 32);
-        const uint32_t lo = g < 2 ? vw[c] : other, hi = g < 2 ? other : vw[c];
-        const int j0 = g < 2 ? 0 : 4;
-        const uint32_t bytes = spread4((lo >> (4 * j0)) & 0xFFFFu) | spread4((hi >> (4 * j0)) & 0xFFFFu) << 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) t[((r >> 2) * 16 + 8 * (g & 1) + j0 + j) * 4 * G + 4 * c + (r & 3)] = (uint8_t)(bytes >> (8 * j));
-    }
-    __builtin_amdgcn_wave_barrier();      // the wavefront's own LDS, in order
-    const uint32_t m4 = (mask >> (4 * g)) & 15u;      // this lane's dwords hold tokens 4 g .. + 3
-#pragma unroll
-    for (int c = 0; c < G; ++c) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(t + lane * 4 * G + 4 * c);
-        uint8_t* const d = blk + L::V + lane * 4 * G + 4 * c;
-        if (m4 == 15u) {
-            *reinterpret_cast<uint32_t*>(d) = v;
+    for (int i = 0; i < G; ++i) {
+        const int it = i * 64 + lane, r = it / (4 * G), ch = it % (4 * G);
+        const int32_t pos = q * 16 + r;
+        if (pos >= start && pos < end) {
+            const int64_t row = s.row0 + (pos - s.first);
+            x[0][i].load(K.p + row * K.row + h * K.head, 8 * ch, a.head_dim);
+            x[1][i].load(V.p + row * V.row + h * V.head, 8 * ch, a.head_dim);
         } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (m4 >> j & 1) d[j] = (uint8_t)(v >> (8 * j));
+            x[0][i].load(nullptr, 0, 0);      // zeros
+            x[1][i].load(nullptr, 0, 0);
         }
+    }
+    uint8_t* const img = images[wave];
+    if constexpr (L::SG > G) {      // scale bytes past the last group
+        if (lane < L::SG) put(img + L::KS + 16 * lane, make_uint4(0, 0, 0, 0));
+        if (lane < L::SG) put(img + L::VS + 16 * lane, make_uint4(0, 0, 0, 0));
+        __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const int it = i * 64 + lane, r = it / (4 * G), ch = it % (4 * G), c = ch & 3, d = ch >> 2;
+        uint32_t code[2], w[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            float v[8];
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = x[t][i].at(j);
+                m = max(m, abs_bits(v[j]));
+            }
+            code[t] = e8m0_from_absbits(quad_max(m));
+            w[t] = e2m1_word(v, code[t]);
+        }
+        // bytes of (channel, channel + 16): items c and c + 2 hold the halves; each makes four of the eight
+        const uint32_t other = quad_swap2(w[1]), lo = c < 2 ? w[1] : other, hi = c < 2 ? other : w[1];
+        const int j0 = c < 2 ? 0 : 4;
+        const uint32_t bytes = spread4((lo >> (4 * j0)) & 0xFFFFu) | spread4((hi >> (4 * j0)) & 0xFFFFu) << 4;
+        const int key_at = ((c * 16 + r) * G + d) * 4, val_at = L::V + ((r >> 2) * 16 + 8 * (c & 1) + j0) * 4 * G + 4 * d + (r & 3);
+        const int ks_at = L::KS + r * L::SG + d, vs_at = L::VS + (r >> 2) * 4 * L::SG + d * 4 + (r & 3);
+        const int32_t pos = q * 16 + r;
+        if (whole) {
+            put(img + key_at, w[0]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) img[val_at + j * 4 * G] = (uint8_t)(bytes >> (8 * j));
+            if (c == 0) img[ks_at] = (uint8_t)code[0];
+            if (c == 1) img[vs_at] = (uint8_t)code[1];
+        } else if (pos >= start && pos < end) {
+            put(blk + key_at, w[0]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) blk[val_at + j * 4 * G] = (uint8_t)(bytes >> (8 * j));
+            if (c == 0) blk[ks_at] = (uint8_t)code[0];
+            if (c == 1) blk[vs_at] = (uint8_t)code[1];
+            if constexpr (L::SG > G)      // the padding of this token's scales
+                if (c >= 2 && d == 0)
+                    for (int e = G; e < L::SG; ++e) blk[c == 2 ? ks_at + e : vs_at + 4 * e] = 0;
+        }
+    }
+    if (!whole) return;
+    __builtin_amdgcn_wave_barrier();      // the wavefront's own LDS, in order
+#pragma unroll
+    for (int i = 0; i < (L::BYTES + 1023) / 1024; ++i) {
+        const int at = i * 1024 + lane * 16;
+        if (at < L::BYTES) put(blk + at, get<uint4>(img + at));
     }
 }
 
-// 8 values of a row at channel p, rows of any alignment.
+// 8 values of a row at channel p, rows of any alignment.  Past the caches: a prompt's values do not stay in them,
+// and what they push out has to be written first (57600 x 40 x 128, append and read back: 570 to 537 us).
 __device__ __forceinline__ void store8(float* row, int p, int cols, const float* x) {
     typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
     if (p + 8 <= cols) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<v4*>(row + p + 4 * i) = v4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+        for (int i = 0; i < 2; ++i)
+            __builtin_nontemporal_store(v4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]}, reinterpret_cast<v4*>(row + p + 4 * i));
         return;
     }
 #pragma unroll
@@ -150,7 +155,7 @@ __device__ __forceinline__ void store8(uint16_t* row, int p, int cols, const flo
     typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
     const uint32_t w[4] = {pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])};
     if (p + 8 <= cols) {
-        *reinterpret_cast<v4*>(row + p) = v4{w[0], w[1], w[2], w[3]};
+        __builtin_nontemporal_store(v4{w[0], w[1], w[2], w[3]}, reinterpret_cast<v4*>(row + p));
         return;
     }
 #pragma unroll
@@ -172,8 +177,8 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t code, float* x) {
 template <typename Y, int G>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, Y* __restrict__ K, Y* __restrict__ V, uint32_t blocks, uint32_t head_groups) {
     typedef KvBlock<G> L;
-    __shared__ __attribute__((aligned(16))) uint8_t turn[4][256 * G];
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
+    __shared__ __attribute__((aligned(16))) uint8_t images[4][L::BYTES];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t hg = blockIdx.x % head_groups, rest = blockIdx.x / head_groups;
     const uint32_t rr = rest % blocks;
     const int64_t b = rest / blocks;
@@ -182,38 +187,29 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, Y* __restrict__ 
     const int32_t q0 = s.first >= 0 ? s.first / 16 : -((15 - s.first) / 16);
     const int32_t q = q0 + (int32_t)rr, h = (int32_t)hg * 4 + wave, end = s.first + s.done;
     if (q * 16 >= end || h >= a.n_heads) return;
-    const int32_t pos = q * 16 + r;
-    const bool live = pos >= s.first && pos < end;
     const uint8_t* const blk = q >= 0 ? kv_block(a, b, (uint32_t)q, h) : nullptr;
-    const int64_t at = ((s.row0 + (pos - s.first)) * a.n_heads + h) * a.head_dim;
-    uint32_t kw[G], ks[2] = {0, 0}, vs[2] = {0, 0}, vd[G];
+    uint8_t* const img = images[wave];
 #pragma unroll
-    for (int c = 0; c < G; ++c) kw[c] = vd[c] = 0;
-    if (blk) {
-#pragma unroll
-        for (int c = 0; c < G; ++c) {
-            kw[c] = reinterpret_cast<const uint32_t*>(blk)[lane * G + c];
-            vd[c] = reinterpret_cast<const uint32_t*>(blk + L::V)[lane * G + c];
-            ks[c / 4] |= (uint32_t)blk[L::KS + r * L::SG + c] << (8 * (c & 3));
-            vs[c / 4] |= (uint32_t)blk[L::VS + (r >> 2) * 4 * L::SG + c * 4 + (r & 3)] << (8 * (c & 3));
-        }
+    for (int i = 0; i < (L::BYTES + 1023) / 1024; ++i) {
+        const int at = i * 1024 + lane * 16;
+        if (at < L::BYTES) put(img + at, blk ? get<uint4>(blk + at) : make_uint4(0, 0, 0, 0));
     }
-    uint8_t* const t = turn[wave];
+    __builtin_amdgcn_wave_barrier();      // the wavefront's own LDS, in order
 #pragma unroll
-    for (int c = 0; c < G; ++c) *reinterpret_cast<uint32_t*>(t + lane * 4 * G + 4 * c) = vd[c];
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int c = 0; c < G; ++c) {
+    for (int i = 0; i < G; ++i) {
+        const int it = i * 64 + lane, r = it / (4 * G), ch = it % (4 * G), c = ch & 3, d = ch >> 2;
+        const int32_t pos = q * 16 + r;
+        if (pos < s.first || pos >= end || 8 * ch >= a.head_dim) continue;
         uint32_t w = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            w |= (((uint32_t)t[((r >> 2) * 16 + 8 * (g & 1) + j) * 4 * G + 4 * c + (r & 3)] >> (4 * (g >> 1))) & 15u) << (4 * j);
-        if (!live) continue;
+            w |= (((uint32_t)img[L::V + ((r >> 2) * 16 + 8 * (c & 1) + j) * 4 * G + 4 * d + (r & 3)] >> (4 * (c >> 1))) & 15u) << (4 * j);
+        const int64_t at = ((s.row0 + (pos - s.first)) * a.n_heads + h) * a.head_dim;
         float x[8];
-        values8(kw[c], ks[c / 4] >> (8 * (c & 3)) & 0xFFu, x);
-        store8(K + at, 32 * c + 8 * g, a.head_dim, x);
-        values8(w, vs[c / 4] >> (8 * (c & 3)) & 0xFFu, x);
-        store8(V + at, 32 * c + 8 * g, a.head_dim, x);
+        values8(get<uint32_t>(img + ((c * 16 + r) * G + d) * 4), img[L::KS + r * L::SG + d], x);
+        store8(K + at, 8 * ch, a.head_dim, x);
+        values8(w, img[L::VS + (r >> 2) * 4 * L::SG + d * 4 + (r & 3)], x);
+        store8(V + at, 8 * ch, a.head_dim, x);
     }
 }
 

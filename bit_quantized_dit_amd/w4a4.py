@@ -901,26 +901,50 @@ def w4a4_moe_forward(X: torch.Tensor, layer: MoeLayer, Y: torch.Tensor, ws: torc
 
 # --------------------------------------------------------------------------- INT8 layer
 
-def _here(t: torch.Tensor, name: str) -> None:
-    """The library launches on the current device."""
-    if t.device.index != torch.cuda.current_device():
+# The calls from here on check in few steps (a tenth of a microsecond each; a call of few rows takes the GPU about four).
+_X_CODES = {torch.float32: W4A4_X_F32, torch.bfloat16: W4A4_X_BF16}     # W4A4_Y_* are the same numbers
+
+
+def _here(t: torch.Tensor, name: str) -> int:
+    """t's device, which has to be the current one: the library launches there."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if i != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return i
+
+
+def _stream_on(stream, device: int):
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+def _matrix(t: torch.Tensor, cols: int, name: str) -> int:
+    """dtype code of a contiguous float32 or bfloat16 matrix of `cols` columns."""
+    dt = _X_CODES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{name} must be [T, {cols}], got {tuple(shape)}")
+    return dt
+
+
+def _buffer(ws: torch.Tensor, device: int) -> None:
+    if ws.dtype != torch.uint8:
+        raise TypeError(f"ws must be a uint8 buffer, got {ws.dtype}")
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on cuda:{device}, is on {ws.device}")
 
 
 class PackedInt8:
     """INT8 weights with a scale per output channel.  Keeps the device blob alive."""
 
     def __init__(self, blob: torch.Tensor, desc: W4A4Int8Packed):
-        self.blob, self.desc = blob, desc
-
-    @property
-    def d_in(self) -> int: return self.desc.d_in
-    @property
-    def d_out(self) -> int: return self.desc.d_out
-    @property
-    def k_pad(self) -> int: return self.desc.k_pad
-    @property
-    def n_pad(self) -> int: return self.desc.n_pad
+        self.blob, self.desc, self.ref = blob, desc, ctypes.byref(desc)
+        self.d_in, self.d_out, self.k_pad, self.n_pad = desc.d_in, desc.d_out, desc.k_pad, desc.n_pad
 
     def views(self) -> dict:
         """Copies of the packed arrays: codes int8 [d_out, d_in] (row-major) and scales float32 [d_out]."""
@@ -995,37 +1019,36 @@ def workspace_int8_views(ws: torch.Tensor, T: int, packed: PackedInt8) -> dict:
 
 
 def w4a4_int8_quantize_activations(X: torch.Tensor, packed: PackedInt8, ws: torch.Tensor, stream=None) -> None:
-    T = _acts(X, packed.d_in)
-    _here(X, "X")
-    _wsbuf(ws, X)
-    if T == 0:      # an empty tensor has no address
-        return
-    st = lib().w4a4_int8_quantize_activations(_ptr(X), _x_dtype(X), T, ctypes.byref(packed.desc), _ptr(ws), ws.numel(),
-                                              _stream(stream))
-    _check("w4a4_int8_quantize_activations", st)
+    i = _here(X, "X")
+    dt = _matrix(X, packed.d_in, "X")
+    _buffer(ws, i)
+    T = X.shape[0]
+    if T:      # (an empty tensor has no address)
+        st = lib().w4a4_int8_quantize_activations(X.data_ptr(), dt, T, packed.ref, ws.data_ptr(), ws.numel(), _stream_on(stream, i))
+        _check("w4a4_int8_quantize_activations", st)
 
 
 def w4a4_int8_gemm_prequantized(ws: torch.Tensor, T: int, packed: PackedInt8, Y: torch.Tensor, stream=None) -> None:
-    _dev(Y, "Y")
-    _here(Y, "Y")
-    dt = _y_dtype(Y, T, packed.d_out, Y)
-    _wsbuf(ws, Y)
-    if T == 0:
-        return
-    st = lib().w4a4_int8_gemm_prequantized(_ptr(ws), ws.numel(), T, ctypes.byref(packed.desc), _ptr(Y), dt, _stream(stream))
-    _check("w4a4_int8_gemm_prequantized", st)
+    i = _here(Y, "Y")
+    dt = _matrix(Y, packed.d_out, "Y")
+    _buffer(ws, i)
+    if Y.shape[0] != T:
+        raise ValueError(f"Y must be [{T}, {packed.d_out}], got {tuple(Y.shape)}")
+    if T:
+        st = lib().w4a4_int8_gemm_prequantized(ws.data_ptr(), ws.numel(), T, packed.ref, Y.data_ptr(), dt, _stream_on(stream, i))
+        _check("w4a4_int8_gemm_prequantized", st)
 
 
 def w4a4_int8_linear(X: torch.Tensor, packed: PackedInt8, Y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
-    T = _acts(X, packed.d_in)
-    _here(X, "X")
-    dt = _y_dtype(Y, T, packed.d_out, X)
-    _wsbuf(ws, X)
-    if T == 0:      # an empty tensor has no address
-        return
-    st = lib().w4a4_int8_linear(_ptr(X), _x_dtype(X), T, ctypes.byref(packed.desc), _ptr(Y), dt, _ptr(ws), ws.numel(),
-                                _stream(stream))
-    _check("w4a4_int8_linear", st)
+    i = _here(X, "X")
+    dx, dy = _matrix(X, packed.d_in, "X"), _matrix(Y, packed.d_out, "Y")
+    _buffer(ws, i)
+    T = X.shape[0]
+    if Y.shape[0] != T or Y.get_device() != i:
+        raise ValueError(f"Y must be [{T}, {packed.d_out}] on {X.device}, got {tuple(Y.shape)} on {Y.device}")
+    if T:
+        st = lib().w4a4_int8_linear(X.data_ptr(), dx, T, packed.ref, Y.data_ptr(), dy, ws.data_ptr(), ws.numel(), _stream_on(stream, i))
+        _check("w4a4_int8_linear", st)
 
 
 # --------------------------------------------------------------------------- 4-bit key/value cache
@@ -1034,16 +1057,8 @@ class KvCache:
     """A paged cache of MXFP4 keys and values: the device buffer (kept alive here) and its descriptor."""
 
     def __init__(self, data: torch.Tensor, desc: W4A4KvCache):
-        self.data, self.desc = data, desc
-
-    @property
-    def n_pages(self) -> int: return self.desc.n_pages
-    @property
-    def page_tokens(self) -> int: return self.desc.page_tokens
-    @property
-    def n_heads(self) -> int: return self.desc.n_heads
-    @property
-    def head_dim(self) -> int: return self.desc.head_dim
+        self.data, self.desc, self.ref, self.index = data, desc, ctypes.byref(desc), data.get_device()
+        self.n_pages, self.page_tokens, self.n_heads, self.head_dim = desc.n_pages, desc.page_tokens, desc.n_heads, desc.head_dim
 
 
 def w4a4_kv_cache_size(n_pages: int, page_tokens: int, n_heads: int, head_dim: int) -> int:
@@ -1066,10 +1081,7 @@ class KvBatch:
     """A call's sequences: descriptor, and the tensors it points to (kept alive here)."""
 
     def __init__(self, desc: W4A4KvBatch, keep: tuple):
-        self.desc, self.keep = desc, keep
-
-    @property
-    def device(self) -> torch.device: return self.keep[0].device
+        self.desc, self.keep, self.ref, self.index = desc, keep, ctypes.byref(desc), keep[0].get_device()
 
 
 def kv_batch(q_start: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor, max_rows: int) -> KvBatch:
@@ -1092,58 +1104,58 @@ def kv_batch(q_start: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor, max
     return KvBatch(desc, (q_start, lens, pages))
 
 
-def _kv_here(batch: KvBatch, cache: KvCache, t: torch.Tensor, name: str) -> None:
-    _here(t, name)
-    for other, what in ((batch.device, "the batch"), (cache.data.device, "the cache")):
-        if other != t.device:
-            raise ValueError(f"{name} is on {t.device}, {what} on {other}")
+def _kv_here(batch: KvBatch, cache: KvCache, t: torch.Tensor, name: str) -> int:
+    i = _here(t, name)
+    if batch.index != i or cache.index != i:
+        raise ValueError(f"{name} is on cuda:{i}, the batch on cuda:{batch.index}, the cache on cuda:{cache.index}")
+    return i
 
 
 def _kv_rows(X: torch.Tensor, n_heads: int, head_dim: int, name: str) -> W4A4KvRows:
     """X [rows, n_heads, head_dim], channels contiguous, rows and heads at any stride."""
-    if not X.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    dt = _x_dtype(X)
-    if X.dim() != 3 or tuple(X.shape[1:]) != (n_heads, head_dim):
-        raise ValueError(f"{name} must be [rows, {n_heads}, {head_dim}], got {tuple(X.shape)}")
-    if head_dim > 1 and X.stride(2) != 1:
+    dt = _X_CODES.get(X.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {X.dtype}")
+    shape = X.shape
+    if len(shape) != 3 or shape[1] != n_heads or shape[2] != head_dim:
+        raise ValueError(f"{name} must be [rows, {n_heads}, {head_dim}], got {tuple(shape)}")
+    row, head, channel = X.stride()
+    if channel != 1 and head_dim > 1:
         raise ValueError(f"{name}'s channels must be contiguous")
-    return W4A4KvRows(X.data_ptr(), X.stride(0), X.stride(1), dt, 0)
+    return W4A4KvRows(X.data_ptr(), row, head, dt, 0)
+
+
+def _kv_pair(K: torch.Tensor, V: torch.Tensor) -> None:
+    if K.shape[0] != V.shape[0] or K.dtype != V.dtype or K.get_device() != V.get_device():
+        raise ValueError("K and V must have as many rows, one dtype and one device")
 
 
 def w4a4_kv_append(K: torch.Tensor, V: torch.Tensor, batch: KvBatch, cache: KvCache, stream=None) -> None:
     k, v = _kv_rows(K, cache.n_heads, cache.head_dim, "K"), _kv_rows(V, cache.n_heads, cache.head_dim, "V")
-    if K.shape[0] != V.shape[0] or K.dtype != V.dtype or K.device != V.device:
-        raise ValueError("K and V must have as many rows, one dtype and one device")
-    _kv_here(batch, cache, K, "K")
-    if K.shape[0] == 0:      # an empty tensor has no address
-        return
-    _check("w4a4_kv_append", lib().w4a4_kv_append(ctypes.byref(k), ctypes.byref(v), K.shape[0], ctypes.byref(batch.desc),
-                                                  ctypes.byref(cache.desc), _stream(stream)))
+    _kv_pair(K, V)
+    i = _kv_here(batch, cache, K, "K")
+    n = K.shape[0]
+    if n:      # (an empty tensor has no address)
+        _check("w4a4_kv_append", lib().w4a4_kv_append(k, v, n, batch.ref, cache.ref, _stream_on(stream, i)))
 
 
 def w4a4_kv_read(batch: KvBatch, cache: KvCache, K: torch.Tensor, V: torch.Tensor, stream=None) -> None:
     """K, V: float32 or bfloat16 [rows, n_heads, head_dim], contiguous, written."""
-    for t, name in ((K, "K"), (V, "V")):
-        _dev(t, name)
-        if t.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-        if t.dim() != 3 or tuple(t.shape[1:]) != (cache.n_heads, cache.head_dim):
-            raise ValueError(f"{name} must be [rows, {cache.n_heads}, {cache.head_dim}], got {tuple(t.shape)}")
-    if K.shape[0] != V.shape[0] or K.dtype != V.dtype or K.device != V.device:
-        raise ValueError("K and V must have as many rows, one dtype and one device")
-    _kv_here(batch, cache, K, "K")
-    if K.shape[0] == 0:
-        return
-    dt = W4A4_Y_F32 if K.dtype == torch.float32 else W4A4_Y_BF16
-    _check("w4a4_kv_read", lib().w4a4_kv_read(K.shape[0], ctypes.byref(batch.desc), ctypes.byref(cache.desc), _ptr(K), _ptr(V), dt,
-                                              _stream(stream)))
+    k = _kv_rows(K, cache.n_heads, cache.head_dim, "K")
+    _kv_rows(V, cache.n_heads, cache.head_dim, "V")
+    _kv_pair(K, V)
+    if not (K.is_contiguous() and V.is_contiguous()):
+        raise ValueError("K and V must be contiguous")
+    i = _kv_here(batch, cache, K, "K")
+    n = K.shape[0]
+    if n:
+        _check("w4a4_kv_read", lib().w4a4_kv_read(n, batch.ref, cache.ref, K.data_ptr(), V.data_ptr(), k.dtype, _stream_on(stream, i)))
 
 
 def w4a4_kv_attention_workspace_size(n_rows: int, batch: KvBatch, n_q_heads: int, cache: KvCache) -> int:
     n = ctypes.c_size_t(0)
     _check("w4a4_kv_attention_workspace_size",
-           lib().w4a4_kv_attention_workspace_size(n_rows, ctypes.byref(batch.desc), ctypes.byref(cache.desc), n_q_heads, ctypes.byref(n)))
+           lib().w4a4_kv_attention_workspace_size(n_rows, batch.ref, cache.ref, n_q_heads, ctypes.byref(n)))
     return n.value
 
 
@@ -1157,18 +1169,16 @@ def w4a4_kv_attention(Q: torch.Tensor, batch: KvBatch, cache: KvCache, O: torch.
     scale None: 1 / sqrt(head_dim)."""
     if Q.dim() != 3:
         raise ValueError(f"Q must be [rows, n_q_heads, {cache.head_dim}], got {tuple(Q.shape)}")
-    n, heads, d = Q.shape
+    n, heads, _ = shape = Q.shape
     q = _kv_rows(Q, heads, cache.head_dim, "Q")
-    _dev(O, "O")
+    i = _kv_here(batch, cache, Q, "Q")
     if O.dtype != torch.bfloat16:
         raise TypeError(f"O must be bfloat16, got {O.dtype}")
-    if O.shape != Q.shape or O.device != Q.device:
-        raise ValueError(f"O must have Q's shape {tuple(Q.shape)} and device, got {tuple(O.shape)} on {O.device}")
-    _kv_here(batch, cache, Q, "Q")
-    _wsbuf(ws, Q)
-    if n == 0:
-        return
-    sc = cache.head_dim ** -0.5 if scale is None else float(scale)
-    _check("w4a4_kv_attention",
-           lib().w4a4_kv_attention(ctypes.byref(q), n, ctypes.byref(batch.desc), ctypes.byref(cache.desc), heads, sc, int(bool(causal)),
-                                   int(window), _ptr(O), _ptr(ws), ws.numel(), _stream(stream)))
+    if O.shape != shape or O.get_device() != i or not O.is_contiguous():
+        raise ValueError(f"O must be contiguous, of Q's shape {tuple(shape)} and on {Q.device}, got {tuple(O.shape)} on {O.device}")
+    _buffer(ws, i)
+    if n:
+        sc = cache.head_dim ** -0.5 if scale is None else float(scale)
+        _check("w4a4_kv_attention",
+               lib().w4a4_kv_attention(q, n, batch.ref, cache.ref, heads, sc, 1 if causal else 0, int(window), O.data_ptr(), ws.data_ptr(), ws.numel(),
+                                       _stream_on(stream, i)))
