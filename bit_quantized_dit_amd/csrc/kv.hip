@@ -137,46 +137,50 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvArgs a, KvIn<X> K, KvI
     }
 }
 
-// 8 values of a row at channel p, rows of any alignment.  Past the caches: a prompt's values do not stay in them,
-// and what they push out has to be written first (57600 x 40 x 128, append and read back: 570 to 537 us).
-__device__ __forceinline__ void store8(float* row, int p, int cols, const float* x) {
+// 16 bytes of a row at channel p, rows of any alignment.  Where rows are whole lines they go past the
+// caches: a prompt's values do not stay in them, and what they push out has to be written first (57600 x 40 x 128,
+// append and read back: 570 to 537 us); lines in parts are joined in the L2 (9000 x 6 x 72 in fp32: 46 us, past it 57).
+template <bool LINES> __device__ __forceinline__ void store16(float* row, int p, int cols, const float* x) {
     typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
-    if (p + 8 <= cols) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            __builtin_nontemporal_store(v4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]}, reinterpret_cast<v4*>(row + p + 4 * i));
+    const v4 v = {x[0], x[1], x[2], x[3]};
+    if (p + 4 <= cols) {
+        if constexpr (LINES) __builtin_nontemporal_store(v, reinterpret_cast<v4*>(row + p));
+        else *reinterpret_cast<v4*>(row + p) = v;
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
         if (p + i < cols) row[p + i] = x[i];
 }
-__device__ __forceinline__ void store8(uint16_t* row, int p, int cols, const float* x) {
+template <bool LINES> __device__ __forceinline__ void store16(uint16_t* row, int p, int cols, const float* x) {
     typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
-    const uint32_t w[4] = {pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])};
+    const v4 v = {pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])};
     if (p + 8 <= cols) {
-        __builtin_nontemporal_store(v4{w[0], w[1], w[2], w[3]}, reinterpret_cast<v4*>(row + p));
+        if constexpr (LINES) __builtin_nontemporal_store(v, reinterpret_cast<v4*>(row + p));
+        else *reinterpret_cast<v4*>(row + p) = v;
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (p + i < cols) row[p + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        if (p + i < cols) row[p + i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
 }
 
-// Eight nibbles times the scale of `code`: exact in binary32 and in bf16.
-__device__ __forceinline__ void values8(uint32_t w, uint32_t code, float* x) {
+// EL nibbles times the scale of `code`: exact in binary32 and in bf16.
+template <int EL> __device__ __forceinline__ void values(uint32_t w, uint32_t code, float* x) {
     typedef float v2f __attribute__((ext_vector_type(2)));
     const float s = __uint_as_float(code == 0xFFu ? 0x7FC00000u : max(code << 23, 0x00400000u));
     const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
     const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
     const float v[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = v[j] * s;
+    for (int j = 0; j < EL; ++j) x[j] = v[j] * s;
 }
 
-template <typename Y, int G>
+// An item is 16 bytes of output: EL channels.
+template <typename Y, int G, bool LINES>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, Y* __restrict__ K, Y* __restrict__ V, uint32_t blocks, uint32_t head_groups) {
     typedef KvBlock<G> L;
+    constexpr int EL = 16 / sizeof(Y), ITEMS = 32 * G / EL;
     __shared__ __attribute__((aligned(16))) uint8_t images[4][L::BYTES];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t hg = blockIdx.x % head_groups, rest = blockIdx.x / head_groups;
@@ -196,20 +200,20 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, Y* __restrict__ 
     }
     __builtin_amdgcn_wave_barrier();      // the wavefront's own LDS, in order
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-        const int it = i * 64 + lane, r = it / (4 * G), ch = it % (4 * G), c = ch & 3, d = ch >> 2;
+    for (int i = 0; i < ITEMS / 4; ++i) {
+        const int it = i * 64 + lane, r = it / ITEMS, p = it % ITEMS * EL, d = p >> 5, c = p >> 3 & 3;
         const int32_t pos = q * 16 + r;
-        if (pos < s.first || pos >= end || 8 * ch >= a.head_dim) continue;
+        if (pos < s.first || pos >= end || p >= a.head_dim) continue;
         uint32_t w = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w |= (((uint32_t)img[L::V + ((r >> 2) * 16 + 8 * (c & 1) + j) * 4 * G + 4 * d + (r & 3)] >> (4 * (c >> 1))) & 15u) << (4 * j);
+        for (int j = 0; j < EL; ++j)
+            w |= (((uint32_t)img[L::V + ((r >> 2) * 16 + (p & 15) + j) * 4 * G + 4 * d + (r & 3)] >> (4 * (c >> 1))) & 15u) << (4 * j);
         const int64_t at = ((s.row0 + (pos - s.first)) * a.n_heads + h) * a.head_dim;
         float x[8];
-        values8(get<uint32_t>(img + ((c * 16 + r) * G + d) * 4), img[L::KS + r * L::SG + d], x);
-        store8(K + at, 8 * ch, a.head_dim, x);
-        values8(w, img[L::VS + (r >> 2) * 4 * L::SG + d * 4 + (r & 3)], x);
-        store8(V + at, 8 * ch, a.head_dim, x);
+        values<EL>(get<uint32_t>(img + ((c * 16 + r) * G + d) * 4) >> (p & 4 ? 16 : 0), img[L::KS + r * L::SG + d], x);
+        store16<LINES>(K + at, p, a.head_dim, x);
+        values<EL>(w, img[L::VS + (r >> 2) * 4 * L::SG + d * 4 + (r & 3)], x);
+        store16<LINES>(V + at, p, a.head_dim, x);
     }
 }
 
@@ -234,7 +238,8 @@ hipError_t run_append(const w4a4_kv_rows& K, const w4a4_kv_rows& V, const KvArgs
 }
 template <typename Y, int G>
 hipError_t run_read(void* K, void* V, const KvArgs& a, const Grid& g, hipStream_t st) {
-    hipLaunchKernelGGL((kv_read_kernel<Y, G>), g.n, dim3(256), 0, st, a, (Y*)K, (Y*)V, g.blocks, g.head_groups);
+    if (a.head_dim * sizeof(Y) % 128 == 0) hipLaunchKernelGGL((kv_read_kernel<Y, G, true>), g.n, dim3(256), 0, st, a, (Y*)K, (Y*)V, g.blocks, g.head_groups);
+    else hipLaunchKernelGGL((kv_read_kernel<Y, G, false>), g.n, dim3(256), 0, st, a, (Y*)K, (Y*)V, g.blocks, g.head_groups);
     return hipGetLastError();
 }
 
