@@ -523,6 +523,7 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     // tokens that the row sees
     const int64_t pos = (int64_t)s.first + qi, from = a.causal && a.window ? pos - a.window + 1 : 0;
     const int32_t lo = from < 0 ? 0 : (int32_t)from, hi = !on ? -1 : a.causal ? (int32_t)pos : s.len - 1;
+    const uint32_t from_lo = (uint32_t)lo, span = hi < lo ? 0u : (uint32_t)(hi - lo) + 1u;
     // tokens that all of the wavefront's rows see (where some row is missing: none)
     const int64_t i0 = ((int)m0 + wave * 32) / a.ratio, i1 = ((int)m0 + wave * 32 + 31) / a.ratio;
     const int64_t all_hi = wave * 32 + 32 > rows ? -1 : a.causal ? s.first + i0 : s.len - 1;
@@ -706,12 +707,17 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
         const int64_t p0 = st.start + (int64_t)k * 64;
         const uint4 f = flags_of(slot);
         if (p0 + 63 <= all_hi && p0 >= all_lo && !((f.x | f.y | f.z | f.w) & 2)) return;
-        const uint32_t gone = (f.x >> 1 & 1) | (f.y & 2) | (f.z & 2) << 1 | (f.w & 2) << 2;
+        const uint32_t off = (uint32_t)((int32_t)p0 + 4 * h2) - from_lo;      // of the first score, from the row's first token on
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int32_t t = (int32_t)p0 + 8 * (i >> 2) + 4 * h2 + (i & 3);
-            if (t < lo || t > hi || (gone >> (i >> 3) & 1)) sc[i >> 4][i & 15] = -__builtin_inff();
-        }
+        for (int i = 0; i < 32; ++i)
+            if (off + 8 * (i >> 2) + (i & 3) >= span) sc[i >> 4][i & 15] = -__builtin_inff();
+        const uint32_t gone[4] = {f.x & 2, f.y & 2, f.z & 2, f.w & 2};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (gone[u]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sc[u >> 1][8 * (u & 1) + i] = -__builtin_inff();
+            }
     };
     auto widen_all = [&](int kslot, int slot) __attribute__((always_inline)) {
         prepare(slot);
