@@ -19,8 +19,12 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 
+// Whether the few-token kernel runs: up to 64 tokens, and layers whose tiles would leave most CUs idle (us a call,
+// tiles and this kernel: 333 x 4999 -> 1111 26.6 and 18.4, 256 x 5120 -> 3000 27.5 and 20.9, 1024 x 2048 -> 2048 27.4 and
+// 22.0; even at 256 x 5120 -> 5120, 26.3 and 27.1; 512 x 5120 -> 5120 31.3 and 45.5).  Short inputs: 300 x 800 -> 2000 13.6
+// and 8.7, 1000 x 512 -> 4096 18.5 and 18.8.
 bool int8_few(int64_t T, int64_t N, int64_t k_pad) {
-    return T <= 64 || (T <= 1024 && (T + 63) / 64 * ((N + 15) / 16) * (k_pad / 128) <= (k_pad < 1024 ? 8192 : 32768));
+    return T <= 64 || (T <= 1024 && (T + 63) / 64 * ((N + 15) / 16) * (k_pad / 128) <= (k_pad < 1024 ? 16000 : 45000));
 }
 
 // Linear tile id -> (token tile, feature tile): ids that share an XCD get a contiguous range of

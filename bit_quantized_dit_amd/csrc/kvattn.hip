@@ -948,7 +948,8 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
         // last ones end closer together (64 ragged sequences: 220 us, in one round 240)
         const int64_t target = p.units <= round / 4 ? round - p.units : 2 * round;
         p.groups = p.units;
-        if (cap > 32 * FEW_LEAST) {
+        // (many sequences fill the CUs by themselves, and looking a range up among them takes longer)
+        if (cap > 32 * FEW_LEAST && p.units < 4 * round && b.n_seqs <= 1024) {
             p.target = (int32_t)target;
             p.groups = most < target + p.units ? most : target + p.units;
             p.slots = most < 2 * target ? most : 2 * target;

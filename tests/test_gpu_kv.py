@@ -57,10 +57,10 @@ class Setup:
         B.w4a4_kv_append(self.dev(self.K), self.dev(self.V), self.batch(self.lens), self.cache)
         torch.cuda.synchronize()
 
-    def values(self, i):
+    def values(self, i, heads=slice(None)):
         """Cached keys and values of sequence i, float64."""
         a, e = self.start[i], self.start[i + 1]
-        return R.mxfp4(self.K[a:e])[2], R.mxfp4(self.V[a:e])[2]
+        return R.mxfp4(self.K[a:e, heads])[2], R.mxfp4(self.V[a:e, heads])[2]
 
 
 def _guarded(shape, dtype, fill=7.0):
@@ -183,8 +183,9 @@ def test_bad_positions_and_pages():
     assert np.array_equal(k[:9].double().cpu().numpy(), s.values(0)[0][8:17]) and bool((k[9:] == 7).all()) and bool((v[9:] == 7).all())
 
 
-def _check_attention(s, rows, Hq, qt=BF16, causal=True, window=0, scale=None, lens=None, pages=None, there=None, q=None, max_rows=None, poison=True):
-    """One call against the 64-bit form.  there(i, t): whether token t of sequence i has a page."""
+def _check_attention(s, rows, Hq, qt=BF16, causal=True, window=0, scale=None, lens=None, pages=None, there=None, q=None, max_rows=None, heads=None):
+    """One call against the 64-bit form.  there(i, t): whether token t of sequence i has a page; heads: the
+    key/value heads that are compared (all)."""
     lens = s.lens if lens is None else lens
     print(f"attention rows={rows} lens={lens} Hq={Hq} H={s.H} D={s.D} causal={causal} window={window} q={qt}", flush=True)
     rng = np.random.default_rng(5)
@@ -205,7 +206,8 @@ def _check_attention(s, rows, Hq, qt=BF16, causal=True, window=0, scale=None, le
     few = (max(rows) if max_rows is None else max_rows) * (Hq // s.H) <= (64 if s.D <= 128 else 32)
     at, err2, var, nr2 = 0, 0.0, 0.0, 0.0
     for i, r in enumerate(rows):
-        k, v = s.values(i)
+        some = list(range(s.H)) if heads is None else heads
+        k, v = s.values(i, some)
         k, v = k[:lens[i]], v[:lens[i]]
         pos = np.arange(lens[i] - r, lens[i])
         lo = np.maximum(pos - window + 1, 0) if causal and window else np.zeros(r, np.int64)
@@ -215,8 +217,9 @@ def _check_attention(s, rows, Hq, qt=BF16, causal=True, window=0, scale=None, le
             cum = np.concatenate([[0], np.cumsum(keep)])
             k, v = k[keep], v[keep]
             lo, hi = cum[np.clip(lo, 0, lens[i])], cum[np.clip(hi, 0, lens[i])]
-        for h in range(Hq):
-            o, tol, va = R.attention(qb[at:at + r, h], k[:, h // (Hq // s.H)], v[:, h // (Hq // s.H)], sc, lo, hi, few)
+        for h in [j * (Hq // s.H) + e for j in some for e in range(Hq // s.H)]:
+            kh = some.index(h // (Hq // s.H))
+            o, tol, va = R.attention(qb[at:at + r, h], k[:, kh], v[:, kh], sc, lo, hi, few)
             got = O[at:at + r, h].double().cpu()
             assert torch.equal(torch.isnan(got), torch.isnan(o)), f"sequence {i} head {h}: NaN pattern"
             ok = ~torch.isnan(o)
@@ -229,7 +232,7 @@ def _check_attention(s, rows, Hq, qt=BF16, causal=True, window=0, scale=None, le
             nr2 += float((o[ok] ** 2).sum())
         at += r
     # the sum of many independent roundings' squares: within a tenth where there are thousands
-    assert err2 <= 1.21 * var + 1e-30 or n * Hq * s.D < 4000, f"root mean square error {err2 ** 0.5:.3e}, bound {var ** 0.5:.3e}"
+    assert err2 <= 1.21 * var + 1e-30 or n * len(some) * (Hq // s.H) * s.D < 4000, f"root mean square error {err2 ** 0.5:.3e}, bound {var ** 0.5:.3e}"
     return O[:n].clone()
 
 
@@ -267,6 +270,33 @@ def test_attention_many_rows_widths(D):
 def test_attention_many_rows(rows, lens, Hq, H, causal, window):
     s = Setup(lens, H, 128, 16)
     _check_attention(s, rows, Hq, BF16, causal, window)
+
+
+@pytest.mark.parametrize("D", [31, 64, 72, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 70), (False, 0)])
+def test_attention_of_many_heads(D, causal, window):
+    """Enough heads that eight wavefronts share a tile: rows of one, part of one and several row tiles, pages that are
+    not there, NaN keys and values."""
+    def edit(s):
+        s.V[150, 3, 0], s.K[160, 5, 1], s.V[3, 257, D - 1] = np.nan, np.inf, -np.inf
+    s = Setup([333, 90], 260, D, 16, edit=edit)
+    heads = [0, 3, 5, 130, 257, 259]
+    _check_attention(s, [300, 90], 260, BF16, causal, window, heads=heads)
+    _check_attention(s, [70, 1], 520, F32, causal, window, heads=heads)
+    bad = s.pages.clone()
+    bad[0, 4], bad[0, 20], bad[1, 5] = -1, s.n_pages, 1 << 30
+    there = lambda i, t: not ((i == 0 and t // 16 in (4, 20)) or (i == 1 and t // 16 == 5))
+    _check_attention(s, [300, 90], 260, BF16, causal, window, pages=bad, there=there, heads=heads)
+
+
+@pytest.mark.parametrize("H,rows", [(300, 70), (3, 700)])
+def test_attention_of_many_rows_in_ranges(H, rows):
+    """Long sequences whose tokens are cut, for workgroups of eight and of four wavefronts."""
+    s = Setup([1300], H, 64, 64)
+    for causal in (True, False):
+        _check_attention(s, [rows], H, causal=causal, heads=[0, 1, H - 1])
+    s = Setup([5000, 900], 1, 64, 64)
+    _check_attention(s, [80, 70], 1)
 
 
 @pytest.mark.parametrize("rows", [[3, 2, 5], [90, 2, 70]])
@@ -343,6 +373,55 @@ def test_long_ranges_are_joined():
     _check_attention(s, [100, 80, 1], 2, pages=wide)
     b = _check_attention(s, [1, 1, 1], 4, pages=wide)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,H,Hq", [(65, 1, 1), (130, 2, 10), (300, 1, 4), (1100, 1, 2)])
+def test_many_sequences(n, H, Hq):
+    """More sequences than a wavefront has lanes, some without rows or tokens, a few long, in a table of long ones."""
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.choice([0, 1, 15, 40, 200], n)]
+    lens[3], lens[n - 2] = 1500, 2100
+    rows = [int(x) for x in rng.choice([0, 1, 1, 2], n)]
+    rows[3], rows[n - 2], rows[n - 1] = 1, 2, 1
+    s = Setup(lens, H, 32, 16)
+    wide = torch.full((n, 2000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :s.pages.shape[1]] = s.pages
+    _check_attention(s, rows, Hq, pages=wide)
+
+
+def test_cache_past_four_gigabytes():
+    """Blocks whose offsets need more than 32 bits, and those in front of them left alone."""
+    H, D, page = 8, 128, 64
+    page_bytes = H * page // 16 * 2176
+    n_pages = (5 << 30) // page_bytes
+    cache = B.kv_cache(n_pages, page, H, D)
+    assert cache.data.numel() > 1 << 32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    K, V = (torch.randn(200, H, D, device="cuda", generator=g).bfloat16() for _ in range(2))
+    pages = torch.tensor([[n_pages - 1, 0, n_pages - 3, n_pages // 2]], dtype=torch.int32, device="cuda")
+    used = sorted(pages[0].tolist())
+    for p in used:
+        cache.data[p * page_bytes:(p + 1) * page_bytes].fill_(255)
+    marks = [p * page_bytes - 16 for p in used if p] + [(p + 1) * page_bytes for p in used if p + 1 < n_pages]
+    for m in marks:
+        cache.data[m:m + 16] = 77
+    lens = torch.tensor([200], dtype=torch.int32, device="cuda")
+    b = B.kv_batch(torch.tensor([0, 200], dtype=torch.int32, device="cuda"), lens, pages, max_rows=200)
+    B.w4a4_kv_append(K, V, b, cache)
+    k, v = torch.empty_like(K), torch.empty_like(V)
+    B.w4a4_kv_read(b, cache, k, v)
+    for got, x in ((k, K), (v, V)):
+        assert np.array_equal(got.double().cpu().numpy(), R.mxfp4(x.float().cpu().numpy())[2])
+    assert all(bool((cache.data[m:m + 16] == 77).all()) for m in marks)
+    for n in (1, 80):
+        Q = torch.randn(n, H, D, device="cuda", generator=g).bfloat16()
+        O = torch.empty_like(Q)
+        bq = B.kv_batch(torch.tensor([0, n], dtype=torch.int32, device="cuda"), lens, pages, max_rows=n)
+        B.w4a4_kv_attention(Q, bq, cache, O, B.alloc_workspace_kv(n, bq, H, cache), causal=False)
+        kd, vd = k.double().cpu(), v.double().cpu()
+        for h in range(H):
+            o, tol, _ = R.attention(Q[:, h].double().cpu(), kd[:, h], vd[:, h], D ** -0.5, np.zeros(n, int), np.full(n, 200), n <= 64)
+            assert bool(((O[:, h].double().cpu() - o).abs() <= tol).all())
 
 
 def test_more_rows_than_max_rows():
