@@ -32,7 +32,8 @@ struct AttnArgs {
     int64_t q_row, q_head;
     uint16_t* out;
     float *part_o, *part_ml;      // [slot][rows_cap][d_pad], [slot][rows_cap][2]
-    int64_t* ranges;              // [n_seqs]: a sequence's first slot * 2^20 + its number of ranges
+    int64_t* joins;               // [n_seqs]: a sequence's first slot * 2^20 + its number of ranges
+    struct Range* ranges;         // by number, of many sequences
     int64_t window;
     float scale;                  // scale * log2(e)
     int32_t ratio, causal, target, rows_cap;
@@ -52,12 +53,14 @@ template <int ST> struct Steps {
 
 // Long sequences are cut into ranges of about the same number of steps, whatever sequence they
 // belong to, so that a ragged batch keeps all CUs busy to the end: with `target` workgroups in mind a
-// range has total / target steps, at least LEAST.  The lengths are the device's, so every
-// workgroup finds its range by itself: a wavefront sums the sequences' steps, 64 at a time,
-// and looks its number up among their ranges.  Ranges of sequences that have several leave their results in
-// slots, of which there are fewer than 2 target (a sequence of n steps > C has at most n / C + 1 < 2 n / C).
-struct Range {
-    int64_t b, slot;      // slot of the sequence's first range (heads lie side by side)
+// range has total / target steps, at least FEW_LEAST.  The lengths are the device's: up to 64 sequences every
+// wavefront sums their steps, one a lane, and looks its number up among their ranges; for more a small kernel does it
+// first, for all (500 sequences of 300 tokens, 8 heads: 92 us with every wavefront looking, 84 with one of
+// each workgroup).  Ranges of sequences that have several leave their results in slots, of which there are fewer
+// than 2 target (a sequence of n steps > C has at most n / C + 1 < 2 n / C).
+constexpr int FEW_LEAST = 16;      // steps of a range: 512 tokens
+struct alignas(16) Range {
+    int32_t b, slot;      // slot of the sequence's first range (heads lie side by side)
     int32_t k, count;     // which of how many ranges; count 0: there is nothing to do
 };
 __device__ __forceinline__ int32_t scan64(int32_t v) {      // inclusive, over the wavefront
@@ -69,55 +72,77 @@ __device__ __forceinline__ int32_t scan64(int32_t v) {      // inclusive, over t
     }
     return v;
 }
-template <int ST, int LEAST> struct Ranges {
-    int32_t chunk;
-    __device__ static int32_t steps(const AttnArgs& a, int64_t b, bool& live) {
-        live = false;
-        if (b >= a.kv.n_seqs) return 0;
-        const KvSeq s = kv_seq(a.kv, b);
-        live = s.done > 0;
-        return live ? Steps<ST>(a, s, 0, s.done * a.ratio).n : 0;
-    }
-    __device__ explicit Ranges(const AttnArgs& a) : chunk(0x7FFFFFFF) {
-        if (!a.target) return;
-        int64_t total = 0;
-        bool live;
-        for (int64_t b = threadIdx.x & 63; b < a.kv.n_seqs; b += 64) total += steps(a, b, live);
+// Steps of a sequence, -1 for one without rows (or past the last one); its ranges of `chunk` steps.
+__device__ __forceinline__ int32_t few_steps(const AttnArgs& a, int64_t b) {
+    if (b >= a.kv.n_seqs) return -1;
+    const KvSeq s = kv_seq(a.kv, b);
+    return s.done > 0 ? Steps<32>(a, s, 0, s.done * a.ratio).n : -1;
+}
+__device__ __forceinline__ int32_t chunk_of(const AttnArgs& a, int64_t total) {
+    const int64_t c = (total * a.kv.n_heads + a.target - 1) / a.target;
+    return (int32_t)(c < FEW_LEAST ? FEW_LEAST : c);
+}
+__device__ __forceinline__ int32_t count_of(int32_t n, int32_t chunk) { return n < 0 ? 0 : n > chunk ? (n + chunk - 1) / chunk : 1; }
+
+__device__ __forceinline__ Range find_range(const AttnArgs& a, uint32_t item) {
+    if (!a.target) return Range{(int32_t)item, 0, 0, item < a.kv.n_seqs ? 1 : 0};
+    if (a.kv.n_seqs > 64) return a.ranges[item];
+    const int lane = threadIdx.x & 63;
+    const int32_t n = few_steps(a, lane);
+    int64_t total = n > 0 ? n : 0;
 #pragma unroll
-        for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
-        const int64_t c = (total * a.kv.n_heads + a.target - 1) / a.target;
-        chunk = (int32_t)(c < LEAST ? LEAST : c);
+    for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
+    const int32_t c = count_of(n, chunk_of(a, total)), m = c > 1 ? c : 0, sc = scan64(c), sm = scan64(m);
+    const uint64_t hit = __ballot((int32_t)item < sc);
+    Range r = {0, 0, 0, 0};
+    if (hit) {
+        r.b = __builtin_ctzll(hit);
+        r.count = __shfl(c, r.b);
+        r.k = (int32_t)item - (__shfl(sc, r.b) - r.count);
+        r.slot = __shfl(sm, r.b) - (r.count > 1 ? r.count : 0);
     }
-    __device__ Range find(const AttnArgs& a, int64_t item) const {
-        Range r = {0, 0, 0, 0};
-        if (!a.target) {
-            r.b = item;
-            r.count = item < a.kv.n_seqs;
-            return r;
-        }
-        int64_t before = 0, slots = 0;
-        for (int64_t b0 = 0; b0 < a.kv.n_seqs; b0 += 64) {
-            bool live;
-            const int lane = threadIdx.x & 63;
-            const int32_t n = steps(a, b0 + lane, live);
-            const int32_t c = live ? (n > chunk ? (n + chunk - 1) / chunk : 1) : 0, m = c > 1 ? c : 0;
-            const int32_t sc = scan64(c), sm = scan64(m);
-            const uint64_t hit = __ballot(item < before + sc);
-            if (hit) {
-                const int w = __builtin_ctzll(hit);
-                const int32_t cw = __shfl(c, w);
-                r.b = b0 + w;
-                r.count = cw;
-                r.k = (int32_t)(item - (before + __shfl(sc, w) - cw));
-                r.slot = slots + __shfl(sm, w) - (cw > 1 ? cw : 0);
-                return r;
-            }
-            before += __shfl(sc, 63);
-            slots += __shfl(sm, 63);
-        }
-        return r;
+    return r;
+}
+
+// The same for many sequences: every item's range, and what the join reads.
+__global__ __launch_bounds__(1024) void kv_plan_kernel(AttnArgs a, int32_t items) {
+    __shared__ int64_t part[16];
+    __shared__ int32_t part_c[16], part_m[16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t total = 0;
+    for (int64_t b = threadIdx.x; b < a.kv.n_seqs; b += 1024) {
+        const int32_t n = few_steps(a, b);
+        total += n > 0 ? n : 0;
     }
-};
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
+    if (lane == 0) part[wave] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < 16; ++w) total += part[w];
+    const int32_t chunk = chunk_of(a, total);
+    int32_t before = 0, slots = 0;      // items and slots of the sequences before these 1024
+    for (int64_t b0 = 0; b0 < a.kv.n_seqs; b0 += 1024) {
+        const int64_t b = b0 + threadIdx.x;
+        const int32_t c = count_of(few_steps(a, b), chunk), m = c > 1 ? c : 0, sc = scan64(c), sm = scan64(m);
+        __syncthreads();
+        if (lane == 63) {
+            part_c[wave] = sc;
+            part_m[wave] = sm;
+        }
+        __syncthreads();
+        int32_t at = before + sc - c, slot = slots + sm - m;
+        for (int w = 0; w < 16; ++w) {
+            at += w < wave ? part_c[w] : 0;
+            slot += w < wave ? part_m[w] : 0;
+            before += part_c[w];
+            slots += part_m[w];
+        }
+        for (int k = 0; k < c && at + k < items; ++k) a.ranges[at + k] = Range{(int32_t)b, slot, k, c};
+        if (b < a.kv.n_seqs) a.joins[b] = (int64_t)slot << 20 | c;
+    }
+    for (int i = before + threadIdx.x; i < items; i += 1024) a.ranges[i] = Range{0, 0, 0, 0};
+}
 
 template <int N> __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
     __builtin_memcpy(w, __builtin_assume_aligned(p, N % 4 == 0 ? 16 : N % 2 == 0 ? 8 : 4), 4 * N);
@@ -192,7 +217,6 @@ __device__ __forceinline__ void store_out4(uint16_t* row, int d, int D, v4f v) {
 // need no registers, so that many steps are in flight beside the accumulators; the copies past the
 // last step run with empty ranges, so that every wait counts the same number.  The wavefronts'
 // results meet in LDS.
-constexpr int FEW_LEAST = 16;      // steps of a range: 512 tokens
 template <int G, int MT> struct Few {      // wavefronts of a workgroup, steps of a ring, wavefronts a SIMD (for the register budget)
     static constexpr int NW = 4, R = 2, OCC = G * MT <= 4 ? 4 : G * MT <= 8 ? 2 : 1;
     static constexpr int COPIES = (KvBlock<G>::BYTES + 1023) / 1024, STEP = 2 * KvBlock<G>::BYTES, LD = 32 * G + 4;
@@ -211,17 +235,16 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t item = blockIdx.x / (uint32_t)a.kv.n_heads;
     const int h = (int)(blockIdx.x - item * (uint32_t)a.kv.n_heads);
-    const Ranges<32, FEW_LEAST> ranges(a);
-    Range rg = ranges.find(a, item);
+    Range rg = find_range(a, item);
     rg.k = __builtin_amdgcn_readfirstlane(rg.k);
     rg.count = __builtin_amdgcn_readfirstlane(rg.count);
     if (rg.count == 0) return;
-    const int64_t b = __builtin_amdgcn_readfirstlane((int)rg.b);
+    const int64_t b = __builtin_amdgcn_readfirstlane(rg.b);
     const KvSeq s = kv_seq(a.kv, b);
     const int rows = s.done * a.ratio;
     const Steps<32> st(a, s, 0, rows);
     if (rows == 0) return;
-    if (a.target && rg.k == 0 && h == 0 && threadIdx.x == 0) a.ranges[b] = rg.slot << 20 | rg.count;      // for the join
+    if (a.target && rg.k == 0 && h == 0 && threadIdx.x == 0) a.joins[b] = (int64_t)rg.slot << 20 | rg.count;
     // equal parts of the sequence's steps; this wavefront's are s0 + wave, + NW, ..
     const int s0 = (int)((int64_t)st.n * rg.k / rg.count), s1 = (int)((int64_t)st.n * (rg.k + 1) / rg.count);
     const int mine = s1 - s0 > wave ? (s1 - s0 - wave + NW - 1) / NW : 0;
@@ -453,7 +476,7 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
                 const float r = l == 0.0f ? 0.0f : 1.0f / l;
                 store_out4(a.out + ((s.row0 + i) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + j) * a.kv.head_dim, d, a.kv.head_dim, o * r);
             } else {
-                const int64_t at = ((rg.slot + rg.k) * a.kv.n_heads + h) * a.rows_cap + row;
+                const int64_t at = ((int64_t)(rg.slot + rg.k) * a.kv.n_heads + h) * a.rows_cap + row;
                 *reinterpret_cast<v4f*>(a.part_o + at * DP + d) = o;
                 if (d == 0) {
                     a.part_ml[2 * at] = top;
@@ -850,44 +873,47 @@ __device__ __forceinline__ void store_joined(const AttnArgs& a, const KvSeq& s, 
                o * (l == 0.0f ? 0.0f : 1.0f / l));
 }
 
-// Of few rows, one a workgroup: d_pad / 4 lanes take four channels each and every KK-th range.
+// Of few rows, a sequence and head a workgroup: d_pad / 4 lanes take four channels each of every GR-th
+// range of a row, GR groups of them a row.
 template <int G>
-__global__ __launch_bounds__(256) void kv_join_kernel(AttnArgs a) {
-    constexpr int DP = 32 * G, QL = DP / 4, KK = 256 / QL;
-    __shared__ __attribute__((aligned(16))) float red[KK][DP];
-    __shared__ float red_m[KK], red_l[KK];
-    const uint32_t unit = blockIdx.x / (uint32_t)a.rows_cap;
-    const int m = (int)(blockIdx.x - unit * (uint32_t)a.rows_cap);
-    const int64_t b = unit / (uint32_t)a.kv.n_heads;
-    const int h = (int)(unit - (uint32_t)b * (uint32_t)a.kv.n_heads);
+__global__ __launch_bounds__(512) void kv_join_kernel(AttnArgs a) {
+    constexpr int DP = 32 * G, QL = DP / 4, NG = 512 / QL;
+    __shared__ __attribute__((aligned(16))) float red[NG][DP];
+    __shared__ float red_m[NG], red_l[NG];
+    const int64_t b = blockIdx.x / (uint32_t)a.kv.n_heads;
+    const int h = (int)(blockIdx.x - (uint32_t)b * (uint32_t)a.kv.n_heads);
+    const int64_t r = a.joins[b];      // (undefined where the sequence has no rows)
     const KvSeq s = kv_seq(a.kv, b);
-    if (m >= s.done * a.ratio) return;
-    const int64_t r = a.ranges[b];
-    const int count = (int)(r & 0xFFFFF);
-    if (count <= 1) return;
-    const int q = threadIdx.x % QL, kk = threadIdx.x / QL;
-    float top, l;
-    v4f o;
-    if (kk < KK) {      // (192 channels: 48 lanes a range, 16 lanes left over)
-        join_ranges<DP>(a, ((r >> 20) * a.kv.n_heads + h) * a.rows_cap + m, (int64_t)a.kv.n_heads * a.rows_cap, kk, count, KK, q, top, l, o);
-        *reinterpret_cast<v4f*>(&red[kk][4 * q]) = o;
-        if (q == 0) {
-            red_m[kk] = top;
-            red_l[kk] = l;
+    const int rows = s.done * a.ratio, count = (int)(r & 0xFFFFF);
+    if (rows == 0 || count <= 1) return;
+    const int GR = rows >= NG ? 1 : NG / rows, pass = NG / GR;      // groups of a row, rows at a time
+    const int q = threadIdx.x % QL, group = threadIdx.x / QL, sub = group % GR;
+    for (int m0 = 0; m0 < rows; m0 += pass) {
+        const int m = m0 + group / GR;
+        const bool on = group < pass * GR && m < rows;
+        float top = M_NONE, l = 0.0f;
+        v4f o = v4f{0, 0, 0, 0};
+        if (on) join_ranges<DP>(a, ((r >> 20) * a.kv.n_heads + h) * a.rows_cap + m, (int64_t)a.kv.n_heads * a.rows_cap, sub, count, GR, q, top, l, o);
+        if (GR > 1) {      // uniform
+            __syncthreads();
+            if (on) {
+                *reinterpret_cast<v4f*>(&red[group][4 * q]) = o;
+                if (q == 0) {
+                    red_m[group] = top;
+                    red_l[group] = l;
+                }
+            }
+            __syncthreads();
+            if (!on || sub) continue;
+            for (int k = 1; k < GR; ++k) {
+                const float m1 = red_m[group + k], t = __builtin_fmaxf(top, m1), f0 = __builtin_amdgcn_exp2f(top - t), f1 = __builtin_amdgcn_exp2f(m1 - t);
+                l = l * f0 + red_l[group + k] * f1;
+                o = o * f0 + *reinterpret_cast<const v4f*>(&red[group + k][4 * q]) * f1;
+                top = t;
+            }
         }
+        if (on) store_joined(a, s, h, m, q, l, o);
     }
-    __syncthreads();
-    if (kk != 0) return;
-    top = M_NONE;
-    for (int k = 0; k < KK; ++k) top = __builtin_fmaxf(top, red_m[k]);
-    l = 0.0f;
-    o = v4f{0, 0, 0, 0};
-    for (int k = 0; k < KK; ++k) {
-        const float f = __builtin_amdgcn_exp2f(red_m[k] - top);
-        l += red_l[k] * f;
-        o += *reinterpret_cast<const v4f*>(&red[k][4 * q]) * f;
-    }
-    store_joined(a, s, h, m, q, l, o);
 }
 
 // Of many rows, tiles of ROWS of them, KK a workgroup: d_pad / 4 lanes take a row's few ranges.
@@ -917,7 +943,7 @@ struct Plan {
     int mt, waves;          // mt 0: many rows, of a workgroup of so many wavefronts
     int64_t units, row_tiles, groups, slots;
     int32_t target, nsplit, rows_cap;
-    size_t o_bytes, ml_bytes, range_bytes, bytes;
+    size_t o_bytes, ml_bytes, join_bytes, bytes;
 };
 int64_t few_round(int g, int mt) {
     int64_t r = 0;
@@ -944,12 +970,12 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
     if (p.mt) {
         const int64_t most = p.units * ((cap / 32 + FEW_LEAST) / FEW_LEAST), round = few_round(c.d_pad / 32, p.mt);
         // One round of workgroups where few sequences leave most of it to full ranges (one row over 57600
-        // tokens, 40 heads: 59 us, in two rounds 62); else two, whose ranges are shorter, so that the
-        // last ones end closer together (64 ragged sequences: 220 us, in one round 240)
-        const int64_t target = p.units <= round / 4 ? round - p.units : 2 * round;
+        // tokens, 40 heads: 59 us, in two rounds 62); else about two, whose ranges are shorter, so that the
+        // last ones end closer together (64 ragged sequences: 220 us, in one round 240).  Sequences that fill the CUs by
+        // themselves stay whole.
+        const int64_t target = p.units <= round / 4 ? round - p.units : p.units < round ? 2 * round - p.units : round;
         p.groups = p.units;
-        // (many sequences fill the CUs by themselves, and looking a range up among them takes longer)
-        if (cap > 32 * FEW_LEAST && p.units < 4 * round && b.n_seqs <= 1024) {
+        if (cap > 32 * FEW_LEAST && p.units < 4 * round) {
             p.target = (int32_t)target;
             p.groups = most < target + p.units ? most : target + p.units;
             p.slots = most < 2 * target ? most : 2 * target;
@@ -967,8 +993,8 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
     }
     p.o_bytes = up256((size_t)(p.slots * rows) * c.d_pad * 4);
     p.ml_bytes = up256((size_t)(p.slots * rows) * 8);
-    p.range_bytes = p.target ? up256((size_t)b.n_seqs * 8) : 0;
-    p.bytes = p.o_bytes + p.ml_bytes + p.range_bytes;
+    p.join_bytes = p.target ? up256((size_t)b.n_seqs * 8) : 0;
+    p.bytes = p.o_bytes + p.ml_bytes + p.join_bytes + (p.target && b.n_seqs > 64 ? up256((size_t)((p.groups + c.n_heads - 1) / c.n_heads) * sizeof(Range)) : 0);
     return p;
 }
 
@@ -1003,7 +1029,8 @@ hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4
     a.out = O;
     a.part_o = (float*)ws;
     a.part_ml = (float*)((uint8_t*)ws + p.o_bytes);
-    a.ranges = (int64_t*)((uint8_t*)ws + p.o_bytes + p.ml_bytes);
+    a.joins = (int64_t*)((uint8_t*)ws + p.o_bytes + p.ml_bytes);
+    a.ranges = (Range*)((uint8_t*)ws + p.o_bytes + p.ml_bytes + p.join_bytes);
     a.window = window;
     a.scale = scale * 1.44269504088896340736f;
     a.ratio = n_q_heads / c.n_heads;
@@ -1013,6 +1040,8 @@ hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4
     const bool qb = Q.dtype == W4A4_X_BF16;
     return kv_groups(c.d_pad, [&](auto gc) {
         constexpr int G = gc();
+        if (p.target && b.n_seqs > 64)
+            hipLaunchKernelGGL(kv_plan_kernel, dim3(1), dim3(1024), 0, stream, a, (int32_t)((p.groups + c.n_heads - 1) / c.n_heads));
         if (p.mt) {
             if (p.mt == 1) run_few<G, 1>(a, p, qb, stream);
             else if (p.mt == 2) run_few<G, 2>(a, p, qb, stream);
@@ -1026,8 +1055,8 @@ hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !p.slots) return e;
         constexpr int KK = 256 / (8 * G);      // rows of a workgroup
-        const dim3 join((uint32_t)(p.mt ? p.units * p.rows_cap : p.units * ((p.rows_cap + KK - 1) / KK)));
-        if (p.mt) hipLaunchKernelGGL((kv_join_kernel<G>), join, dim3(256), 0, stream, a);
+        const dim3 join((uint32_t)(p.mt ? p.units : p.units * ((p.rows_cap + KK - 1) / KK)));
+        if (p.mt) hipLaunchKernelGGL((kv_join_kernel<G>), join, dim3(512), 0, stream, a);
         else if (p.waves == 4) hipLaunchKernelGGL((kv_join_many_kernel<G, 128>), join, dim3(256), 0, stream, a, p.nsplit);
         else if constexpr (G <= 4) hipLaunchKernelGGL((kv_join_many_kernel<G, 256>), join, dim3(256), 0, stream, a, p.nsplit);
         return hipGetLastError();
