@@ -196,7 +196,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, Y* __restrict__ 
 #pragma unroll
     for (int i = 0; i < (L::BYTES + 1023) / 1024; ++i) {
         const int at = i * 1024 + lane * 16;
-        if (at < L::BYTES) put(img + at, blk ? get<uint4>(blk + at) : make_uint4(0, 0, 0, 0));
+        if (at < L::BYTES) put(img + at, blk ? __builtin_nontemporal_load(reinterpret_cast<const v4i*>(blk + at)) : v4i{0, 0, 0, 0});
     }
     __builtin_amdgcn_wave_barrier();      // the wavefront's own LDS, in order
 #pragma unroll

@@ -304,7 +304,7 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
 #pragma unroll
             for (int i = 0; i < F::COPIES; ++i) {
                 const int off = i * 1024 + lane * 16;
-                if (off < L::BYTES) dma16(srd, ring + slot * F::STEP + u * L::BYTES + i * 1024, off, 0);
+                if (off < L::BYTES) dma16_once(srd, ring + slot * F::STEP + u * L::BYTES + i * 1024, off, 0);
             }
         }
     };

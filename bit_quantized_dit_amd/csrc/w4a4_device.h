@@ -70,6 +70,14 @@ __device__ __forceinline__ void dma16(v4i srd, uint32_t lds, int voff, int soff)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(lds), "v"(voff), "s"(srd), "s"(soff));
 }
+// The same for data that is read once: marked non-temporal.
+__device__ __forceinline__ void dma16_once(v4i srd, uint32_t lds, int voff, int soff) {
+    srd = uniform(srd);
+    lds = __builtin_amdgcn_readfirstlane(lds);
+    soff = __builtin_amdgcn_readfirstlane(soff);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                 :: "s"(lds), "v"(voff), "s"(srd), "s"(soff));
+}
 __device__ __forceinline__ void dma4(v4i srd, uint32_t lds, int voff, int soff) {
     srd = uniform(srd);
     lds = __builtin_amdgcn_readfirstlane(lds);
