@@ -140,6 +140,7 @@ int w4a4_kv_attention(const w4a4_kv_rows* Q, int64_t n_rows, const w4a4_kv_batch
     if (misaligned(O) || misaligned(ws)) return W4A4_ERR_ALIGN;
     if (ws_bytes < kv_attention_ws(n_rows, *batch, *cache, n_q_heads)) return W4A4_ERR_SHAPE;
     if (nothing(n_rows, batch)) return W4A4_OK;
+    if (window > kMaxTokens) window = 0;      // no sequence is longer
     return dev_status(launch_kv_attention(*Q, n_rows, *batch, *cache, n_q_heads, scale, causal != 0, window, O, ws, (hipStream_t)stream));
 }
 

@@ -968,7 +968,8 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
     p.row_tiles = p.mt ? 1 : (rows + tile - 1) / tile;
     p.nsplit = 1;
     if (p.mt) {
-        const int64_t most = p.units * ((cap / 32 + FEW_LEAST) / FEW_LEAST), round = few_round(c.d_pad / 32, p.mt);
+        // (tokens that start and end inside a step: two steps more)
+        const int64_t most = p.units * ((cap / 32 + 2 + FEW_LEAST - 1) / FEW_LEAST), round = few_round(c.d_pad / 32, p.mt);
         // One round of workgroups where few sequences leave most of it to full ranges (one row over 57600
         // tokens, 40 heads: 59 us, in two rounds 62); else about two, whose ranges are shorter, so that the
         // last ones end closer together (64 ragged sequences: 220 us, in one round 240).  Sequences that fill the CUs by

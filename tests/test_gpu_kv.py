@@ -375,6 +375,15 @@ def test_long_ranges_are_joined():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("window", [500, 530, 1000, 1023, 1025, 2500, 1 << 40])
+def test_windows_that_are_cut(window):
+    """Windows of several ranges that start and end inside a step."""
+    s = Setup([3001, 1040, 700], 2, 32, 16)
+    for rows in ([1, 1, 1], [7, 2, 3], [9, 16, 1]):
+        _check_attention(s, rows, 2, window=window)
+    _check_attention(s, [100, 70, 1], 2, window=window)
+
+
 @pytest.mark.parametrize("n,H,Hq", [(65, 1, 1), (130, 2, 10), (300, 1, 4), (1100, 1, 2)])
 def test_many_sequences(n, H, Hq):
     """More sequences than a wavefront has lanes, some without rows or tokens, a few long, in a table of long ones."""
