@@ -9,7 +9,8 @@ using namespace w4a4;
 
 namespace {
 
-constexpr int64_t kMaxT = (int64_t)1 << 26;
+// 16 tokens a workgroup of up to 1024 work items, which a launch counts in 32 bits
+constexpr int64_t kMaxT = ((int64_t)1 << 26) - 16;
 // 256 x 256 tiles of outputs: a launch counts its work items, 512 a tile, in 32 bits
 constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 4096;
 

@@ -135,7 +135,7 @@ int w4a4_kv_attention(const w4a4_kv_rows* Q, int64_t n_rows, const w4a4_kv_batch
     if (!st) st = check_heads(batch, cache, n_q_heads);
     if (!st) st = check_rows(Q);
     if (st) return st;
-    if (!O || !ws || !(scale > 0.0f) || !std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window && !causal))
+    if (!O || !ws || !(scale > 0.0f) || !std::isfinite(scale * 1.44269504088896340736f) || (causal != 0 && causal != 1) || window < 0 || (window && !causal))
         return W4A4_ERR_INVALID;
     if (misaligned(O) || misaligned(ws)) return W4A4_ERR_ALIGN;
     if (ws_bytes < kv_attention_ws(n_rows, *batch, *cache, n_q_heads)) return W4A4_ERR_SHAPE;

@@ -55,8 +55,7 @@ template <int ST> struct Steps {
 // belong to, so that a ragged batch keeps all CUs busy to the end: with `target` workgroups in mind a
 // range has total / target steps, at least FEW_LEAST.  The lengths are the device's: up to 64 sequences every
 // wavefront sums their steps, one a lane, and looks its number up among their ranges; for more a small kernel does it
-// first, for all (500 sequences of 300 tokens, 8 heads: 92 us with every wavefront looking, 84 with one of
-// each workgroup).  Ranges of sequences that have several leave their results in slots, of which there are fewer
+// first, for all (500 sequences of 300 tokens in a long table, 8 heads: 53 us, with every wavefront looking 112).  Ranges of sequences that have several leave their results in slots, of which there are fewer
 // than 2 target (a sequence of n steps > C has at most n / C + 1 < 2 n / C).
 constexpr int FEW_LEAST = 16;      // steps of a range: 512 tokens
 struct alignas(16) Range {
@@ -212,10 +211,15 @@ __device__ __forceinline__ void store_out4(uint16_t* row, int d, int D, v4f v) {
 
 // ---------------------------------------------------------------- few rows
 //
-// Up to 16 MT stacked rows: bound by reading the cache.  A wavefront takes every NW-th step of
+// Up to 16 MT stacked rows: bound by reading the cache (64 ragged sequences of 8 heads and 1.16 GB: 205 us, 5.6 TB/s;
+// one row of 40 heads over 57600 tokens, 313 MB: 57 us, 5.5 TB/s; a kernel that only reads reaches 6.1), or, for a
+// few hundred tokens, by the latency of its dependent loads (9 us).  The tiles are those of the 16-row instruction,
+// as a sequence's one row and its ratio of heads seldom fill more.  The matrix unit has time to spare, so weights are
+// multiplied as two bf16 terms (16 bits) and their rounding does not show.  A wavefront takes every NW-th step of
 // 32 tokens of its workgroup's range.  Its two blocks go into a ring of R steps in LDS by copies that
-// need no registers, so that many steps are in flight beside the accumulators; the copies past the
-// last step run with empty ranges, so that every wait counts the same number.  The wavefronts'
+// need no registers, so that many steps are in flight beside the accumulators, and go past the caches, as no one
+// reads them twice (through them: 227 and 64 us); rings of 4 steps, of which fewer wavefronts fit, are slower, and so
+// are workgroups of 8 wavefronts.  The copies past the last step run with empty ranges, so that every wait counts the same number.  The wavefronts'
 // results meet in LDS.
 template <int G, int MT> struct Few {      // wavefronts of a workgroup, steps of a ring, wavefronts a SIMD (for the register budget)
     static constexpr int NW = 4, R = 2, OCC = G * MT <= 4 ? 4 : G * MT <= 8 ? 2 : 1;
@@ -489,6 +493,11 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
 }
 
 // ---------------------------------------------------------------- many rows
+//
+// Bound by the matrix unit, the vector unit's softmax and widening beside it, and the board's power: 4096 rows of 40
+// heads over 57600 tokens 4278 us, 1.13 PFLOP/s at 2.07 GHz, matrix unit 51% of the cycles (a large bf16 product
+// of the library: 1.24; without the widening 3860, without the exponentials 4040, without either 3290).  So weights are one
+// bf16 term here: two would double the second product.
 //
 // A workgroup owns 32 rows a wavefront and walks tiles of 64 tokens.  A tile's codes are widened once,
 // every wavefront its share, into LDS; rows of LDS are 16 bytes longer than their data, so that the
@@ -971,8 +980,8 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
         // (tokens that start and end inside a step: two steps more)
         const int64_t most = p.units * ((cap / 32 + 2 + FEW_LEAST - 1) / FEW_LEAST), round = few_round(c.d_pad / 32, p.mt);
         // One round of workgroups where few sequences leave most of it to full ranges (one row over 57600
-        // tokens, 40 heads: 59 us, in two rounds 62); else about two, whose ranges are shorter, so that the
-        // last ones end closer together (64 ragged sequences: 220 us, in one round 240).  Sequences that fill the CUs by
+        // tokens, 40 heads: least of 90 calls 55 us, in two rounds 58); else about two, whose ranges are shorter, so that
+        // the last ones end closer together (64 ragged sequences: 194 us, in one round 213).  Sequences that fill the CUs by
         // themselves stay whole.
         const int64_t target = p.units <= round / 4 ? round - p.units : p.units < round ? 2 * round - p.units : round;
         p.groups = p.units;

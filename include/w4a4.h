@@ -505,7 +505,7 @@ int w4a4_moe_forward(const void* X, int x_dtype, int64_t T, const w4a4_moe* moe,
  *   - The integer sums are exact (32 bits; d_in <= W4A4_INT8_MAX_D_IN keeps any codes, -128
  *     included, within them).  An output is fl32(fl32(s_x s_w) fl32(sum)), rounded once more
  *     for bf16, so calls are bit-reproducible whatever the shape.
- *   - Limits: 1 <= d_in <= W4A4_INT8_MAX_D_IN, 1 <= d_out <= W4A4_INT8_MAX_D_OUT, up to 2^26
+ *   - Limits: 1 <= d_in <= W4A4_INT8_MAX_D_IN, 1 <= d_out <= W4A4_INT8_MAX_D_OUT, up to 2^26 - 16
  *     tokens and 2^39 outputs (W4A4_ERR_SHAPE above).
  * The conventions at the top of this file hold. */
 #define W4A4_INT8_MAX_D_IN 131072
@@ -648,7 +648,7 @@ int w4a4_kv_read(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache
 /* Bytes of an attention call's workspace: partial results of long sequences' ranges. */
 int w4a4_kv_attention_workspace_size(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache,
                                      int32_t n_q_heads, size_t* bytes);
-/* O device bf16 [n_rows][n_q_heads][head_dim]; scale > 0; causal 0 or 1; window >= 0 (0: none;
+/* O device bf16 [n_rows][n_q_heads][head_dim]; scale > 0 (scale log2(e) finite); causal 0 or 1; window >= 0 (0: none;
  * only with causal).  Async. */
 int w4a4_kv_attention(const w4a4_kv_rows* Q, int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache,
                       int32_t n_q_heads, float scale, int causal, int64_t window, uint16_t* O, void* ws, size_t ws_bytes,

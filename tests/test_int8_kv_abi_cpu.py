@@ -42,6 +42,7 @@ def test_int8_sizes(L):
             setattr(d, a, v)
         assert L.w4a4_int8_workspace_layout(4, d, out) == code, change
     assert L.w4a4_int8_workspace_layout(-1, _packed(), out) == 1 and L.w4a4_int8_workspace_layout((1 << 26) + 1, _packed(), out) == 2
+    assert L.w4a4_int8_workspace_layout((1 << 26) - 15, _packed(), out) == 2 and L.w4a4_int8_workspace_layout((1 << 26) - 16, _packed(), out) == 0
     assert L.w4a4_int8_workspace_layout(4, None, out) == 1 and L.w4a4_int8_workspace_layout(4, _packed(), None) == 1
 
 
@@ -110,7 +111,7 @@ def test_kv_refusals(L):
         bad[i] = v
         return L.w4a4_kv_attention(*bad)
     for i, v, code in [(0, None, 1), (1, -1, 1), (1, (1 << 26) + 1, 2), (2, None, 1), (3, None, 1), (4, 0, 1), (4, 3, 1), (4, 4098, 2), (5, 0.0, 1),
-                       (5, -1.0, 1), (5, math.nan, 1), (5, math.inf, 1), (6, 2, 1), (7, -1, 1), (8, None, 1), (8, FAKE + 2, 3), (9, None, 1),
+                       (5, -1.0, 1), (5, math.nan, 1), (5, math.inf, 1), (5, 3e38, 1), (6, 2, 1), (7, -1, 1), (8, None, 1), (8, FAKE + 2, 3), (9, None, 1),
                        (9, FAKE + 4, 3)]:
         assert attention(i, v) == code, (i, v)
     bad = list(ok)
