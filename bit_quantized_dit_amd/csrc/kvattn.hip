@@ -198,12 +198,13 @@ __device__ __forceinline__ void load_q8(const AttnArgs& a, int64_t at, int p, bo
 __device__ __forceinline__ v8bf pack_q(const float* x) { return join8(pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])); }
 
 // Four outputs of a row from channel d on.
+__device__ __forceinline__ void store_quad(uint16_t* p, v4f v) { *reinterpret_cast<uint2*>(p) = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])); }
 __device__ __forceinline__ void store_out4(uint16_t* row, int d, int D, v4f v) {
-    const uint32_t w[2] = {pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
-    if (d + 4 <= D && (D & 3) == 0) {
-        *reinterpret_cast<uint2*>(row + d) = make_uint2(w[0], w[1]);
+    if ((D & 3) == 0) {
+        if (d < D) store_quad(row + d, v);
         return;
     }
+    const uint32_t w[2] = {pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (d + i < D) row[d + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
@@ -534,12 +535,13 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     __shared__ uint8_t nans[M::VSLOTS][M::PARTS][64];      // a token's groups that are NaN
     const int lane = threadIdx.x & 63, c = lane & 31, h2 = lane >> 5, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int sp = blockIdx.x % nsplit;
-    const uint32_t rest = blockIdx.x / nsplit;
-    const int tile = (int)(row_tiles - 1 - rest % row_tiles);      // the rows that see most first
-    const int64_t unit = rest / row_tiles;
-    const int64_t b = unit / a.kv.n_heads;
-    const int h = (int)(unit - b * a.kv.n_heads);
+    const uint32_t sp = blockIdx.x % (uint32_t)nsplit, rest = blockIdx.x / (uint32_t)nsplit;
+    // the rows that see most first; tiles past a short sequence's rows stand together, so that the others spread evenly
+    const uint32_t units = (uint32_t)(a.kv.n_seqs * a.kv.n_heads), behind = rest / units, unit = rest - behind * units;
+    const int tile = (int)(row_tiles - 1 - behind);
+    const uint32_t seq = unit / (uint32_t)a.kv.n_heads;
+    const int64_t b = seq;
+    const int h = (int)(unit - seq * (uint32_t)a.kv.n_heads);
     const KvSeq s = kv_seq(a.kv, b);
     const int64_t all_rows = (int64_t)s.done * a.ratio;
     const int64_t m0 = (int64_t)tile * ROWS;
@@ -547,8 +549,12 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     const int rows = (int)(all_rows - m0 < ROWS ? all_rows - m0 : ROWS);
     const Steps<64> st(a, s, (int32_t)m0, (int32_t)(m0 + rows));
     const int parts = many_parts(st.n, nsplit);
-    if (sp >= parts) return;
-    const int s0 = (int)((int64_t)st.n * sp / parts), s1 = (int)((int64_t)st.n * (sp + 1) / parts);
+    if ((int)sp >= parts) return;
+    int s0 = 0, s1 = st.n;
+    if (parts > 1) {
+        s0 = (int)((int64_t)st.n * sp / parts);
+        s1 = (int)((int64_t)st.n * (sp + 1) / parts);
+    }
 
     const int row = wave * 32 + c, m = (int)m0 + row, qi = m / a.ratio, qj = m - qi * a.ratio;
     const bool on = row < rows;
@@ -841,17 +847,19 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     sum += __shfl_xor(sum, 32);
     if (!on) return;
     const float f = parts > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = (unit * nsplit + sp) * a.rows_cap + m;
+    const int64_t at = ((int64_t)unit * nsplit + sp) * a.rows_cap + m;
     uint16_t* const out = a.out + ((s.row0 + qi) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + qj) * a.kv.head_dim;
+    auto each = [&](auto put) __attribute__((always_inline)) {
 #pragma unroll
-    for (int d = 0; d < G; ++d)
+        for (int d = 0; d < G; ++d)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const v4f v = v4f{acc[d][4 * u] * f, acc[d][4 * u + 1] * f, acc[d][4 * u + 2] * f, acc[d][4 * u + 3] * f};
-            const int ch = 32 * d + 8 * u + 4 * h2;
-            if (parts == 1) store_out4(out, ch, a.kv.head_dim, v);
-            else *reinterpret_cast<v4f*>(a.part_o + at * DP + ch) = v;
-        }
+            for (int u = 0; u < 4; ++u)
+                put(32 * d + 8 * u + 4 * h2, v4f{acc[d][4 * u] * f, acc[d][4 * u + 1] * f, acc[d][4 * u + 2] * f, acc[d][4 * u + 3] * f});
+    };
+    // (one branch for all: the elements' stores are many instructions)
+    if (parts > 1) each([&](int ch, v4f v) { *reinterpret_cast<v4f*>(a.part_o + at * DP + ch) = v; });
+    else if ((a.kv.head_dim & 3) == 0) each([&](int ch, v4f v) { if (ch < a.kv.head_dim) store_quad(out + ch, v); });
+    else each([&](int ch, v4f v) { store_out4(out, ch, a.kv.head_dim, v); });
     if (parts > 1 && h2 == 0) {
         a.part_ml[2 * at] = mx;
         a.part_ml[2 * at + 1] = sum;
