@@ -323,7 +323,11 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
             constexpr int WORDS = 4 * L::SG;      // of a block's value scales: tokens 4 (i / sg) .., group i % sg
             if (lane < 2 * WORDS) {
                 uint32_t* const w = reinterpret_cast<uint32_t*>(x + lane / WORDS * L::BYTES + L::VS) + lane % WORDS;
-                if (wild(*w)) *w = tame(*w, nan);
+                if (wild(*w)) {
+                    *w = tame(*w, nan);
+                    const int left = s.len - (pos + lane / WORDS * 16 + lane % WORDS / L::SG * 4);      // tokens that were written
+                    nan &= left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1u;
+                }
             }
             asm volatile("" ::: "memory");
         }
@@ -524,6 +528,39 @@ constexpr float P_MOST = 256.0f;
 constexpr int MANY_LEAST = 8;
 __device__ __forceinline__ int many_parts(int n, int nsplit) { return n / MANY_LEAST < 1 ? 1 : n / MANY_LEAST < nsplit ? n / MANY_LEAST : nsplit; }
 
+// The item'th of all sequences' tiles of ROWS rows, a sequence's last ones, which see most, first.  Of up to 64
+// sequences every wavefront counts their tiles, one a lane, so that no workgroup without rows stands between the others
+// and two of them share a CU only when all CUs have one (5 prompts of 1 to 777 rows: 19.1 us, with gaps 21.2).  More sequences have room
+// for row_tiles tiles each.
+struct TileAt {
+    KvSeq s;
+    int32_t b, tile;      // tile -1: there is none
+};
+template <int ROWS> __device__ __forceinline__ TileAt find_tile(const AttnArgs& a, uint32_t item, uint32_t row_tiles) {
+    TileAt t;
+    if (a.kv.n_seqs > 64) {
+        const uint32_t n = (uint32_t)a.kv.n_seqs, behind = item / n;
+        t.b = (int32_t)(item - behind * n);
+        t.tile = (int32_t)(row_tiles - 1 - behind);
+        t.s = kv_seq(a.kv, t.b);
+        return t;
+    }
+    const int lane = threadIdx.x & 63;
+    KvSeq s = {0, 0, 0, 0, 0};
+    if (lane < a.kv.n_seqs) s = kv_seq(a.kv, lane);
+    const int32_t c = (int32_t)(((int64_t)s.done * a.ratio + ROWS - 1) / ROWS), sc = scan64(c);
+    const uint64_t hit = __ballot((int32_t)item < sc);
+    t.b = hit ? __builtin_ctzll(hit) : 0;
+    auto of = [&](int32_t v) { return __builtin_amdgcn_readlane(v, t.b); };
+    t.s.row0 = (int64_t)((uint64_t)(uint32_t)of((int32_t)(s.row0 >> 32)) << 32 | (uint32_t)of((int32_t)s.row0));
+    t.s.rows = of(s.rows);
+    t.s.done = of(s.done);
+    t.s.len = of(s.len);
+    t.s.first = of(s.first);
+    t.tile = hit ? of(sc) - 1 - (int32_t)item : -1;
+    return t;
+}
+
 template <int G, int WAVES, bool QB>
 __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_kernel(AttnArgs a, uint32_t row_tiles, int32_t nsplit) {
     typedef KvBlock<G> L;
@@ -536,13 +573,13 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     const int lane = threadIdx.x & 63, c = lane & 31, h2 = lane >> 5, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t sp = blockIdx.x % (uint32_t)nsplit, rest = blockIdx.x / (uint32_t)nsplit;
-    // the rows that see most first; tiles past a short sequence's rows stand together, so that the others spread evenly
-    const uint32_t units = (uint32_t)(a.kv.n_seqs * a.kv.n_heads), behind = rest / units, unit = rest - behind * units;
-    const int tile = (int)(row_tiles - 1 - behind);
-    const uint32_t seq = unit / (uint32_t)a.kv.n_heads;
-    const int64_t b = seq;
-    const int h = (int)(unit - seq * (uint32_t)a.kv.n_heads);
-    const KvSeq s = kv_seq(a.kv, b);
+    const uint32_t item = rest / (uint32_t)a.kv.n_heads;
+    const int h = (int)(rest - item * (uint32_t)a.kv.n_heads);
+    const TileAt at_tile = find_tile<ROWS>(a, item, row_tiles);
+    const KvSeq s = at_tile.s;
+    const int64_t b = at_tile.b, unit = b * a.kv.n_heads + h;
+    const int tile = at_tile.tile;
+    if (tile < 0) return;
     const int64_t all_rows = (int64_t)s.done * a.ratio;
     const int64_t m0 = (int64_t)tile * ROWS;
     if (m0 >= all_rows) return;
@@ -725,13 +762,21 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     auto spread_nans = [&](int slot, int64_t p0) __attribute__((always_inline)) {
         const uint4 f = flags_of(slot);
         if (!((f.x | f.y | f.z | f.w) & 1)) return;
-        const uint32_t fb[4] = {f.x, f.y, f.z, f.w};
-        uint32_t bad = 0;
-        for (int t = 0; t < 64; ++t) {
+        // one token a lane; those past the sequence, which were never written, are left out (a last page of random
+        // bytes, ragged prompts: 17.6 us, looked through token by token 19.1)
+        uint32_t bits = 0, bad = 0;
+        bool gone = (int32_t)p0 + lane >= s.len;
+#pragma unroll
+        for (int w = 0; w < M::PARTS; ++w) {
+            const uint32_t fb = reinterpret_cast<const uint32_t*>(&flags[slot][w])[lane >> 4];
+            if (fb & 1) bits |= nans[slot][w][lane];
+            gone |= (fb & 2) != 0;
+        }
+        for (uint64_t left = __ballot(bits != 0 && !gone); left; left &= left - 1) {
+            const int t = __builtin_ctzll(left);
             const int32_t tp = (int32_t)p0 + t;
-            if ((fb[t >> 4] & 2) || tp < lo || tp > hi) continue;
-            for (int w = 0; w < M::PARTS; ++w)
-                if (reinterpret_cast<const uint32_t*>(&flags[slot][w])[t >> 4] & 1) bad |= nans[slot][w][t];
+            const uint32_t group = (uint32_t)__builtin_amdgcn_readlane((int)bits, t);
+            if (tp >= lo && tp <= hi) bad |= group;
         }
 #pragma unroll
         for (int d = 0; d < G; ++d)
@@ -847,7 +892,7 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     sum += __shfl_xor(sum, 32);
     if (!on) return;
     const float f = parts > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = ((int64_t)unit * nsplit + sp) * a.rows_cap + m;
+    const int64_t at = (unit * nsplit + sp) * a.rows_cap + m;
     uint16_t* const out = a.out + ((s.row0 + qi) * a.kv.n_heads * a.ratio + (int64_t)h * a.ratio + qj) * a.kv.head_dim;
     auto each = [&](auto put) __attribute__((always_inline)) {
 #pragma unroll
