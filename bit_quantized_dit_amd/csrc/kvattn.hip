@@ -254,6 +254,41 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
     const int s0 = (int)((int64_t)st.n * rg.k / rg.count), s1 = (int)((int64_t)st.n * (rg.k + 1) / rg.count);
     const int mine = s1 - s0 > wave ? (s1 - s0 - wave + NW - 1) / NW : 0;
 
+    // Block addresses of 32 steps, two a step, one a lane (zero where a block is not there).
+    uint64_t addr = 0;
+    auto lookup = [&](int k) __attribute__((always_inline)) {
+        const int mk = k + (lane >> 1);
+        addr = mk < mine ? (uint64_t)(uintptr_t)kv_block(a.kv, b, (uint32_t)(st.start / 16 + 2 * (s0 + wave + mk * NW) + (lane & 1)), h) : 0;
+    };
+    const uint32_t ring = (uint32_t)(uintptr_t)smem + (uint32_t)wave * R * F::STEP;
+    uint64_t there_bits = 0;      // whether each block of these steps is there
+    auto copy = [&](int k, uint32_t slot) __attribute__((always_inline)) {      // step k of this wavefront into a slot of its ring
+        if ((k & 31) == 0) {
+            lookup(k);
+            there_bits = __ballot(addr != 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int from = 2 * (k & 31) + u;
+            const uint32_t al = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)addr, from);
+            const uint32_t ah = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(addr >> 32), from);
+            const uint64_t p = (uint64_t)ah << 32 | al;
+            const v4i srd = make_srd((const void*)(uintptr_t)p, p ? L::BYTES : 0u);
+#pragma unroll
+            for (int i = 0; i < F::COPIES; ++i) {
+                const int off = i * 1024 + lane * 16;
+                if (off < L::BYTES) dma16_once(srd, ring + slot * F::STEP + u * L::BYTES + i * 1024, off, 0);
+            }
+        }
+    };
+    uint64_t there = 0;      // of the steps whose copies are under way, two bits a step, the next one lowest
+    auto there_of = [&](int k) { return (uint32_t)(there_bits >> (2 * (k & 31))) & 3u; };
+#pragma unroll
+    for (int k = 0; k < R - 1; ++k) {      // on their way while the queries are read
+        copy(k, k);
+        there |= (uint64_t)there_of(k) << (2 * k);
+    }
+
     // this lane's rows: the operand of each block of 32 channels, and the tokens they see
     v8bf q[MT][G];
     int32_t lo[MT], hi[MT];
@@ -286,33 +321,6 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
         for (int t = 0; t < 2 * G; ++t) acc[mt][t] = v4f{0, 0, 0, 0};
     }
 
-    // Block addresses of 32 steps, two a step, one a lane (zero where a block is not there).
-    uint64_t addr = 0;
-    auto lookup = [&](int k) __attribute__((always_inline)) {
-        const int mk = k + (lane >> 1);
-        addr = mk < mine ? (uint64_t)(uintptr_t)kv_block(a.kv, b, (uint32_t)(st.start / 16 + 2 * (s0 + wave + mk * NW) + (lane & 1)), h) : 0;
-    };
-    const uint32_t ring = (uint32_t)(uintptr_t)smem + (uint32_t)wave * R * F::STEP;
-    uint64_t there_bits = 0;      // whether each block of these steps is there
-    auto copy = [&](int k, uint32_t slot) __attribute__((always_inline)) {      // step k of this wavefront into a slot of its ring
-        if ((k & 31) == 0) {
-            lookup(k);
-            there_bits = __ballot(addr != 0);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int from = 2 * (k & 31) + u;
-            const uint32_t al = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)addr, from);
-            const uint32_t ah = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(addr >> 32), from);
-            const uint64_t p = (uint64_t)ah << 32 | al;
-            const v4i srd = make_srd((const void*)(uintptr_t)p, p ? L::BYTES : 0u);
-#pragma unroll
-            for (int i = 0; i < F::COPIES; ++i) {
-                const int off = i * 1024 + lane * 16;
-                if (off < L::BYTES) dma16_once(srd, ring + slot * F::STEP + u * L::BYTES + i * 1024, off, 0);
-            }
-        }
-    };
     // One step from token `pos` on; `there` tells which of its two blocks are in the cache.  Where some row
     // does not see all of its tokens, their scores become -Inf; value scale codes that no weight
     // of zero may be multiplied with are made harmless first, and values that are NaN go by a list of their own.
@@ -425,13 +433,6 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
             }
         }
     };
-    uint64_t there = 0;      // of the steps whose copies are under way, two bits a step, the next one lowest
-    auto there_of = [&](int k) { return (uint32_t)(there_bits >> (2 * (k & 31))) & 3u; };
-#pragma unroll
-    for (int k = 0; k < R - 1; ++k) {
-        copy(k, k);
-        there |= (uint64_t)there_of(k) << (2 * k);
-    }
     uint32_t slot = 0;
     for (int k = 0; k < mine; ++k) {
         // the slot read last is free: its reads are in registers
