@@ -222,8 +222,10 @@ __device__ __forceinline__ void store_out4(uint16_t* row, int d, int D, v4f v) {
 // reads them twice (through them: 227 and 64 us); rings of 4 steps, of which fewer wavefronts fit, are slower, and so
 // are workgroups of 8 wavefronts.  The copies past the last step run with empty ranges, so that every wait counts the same number.  The wavefronts'
 // results meet in LDS.
+// (One wavefront a SIMD has its sums copied between register files at every use: 64 rows of 40 heads of 72 over 57600 tokens 170 us,
+// with two and 52 bytes in scratch 133; 20 rows of 192 channels 143 and 103.  Heads of 256 do not fit: 20 rows 326, with two 363.)
 template <int G, int MT> struct Few {      // wavefronts of a workgroup, steps of a ring, wavefronts a SIMD (for the register budget)
-    static constexpr int NW = 4, R = 2, OCC = G * MT <= 4 ? 4 : G * MT <= 8 ? 2 : 1;
+    static constexpr int NW = 4, R = 2, OCC = G * MT <= 4 ? 4 : G * MT <= 12 ? 2 : 1;
     static constexpr int COPIES = (KvBlock<G>::BYTES + 1023) / 1024, STEP = 2 * KvBlock<G>::BYTES, LD = 32 * G + 4;
     static constexpr int64_t ROUND = 256 * OCC;      // workgroups at a time
     static constexpr int RING = NW * R * STEP, RED = NW * 16 * LD * 4, LDS = RING > RED ? RING : RED;
@@ -1022,7 +1024,11 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
     Plan p = {};
     const int64_t ratio = n_q_heads / c.n_heads, rows = b.max_rows * ratio, all = b.max_pages * c.page_tokens;
     const int64_t cap = window && window + b.max_rows < all ? window + b.max_rows : all;
-    p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= W4A4_KV_FEW_ROWS && c.d_pad <= 128 ? 4 : 0;
+    // Four tiles of rows up to 96 channels (40 rows, 8 heads, 8 sequences of 8192 tokens, us a call: 64 channels 38, the other kernel
+    // 39; 72: 48 and 47; 64 rows of 40 heads over 57600 tokens 102 and 140, 133 and 172), whose sums wider heads would not
+    // leave in registers (128: 143 and 52, 469 and 192).  Two tiles at any width (32 rows, 8 heads, 32 sequences of 4096 tokens:
+    // 128 channels 52 and 139, 256: 147 and 208).
+    p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= W4A4_KV_FEW_ROWS && c.d_pad <= 96 ? 4 : 0;
     p.units = b.n_seqs * c.n_heads;
     p.rows_cap = (int32_t)rows;
     // eight wavefronts share a tile's widening where that leaves every CU a workgroup
@@ -1109,7 +1115,7 @@ hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4
         if (p.mt) {
             if (p.mt == 1) run_few<G, 1>(a, p, qb, stream);
             else if (p.mt == 2) run_few<G, 2>(a, p, qb, stream);
-            else if constexpr (G <= 4) run_few<G, 4>(a, p, qb, stream);
+            else if constexpr (G <= 3) run_few<G, 4>(a, p, qb, stream);
         } else {
             if constexpr (G <= 4) {
                 if (p.waves == 8) run_many<G, 8>(a, p, qb, stream);
