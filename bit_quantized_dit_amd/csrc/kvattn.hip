@@ -55,8 +55,9 @@ template <int ST> struct Steps {
 // belong to, so that a ragged batch keeps all CUs busy to the end: with `target` workgroups in mind a
 // range has total / target steps, at least FEW_LEAST.  The lengths are the device's: up to 64 sequences every
 // wavefront sums their steps, one a lane, and looks its number up among their ranges; for more a small kernel does it
-// first, for all (500 sequences of 300 tokens in a long table, 8 heads: 53 us, with every wavefront looking 112).  Ranges of sequences that have several leave their results in slots, of which there are fewer
-// than 2 target (a sequence of n steps > C has at most n / C + 1 < 2 n / C).
+// first, for all (500 sequences of 300 tokens in a long table, 8 heads: 53 us, with every wavefront looking 112).  Ranges of
+// sequences that have several leave their results in slots, of which there are fewer than 2 target (a sequence of
+// n steps > C has at most n / C + 1 < 2 n / C).
 constexpr int FEW_LEAST = 16;      // steps of a range: 512 tokens
 struct alignas(16) Range {
     int32_t b, slot;      // slot of the sequence's first range (heads lie side by side)

@@ -387,6 +387,17 @@ def test_windows_that_are_cut(window):
     _check_attention(s, [100, 70, 1], 2, window=window)
 
 
+@pytest.mark.parametrize("n", [64, 65, 70])
+def test_many_rows_of_many_sequences(n):
+    """Row tiles counted by a wavefront's lanes, and of more sequences; some without rows."""
+    lens = [37 * i % 211 for i in range(n)]
+    rows = [0 if i % 5 == 4 else min(lens[i], 13 * i % 80) for i in range(n)]
+    rows[3] = lens[3] = 150
+    s = Setup(lens, 1, 32, 16)
+    _check_attention(s, rows, 1)
+    _check_attention(s, rows, 2, window=40)
+
+
 @pytest.mark.parametrize("n,H,Hq", [(65, 1, 1), (130, 2, 10), (300, 1, 4), (1100, 1, 2)])
 def test_many_sequences(n, H, Hq):
     """More sequences than a wavefront has lanes, some without rows or tokens, a few long, in a table of long ones."""
