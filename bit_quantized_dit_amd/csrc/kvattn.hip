@@ -23,8 +23,13 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
-constexpr float M_NONE = -3.0e38f;       // below every score that counts
+constexpr float M_NONE = -3.40282347e38f;      // no score yet: the lowest number
 constexpr float M_SLACK = 8.0f;
+// A weight's exponent is scale s - m, one rounding at the end, with m the rounded scale s of some token: the rounding
+// of m is a factor that all weights share.  It is 2^(1/2) at most while |m| <= 2^24, and past 2^31 it could be
+// infinity or zero.  Rows with maxima past 2^24 therefore round scale s as m was rounded, before m is taken off
+// (calls without such rows: the same times within 1%).
+constexpr float M_FAR = 16777216.0f;
 
 struct AttnArgs {
     KvArgs kv;
@@ -315,6 +320,7 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
     const int64_t last_from = a.causal && a.window ? (int64_t)s.first + s.done - a.window : 0;
 
     v4f acc[MT][2 * G];
+    uint64_t far_rows = 0;      // lanes whose maxima are past M_FAR
     float mx[MT], sum[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -383,19 +389,27 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
             float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(sc[mt][0][0], sc[mt][0][1]), __builtin_fmaxf(sc[mt][0][2], sc[mt][0][3])),
                                         __builtin_fmaxf(__builtin_fmaxf(sc[mt][1][0], sc[mt][1][1]), __builtin_fmaxf(sc[mt][1][2], sc[mt][1][3])));
             top *= a.scale;
-            if (__any(top > mx[mt] + M_SLACK)) {
+            float k = a.scale;
+            if (far_rows | __ballot(top > mx[mt] + M_SLACK)) {
                 top = __builtin_fmaxf(top, __shfl_xor(top, 16));
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32));
                 const float m = __builtin_fmaxf(mx[mt], top), f = __builtin_amdgcn_exp2f(mx[mt] - m);
+                const bool far = __builtin_fabsf(m) > M_FAR && m != M_NONE;
                 mx[mt] = m;
+                far_rows |= __ballot(far);
                 sum[mt] *= f;
 #pragma unroll
                 for (int t = 0; t < 2 * G; ++t) acc[mt][t] *= f;
+                if (far_rows) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sc[mt][i >> 2][i & 3] *= far ? a.scale : 1.0f;
+                    k = far ? 1.0f : a.scale;
+                }
             }
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][i >> 2][i & 3], a.scale, -mx[mt]));
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][i >> 2][i & 3], k, -mx[mt]));
                 sum[mt] += p[i];
             }
             uint32_t wh[4], wl[4];
@@ -614,6 +628,7 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
     float mx = M_NONE, sum = 0.0f;
+    uint64_t far_rows = 0;      // lanes whose maxima are past M_FAR
 
     // This wavefront's share of a tile: of block `blk` the keys of token r16, groups from k0 on, and of the values
     // of tokens 4 hh .. and 8 + 4 hh .. the groups from v0 on (shares that do not divide overlap).
@@ -709,16 +724,16 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     uint32_t pw[16];      // weights
     float tile_sum = 0.0f;
     // weights 2 i, 2 i + 1
-    auto weigh = [&](int i) __attribute__((always_inline)) {
-        const float pa = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 3][2 * (i & 7)], a.scale, -mx));
-        const float pb = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 3][2 * (i & 7) + 1], a.scale, -mx));
+    auto weigh = [&](int i, float k) __attribute__((always_inline)) {
+        const float pa = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 3][2 * (i & 7)], k, -mx));
+        const float pb = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 3][2 * (i & 7) + 1], k, -mx));
         tile_sum = i == 0 ? pa + pb : tile_sum + (pa + pb);
         pw[i] = pk_bf16(pa, pb);
         asm volatile("" : "+v"(pw[i]), "+v"(tile_sum));      // here, between the matrix instructions
     };
     // Whether the weights just taken may be used; if not, they are taken again with a new maximum.
     auto settle = [&]() __attribute__((always_inline)) {
-        if (__any(!(tile_sum <= P_MOST))) {
+        if (far_rows | __ballot(!(tile_sum <= P_MOST))) {
             float top = sc[0][0];
 #pragma unroll
             for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i >> 4][i & 15]);
@@ -729,8 +744,16 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
             sum *= f;
 #pragma unroll
             for (int d = 0; d < G; ++d) acc[d] *= f;
+            const bool far = __builtin_fabsf(mx) > M_FAR && mx != M_NONE;
+            far_rows |= __ballot(far);
+            float k = a.scale;
+            if (far_rows) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) weigh(i);
+                for (int i = 0; i < 32; ++i) sc[i >> 4][i & 15] *= far ? a.scale : 1.0f;
+                k = far ? 1.0f : a.scale;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) weigh(i, k);
         }
         sum += tile_sum;
     };
@@ -846,12 +869,12 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
                 // the weights of 16 tokens are free after their G steps
                 if (i >= G) {
 #pragma unroll
-                    for (int e = 4 * (i - G) / G; e < 4 * (i + 1 - G) / G; ++e) weigh(e);
+                    for (int e = 4 * (i - G) / G; e < 4 * (i + 1 - G) / G; ++e) weigh(e, a.scale);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 12; e < 16; ++e) weigh(e);
+            for (int e = 12; e < 16; ++e) weigh(e, a.scale);
             if constexpr (!FIRST) spread_nans((j - 1) & VS, st.start + (int64_t)(s0 + j - 1) * 64);
             settle();
         };
@@ -881,7 +904,7 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
             }
             hide(s0 + j, j & VS);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) weigh(e);
+            for (int e = 0; e < 16; ++e) weigh(e, a.scale);
             settle();
 #pragma unroll
             for (int i = 0; i < N; ++i) {

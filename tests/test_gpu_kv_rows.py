@@ -1,0 +1,107 @@
+"""Attention over the 4-bit cache: scores anywhere in the range of binary32."""
+import numpy as np
+import pytest
+import torch
+
+from bit_quantized_dit_amd import w4a4 as B
+from tests import kv_ref as R
+from tests.test_gpu_kv import BF16, Setup
+
+pytestmark = pytest.mark.gpu
+
+LOG2E = 1.4426950408889634
+F32_MAX = float(np.finfo(np.float32).max)
+
+
+def _attend(s, rows, q, causal=True, scale=1.0, qt=BF16):
+    n, Hq = q.shape[:2]
+    b = s.batch(rows)
+    O = torch.full((n, Hq, s.D), 7.0, dtype=BF16, device="cuda")
+    B.w4a4_kv_attention(torch.from_numpy(q).cuda().to(qt), b, s.cache, O, B.alloc_workspace_kv(n, b, Hq, s.cache), scale=scale, causal=causal)
+    torch.cuda.synchronize()
+    return O
+
+
+# (rows, tokens, key/value heads, channels): one row, several, ranges that are joined, many rows by four wavefronts, many by eight
+FORMS = [(1, 300, 1, 64), (9, 300, 2, 64), (30, 300, 1, 128), (50, 300, 1, 64), (1, 5000, 1, 64), (9, 5000, 1, 128), (80, 300, 1, 64),
+         (80, 300, 1, 200), (70, 5000, 1, 64), (300, 400, 130, 32)]
+
+
+def _one_channel(rows, n, H, D, ks, q0):
+    """Keys and queries with one channel that is not zero, so that a score is one exact product q0 ks[t]."""
+    def edit(s):
+        s.K[:] = 0
+        s.K[:, :, 0] = np.float32(ks)[:, None]
+    s = Setup([n], H, D, 16, edit=edit)
+    assert np.array_equal(s.values(0, [0])[0][:, 0, 0], np.float64(ks))      # codes hold them
+    q = np.zeros((rows, 2 * H, D), np.float32)
+    q[:, :, 0] = q0
+    return s, q
+
+
+@pytest.mark.parametrize("form", FORMS, ids=str)
+@pytest.mark.parametrize("q0,grid", [(2.0 ** 24, [1, 2, 3]), (2.0 ** 33, [1, 2, 3]), (2.0 ** 60, [1.5, 3, 6]), (-2.0 ** 33, [1.5, 3, 6]), (-2.0 ** 60, [1, 2, 4]),
+                                     (1.375 * 2.0 ** 125, [1, 2, 3, 4]), (-1.25 * 2.0 ** 125, [4, 6]), (-1.375 * 2.0 ** 125, [4])])
+def test_scores_of_any_size(form, q0, grid):
+    """Scores so large that the weights are those of the largest ones alone, up to the ends of binary32: the
+    mean of their values.  A weight of 1 and sums of at most 5000 values in binary32 (2 L + 16 roundings, as in the oracle's
+    bound), then bf16.  Scaled scores below binary32 are -Inf, as the 4 of -1.25 2^127 is beside the 6."""
+    rows, n, H, D = form
+    ks = np.random.default_rng(1).choice(grid, n)
+    ks[0], ks[n // 2] = grid[0], grid[-1]
+    s, q = _one_channel(rows, n, H, D, ks, q0)
+    x = ks * q0 * LOG2E
+    assert (x <= F32_MAX).all() and (x >= -F32_MAX).any()
+    O = _attend(s, [rows], q, causal=False).double().cpu().numpy()
+    best = x == x.max()
+    for h in [0, H - 1]:
+        v = s.values(0, [h])[1][best, 0]
+        want, mag = v.mean(0), np.abs(v).mean(0)
+        tol = (2 * n + 16) * 2.0 ** -23 * mag
+        tol = tol + R.BF16_U * (np.abs(want) + tol)
+        for j in (2 * h, 2 * h + 1):
+            assert (np.abs(O[:, j] - want[None]) <= tol[None]).all(), (h, j, float(np.abs(O[:, j] - want[None]).max()))
+
+
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_scores_past_binary32(form):
+    """A scaled score above the largest number is +Inf and makes its row NaN; all of them below the lowest are -Inf: zero."""
+    rows, n, H, D = form
+    ks = np.full(n, 1.0)
+    ks[n // 3] = 4.0
+    s, q = _one_channel(rows, n, H, D, ks, 1.5 * 2.0 ** 125)
+    assert bool(torch.isnan(_attend(s, [rows], q, causal=False)).all())
+    q[:] = 0
+    q[rows // 2, 1, 0] = 1.5 * 2.0 ** 125      # one row of many
+    nan = torch.isnan(_attend(s, [rows], q, causal=False))
+    assert bool(nan[rows // 2, 1].all()) and int(nan.sum()) == D
+    s, q = _one_channel(rows, n, H, D, np.full(n, 4.0), -1.5 * 2.0 ** 125)
+    assert not bool(_attend(s, [rows], q, causal=False).any())
+
+
+@pytest.mark.parametrize("form", FORMS, ids=str)
+@pytest.mark.parametrize("where", ["first", "last"])
+def test_far_scores_beside_ordinary_ones(form, where):
+    """One block of tokens far below all others (weight zero, in whichever order they come), or one token far above (all of the weight)."""
+    rows, n, H, D = form
+    rng = np.random.default_rng(2)
+    ks = rng.choice([-1.0, -0.5, 0.5, 1.0], n)
+    far = slice(0, 37) if where == "first" else slice(n - 37, n)
+    ks[far] = -2.0 ** 44
+    s, q = _one_channel(rows, n, H, D, ks, 2.0)
+    O = _attend(s, [rows], q, causal=False).double().cpu()
+    keep = np.ones(n, bool)
+    keep[far] = False
+    qd = torch.from_numpy(q).double()
+    for h in [0, H - 1]:
+        k, v = (x[keep, 0] for x in s.values(0, [h]))
+        o, tol, _ = R.attention(qd[:, 2 * h], k, v, 1.0, np.zeros(rows, int), np.full(rows, int(keep.sum())), rows * 2 <= 32)
+        assert bool(((O[:, 2 * h] - o).abs() <= tol).all())
+    at = 3 if where == "first" else n - 3
+    ks[far] = 0.5
+    ks[at] = 2.0 ** 44
+    s, q = _one_channel(rows, n, H, D, ks, 2.0)
+    O = _attend(s, [rows], q, causal=False).double().cpu().numpy()
+    for h in [0, H - 1]:
+        want = s.values(0, [h])[1][at, 0]
+        assert (np.abs(O[:, 2 * h] - want) <= R.BF16_U * np.abs(want) * (1 + 2.0 ** -14)).all()
