@@ -11,8 +11,9 @@
 // of two are bf16 numbers, exactly: one conversion widens and scales two of them.
 //
 // The running maximum moves lazily: p_t = 2^(x_t - m) with m a maximum that is renewed only when
-// a score passes it by more than 2^8, which leaves the result as it is (numerator and denominator
-// carry the same factor) and spares most steps the exchange between lanes and the rescaling of O.
+// a weight passes 2^8 (many rows: a tile's weights 2^16), which leaves the result as it is (numerator and denominator
+// carry the same factor) and spares most steps the exchange between lanes and the rescaling of O.  Every row renews
+// by its own scores alone, so that its bits do not depend on the rows beside it.
 #include "kv_device.h"
 
 namespace w4a4 {
@@ -393,7 +394,8 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
             if (far_rows | __ballot(top > mx[mt] + M_SLACK)) {
                 top = __builtin_fmaxf(top, __shfl_xor(top, 16));
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                const float m = __builtin_fmaxf(mx[mt], top), f = __builtin_amdgcn_exp2f(mx[mt] - m);
+                // (a row's own scores decide: other rows' tokens must not move its rounding)
+                const float m = top > mx[mt] + M_SLACK ? top : mx[mt], f = __builtin_amdgcn_exp2f(mx[mt] - m);
                 const bool far = __builtin_fabsf(m) > M_FAR && m != M_NONE;
                 mx[mt] = m;
                 far_rows |= __ballot(far);
@@ -541,7 +543,8 @@ template <int G, int WAVES> struct Many {
     static constexpr int VSLOTS = G <= 4 && NW == 8 ? 4 : 2;
     static constexpr int OCC = G <= 4 ? 2 : 1;
 };
-constexpr float P_MOST = 256.0f;
+// (a row at a time renews its maximum: with 2^8 the ragged windowed prompts are settled often enough to take 17.6 us, with 2^16 17.0)
+constexpr float P_MOST = 65536.0f;
 // The ranges that a row tile's steps are cut into, out of nsplit that there is room for.
 constexpr int MANY_LEAST = 8;
 __device__ __forceinline__ int many_parts(int n, int nsplit) { return n / MANY_LEAST < 1 ? 1 : n / MANY_LEAST < nsplit ? n / MANY_LEAST : nsplit; }
@@ -733,13 +736,16 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     };
     // Whether the weights just taken may be used; if not, they are taken again with a new maximum.
     auto settle = [&]() __attribute__((always_inline)) {
-        if (far_rows | __ballot(!(tile_sum <= P_MOST))) {
+        const uint64_t over = __ballot(!(tile_sum <= P_MOST));
+        if (far_rows | over) {
             float top = sc[0][0];
 #pragma unroll
             for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i >> 4][i & 15]);
             top *= a.scale;
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-            const float n = __builtin_fmaxf(mx, top), f = __builtin_amdgcn_exp2f(mx - n);
+            // a row's own weights decide, those of both its lanes: other rows' must not move its rounding
+            const bool own = __builtin_amdgcn_inverse_ballot_w64(far_rows | over | over >> 32 | over << 32);
+            const float n = own ? __builtin_fmaxf(mx, top) : mx, f = __builtin_amdgcn_exp2f(mx - n);
             mx = n;
             sum *= f;
 #pragma unroll

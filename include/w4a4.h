@@ -594,11 +594,12 @@ int w4a4_int8_linear(const void* X, int x_dtype, int64_t T, const w4a4_int8_pack
  *     O[row][j] = bf16_rne(sum_t p_t v_t / sum_t p_t),   p_t = exp(scale (q . k_t) - m)
  * over the tokens t that the row sees: all lens[b] of them, or (causal) t <= the row's own
  * position, or (causal, window > 0) also t > position - window.  A row that sees nothing, or no scaled score above
- * the lowest binary32 number, is zero.  Tokens that a row does not see do not change it, whatever they hold.  A NaN or Inf
+ * the lowest binary32 number, is zero.  Tokens that a row does not see, and the
+ * other rows' queries, do not change a bit of it, whatever they hold.  A NaN or Inf
  * in a group of a visible key makes the row NaN, in a group of a visible value its 32 channels.
  *   - Scores, scaled scores (times scale log2(e)), maxima, sums and outputs are binary32.  A scaled score may have any
  *     value: one above the largest number makes its row NaN, one below the lowest is -Inf and has no weight.  The running
- *     sums' p_t are up to 2^8, so that outputs are finite where |v| < 2^120 / (tokens).  The p_t are rounded to bf16 (for sequences of
+ *     sums' p_t are up to 2^16, so that outputs are finite where |v| < 2^112 / (tokens).  The p_t are rounded to bf16 (for sequences of
  *     up to W4A4_KV_FEW_ROWS stacked rows, max_rows * (n_q_heads / n_heads), half as many where d_pad
  *     is above 96: to two bf16 terms, 16 bits) where they are multiplied with the values.
  *   - Results depend on the sequences, not on where their pages are; the order of sums depends on

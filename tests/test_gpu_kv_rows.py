@@ -1,4 +1,4 @@
-"""Attention over the 4-bit cache: scores anywhere in the range of binary32."""
+"""Attention over the 4-bit cache: scores anywhere in the range of binary32, rows beside others that see more."""
 import numpy as np
 import pytest
 import torch
@@ -105,3 +105,25 @@ def test_far_scores_beside_ordinary_ones(form, where):
     for h in [0, H - 1]:
         want = s.values(0, [h])[1][at, 0]
         assert (np.abs(O[:, 2 * h] - want) <= R.BF16_U * np.abs(want) * (1 + 2.0 ** -14)).all()
+
+
+@pytest.mark.parametrize("D", [64, 72, 128, 200])
+@pytest.mark.parametrize("rows,H,Hq", [(8, 2, 4), (16, 1, 2), (40, 1, 1), (100, 2, 2), (200, 1, 1), (100, 260, 260)])
+def test_rows_do_not_move_each_other(rows, H, Hq, D):
+    """Bits of a row are the same whatever the tokens hold that it does not see, and whatever the rows beside it hold."""
+    if H > 100 and D == 200:
+        pytest.skip("eight wavefronts share a tile up to 128 channels")
+    n, last = 260, 5
+    rng = np.random.default_rng(4)
+    q = (rng.standard_normal((rows, Hq, D)) * 2).astype(np.float32)
+    base = _attend(Setup([n], H, D, 16), [rows], q, scale=D ** -0.5)
+    for factor in (20.0, 2.0 ** 40, np.nan):
+        def edit(s): s.K[n - last:] *= factor
+        s = Setup([n], H, D, 16, edit=edit)
+        got = _attend(s, [rows], q, scale=D ** -0.5)
+        assert torch.equal(got[:rows - last], base[:rows - last]), f"tokens of {factor}"
+    for factor in (20.0, 2.0 ** 40, np.inf):
+        p = q.copy()
+        p[1::2] *= factor
+        got = _attend(Setup([n], H, D, 16), [rows], p, scale=D ** -0.5)
+        assert torch.equal(got[::2], base[::2]), f"rows of {factor}"
