@@ -522,7 +522,9 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
 // Bound by the matrix unit, the vector unit's softmax and widening beside it, and the board's power: 4096 rows of 40
 // heads over 57600 tokens 4278 us, 1.13 PFLOP/s at 2.07 GHz, matrix unit 51% of the cycles (a large bf16 product
 // of the library: 1.24; without the widening 3860, without the exponentials 4040, without either 3290).  So weights are one
-// bf16 term here: two would double the second product.
+// bf16 term here: two would double the second product.  TWO: of up to 64 stacked rows of heads of 97 to 128 channels, which
+// the few-row kernel has no registers for, they are two terms as there (64 rows of 40 heads over 57600 tokens 212 us, with one
+// 196; 64 sequences of 40 rows, 8 heads, 2048 tokens 94; error against 64 bits 0.0016 and 0.0023).
 //
 // A workgroup owns 32 rows a wavefront and walks tiles of 64 tokens.  A tile's codes are widened once,
 // every wavefront its share, into LDS; rows of LDS are 16 bytes longer than their data, so that the
@@ -582,11 +584,11 @@ template <int ROWS> __device__ __forceinline__ TileAt find_tile(const AttnArgs& 
     return t;
 }
 
-template <int G, int WAVES, bool QB>
+template <int G, int WAVES, bool TWO, bool QB>
 __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_kernel(AttnArgs a, uint32_t row_tiles, int32_t nsplit) {
     typedef KvBlock<G> L;
     typedef Many<G, WAVES> M;
-    constexpr int DP = 32 * G, ROWS = M::ROWS, KG = M::KG, VG = M::VG, KLD = M::KLD, VLD = M::VLD, N = 4 * G, FR = 4;
+    constexpr int DP = 32 * G, ROWS = M::ROWS, KG = M::KG, VG = M::VG, KLD = M::KLD, VLD = M::VLD, N = 4 * G, FR = TWO ? 2 : 4;
     __shared__ __attribute__((aligned(16))) uint8_t keys[2][M::KB];
     __shared__ __attribute__((aligned(16))) uint8_t vals[M::VSLOTS][M::VB];
     __shared__ uint4 flags[M::VSLOTS][M::PARTS];           // by share and block: 1 values that are NaN, 2 not there
@@ -724,7 +726,7 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     };
 
     v16f sc[2];           // a tile's scores, 32 tokens each
-    uint32_t pw[16];      // weights
+    uint32_t pw[16], pl[TWO ? 16 : 1];      // weights, and what their rounding left
     float tile_sum = 0.0f;
     // weights 2 i, 2 i + 1
     auto weigh = [&](int i, float k) __attribute__((always_inline)) {
@@ -732,6 +734,7 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
         const float pb = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 3][2 * (i & 7) + 1], k, -mx));
         tile_sum = i == 0 ? pa + pb : tile_sum + (pa + pb);
         pw[i] = pk_bf16(pa, pb);
+        if constexpr (TWO) pl[i] = pk_bf16(pa - __uint_as_float(pw[i] << 16), pb - __uint_as_float(pw[i] & 0xFFFF0000u));
         asm volatile("" : "+v"(pw[i]), "+v"(tile_sum));      // here, between the matrix instructions
     };
     // Whether the weights just taken may be used; if not, they are taken again with a new maximum.
@@ -781,6 +784,8 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
     auto value_step = [&](int i) __attribute__((always_inline)) {
         const int u = i / G;
         acc[i % G] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % FR], join8(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]), acc[i % G], 0, 0, 0);
+        if constexpr (TWO)
+            acc[i % G] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % FR], join8(pl[4 * u], pl[4 * u + 1], pl[4 * u + 2], pl[4 * u + 3]), acc[i % G], 0, 0, 0);
     };
     // A tile's flags by block; bit 0 of any, bit 1 of any.
     auto flags_of = [&](int slot) __attribute__((always_inline)) {
@@ -898,26 +903,30 @@ __global__ __launch_bounds__((WAVES * 64), (Many<G, WAVES>::OCC)) void kv_many_k
             spread_nans((n - 1) & VS, st.start + (int64_t)(s1 - 1) * 64);
         }
     } else {
+        // of at most 64 rows: wavefronts without any widen only
+        const bool live = !TWO || wave * 32 < rows;
         for (int j = 0; j < s1 - s0; ++j) {
             if (j) __syncthreads();
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < FR; ++i) fr[i] = key_operand(j & 1, i);
+                for (int i = 0; i < FR; ++i) fr[i] = key_operand(j & 1, i);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                key_step(i);
-                if (i + FR < N) fr[i % FR] = key_operand(j & 1, i + FR);
-                else fr[i % FR] = value_operand(j & VS, i + FR - N);
+                for (int i = 0; i < N; ++i) {
+                    key_step(i);
+                    if (i + FR < N) fr[i % FR] = key_operand(j & 1, i + FR);
+                    else fr[i % FR] = value_operand(j & VS, i + FR - N);
+                }
+                hide(s0 + j, j & VS);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) weigh(e, a.scale);
+                settle();
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    value_step(i);
+                    if (i + FR < N) fr[i % FR] = value_operand(j & VS, i + FR);
+                }
+                spread_nans(j & VS, st.start + (int64_t)(s0 + j) * 64);
             }
-            hide(s0 + j, j & VS);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) weigh(e, a.scale);
-            settle();
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                value_step(i);
-                if (i + FR < N) fr[i % FR] = value_operand(j & VS, i + FR);
-            }
-            spread_nans(j & VS, st.start + (int64_t)(s0 + j) * 64);
             widen_all((j + 1) & 1, (j + 1) & VS);
             fetch(s0 + j + 2);
         }
@@ -1036,6 +1045,7 @@ __global__ __launch_bounds__(256) void kv_join_many_kernel(AttnArgs a, int32_t n
 // ranges that sequences are cut into, so that there are workgroups for every CU.
 struct Plan {
     int mt, waves;          // mt 0: many rows, of a workgroup of so many wavefronts
+    bool two;               // many rows: weights of two terms
     int64_t units, row_tiles, groups, slots;
     int32_t target, nsplit, rows_cap;
     size_t o_bytes, ml_bytes, join_bytes, bytes;
@@ -1056,13 +1066,14 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
     const int64_t cap = window && window + b.max_rows < all ? window + b.max_rows : all;
     // Four tiles of rows up to 96 channels (40 rows, 8 heads, 8 sequences of 8192 tokens, us a call: 64 channels 38, the other kernel
     // 39; 72: 48 and 47; 64 rows of 40 heads over 57600 tokens 102 and 140, 133 and 172), whose sums wider heads would not
-    // leave in registers (128: 143 and 52, 469 and 192).  Two tiles at any width (32 rows, 8 heads, 32 sequences of 4096 tokens:
-    // 128 channels 52 and 139, 256: 147 and 208).
+    // leave in registers (128: 143 and, with weights of two terms as well, 57; 469 and 212).  Two tiles at any width (32 rows, 8 heads,
+    // 32 sequences of 4096 tokens: 128 channels 52 and 139, 256: 147 and 208).
     p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= W4A4_KV_FEW_ROWS && c.d_pad <= 96 ? 4 : 0;
+    p.two = !p.mt && rows <= W4A4_KV_FEW_ROWS && c.d_pad == 128;
     p.units = b.n_seqs * c.n_heads;
     p.rows_cap = (int32_t)rows;
     // eight wavefronts share a tile's widening where that leaves every CU a workgroup
-    p.waves = c.d_pad <= 128 && p.units * ((rows + 255) / 256) >= 256 ? 8 : 4;
+    p.waves = !p.two && c.d_pad <= 128 && p.units * ((rows + 255) / 256) >= 256 ? 8 : 4;
     const int64_t tile = 32 * p.waves;
     p.row_tiles = p.mt ? 1 : (rows + tile - 1) / tile;
     p.nsplit = 1;
@@ -1105,11 +1116,11 @@ void run_few(const AttnArgs& a, const Plan& p, bool qb, hipStream_t st) {
     else hipLaunchKernelGGL((kv_few_kernel<G, MT, false>), grid, threads, 0, st, a);
 }
 
-template <int G, int WAVES>
+template <int G, int WAVES, bool TWO>
 void run_many(const AttnArgs& a, const Plan& p, bool qb, hipStream_t st) {
     const dim3 grid((uint32_t)p.groups), threads(64 * WAVES);
-    if (qb) hipLaunchKernelGGL((kv_many_kernel<G, WAVES, true>), grid, threads, 0, st, a, (uint32_t)p.row_tiles, p.nsplit);
-    else hipLaunchKernelGGL((kv_many_kernel<G, WAVES, false>), grid, threads, 0, st, a, (uint32_t)p.row_tiles, p.nsplit);
+    if (qb) hipLaunchKernelGGL((kv_many_kernel<G, WAVES, TWO, true>), grid, threads, 0, st, a, (uint32_t)p.row_tiles, p.nsplit);
+    else hipLaunchKernelGGL((kv_many_kernel<G, WAVES, TWO, false>), grid, threads, 0, st, a, (uint32_t)p.row_tiles, p.nsplit);
 }
 
 }  // namespace
@@ -1148,9 +1159,12 @@ hipError_t launch_kv_attention(const w4a4_kv_rows& Q, int64_t n_rows, const w4a4
             else if constexpr (G <= 3) run_few<G, 4>(a, p, qb, stream);
         } else {
             if constexpr (G <= 4) {
-                if (p.waves == 8) run_many<G, 8>(a, p, qb, stream);
+                if (p.waves == 8) run_many<G, 8, false>(a, p, qb, stream);
             }
-            if (p.waves == 4) run_many<G, 4>(a, p, qb, stream);
+            if constexpr (G == 4) {
+                if (p.two) run_many<G, 4, true>(a, p, qb, stream);
+            }
+            if (p.waves == 4 && !p.two) run_many<G, 4, false>(a, p, qb, stream);
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !p.slots) return e;

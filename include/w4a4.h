@@ -601,7 +601,7 @@ int w4a4_int8_linear(const void* X, int x_dtype, int64_t T, const w4a4_int8_pack
  *     value: one above the largest number makes its row NaN, one below the lowest is -Inf and has no weight.  The running
  *     sums' p_t are up to 2^16, so that outputs are finite where |v| < 2^112 / (tokens).  The p_t are rounded to bf16 (for sequences of
  *     up to W4A4_KV_FEW_ROWS stacked rows, max_rows * (n_q_heads / n_heads), half as many where d_pad
- *     is above 96: to two bf16 terms, 16 bits) where they are multiplied with the values.
+ *     is above 128: to two bf16 terms, 16 bits) where they are multiplied with the values.
  *   - Results depend on the sequences, not on where their pages are; the order of sums depends on
  *     shape and lengths only, so calls are bit-reproducible.
  *

@@ -1,4 +1,5 @@
-"""Attention over the 4-bit cache: scores anywhere in the range of binary32, rows beside others that see more."""
+"""Attention over the 4-bit cache: what a row's result may depend on.  Scores anywhere in the range of binary32,
+rows beside others whose scores grow, and the weights' precision by the number of stacked rows."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +11,7 @@ from tests.test_gpu_kv import BF16, Setup
 pytestmark = pytest.mark.gpu
 
 LOG2E = 1.4426950408889634
+FEW_ROWS = 64      # W4A4_KV_FEW_ROWS
 F32_MAX = float(np.finfo(np.float32).max)
 
 
@@ -127,3 +129,41 @@ def test_rows_do_not_move_each_other(rows, H, Hq, D):
         p[1::2] *= factor
         got = _attend(Setup([n], H, D, 16), [rows], p, scale=D ** -0.5)
         assert torch.equal(got[::2], base[::2]), f"rows of {factor}"
+
+
+def two_terms(max_rows, ratio, D):
+    """Whether the header promises weights of two bf16 terms."""
+    return max_rows * ratio <= (FEW_ROWS if R.d_pad(D) <= 128 else FEW_ROWS // 2)
+
+
+@pytest.mark.parametrize("D", [31, 64, 96, 97, 100, 127, 128, 130])
+@pytest.mark.parametrize("rows,H,Hq,lens", [([33], 2, 2, [700]), ([8, 3], 1, 8, [900, 40]), ([64, 1, 20], 1, 1, [64, 30, 333]), ([12], 2, 10, [5000]),
+                                            ([1, 1], 1, 64, [3000, 17]), ([40], 260, 260, [90])])
+def test_weights_of_up_to_64_stacked_rows(D, rows, H, Hq, lens):
+    """33 to 64 stacked rows within the bound of weights in two bf16 terms (2^-16 of themselves) up to 128 channels, of one term above,
+    every output and the root mean square; causal, windowed and not."""
+    s = Setup(lens, H, D, 16)
+    n, ratio = sum(rows), Hq // H
+    few = two_terms(max(rows), ratio, D)
+    assert few == (D <= 128)
+    q = (np.random.default_rng(7).standard_normal((n, Hq, D)) * 2).astype(np.float32)
+    b = s.batch(rows)
+    Q = torch.from_numpy(q).cuda().bfloat16()
+    heads = [0, 1, H - 1] if H > 2 else list(range(H))
+    for causal, window in ((True, 0), (True, 100), (False, 0)):
+        O = torch.empty(n, Hq, D, dtype=BF16, device="cuda")
+        B.w4a4_kv_attention(Q, b, s.cache, O, B.alloc_workspace_kv(n, b, Hq, s.cache), causal=causal, window=window)
+        at, err2, var, count = 0, 0.0, 0.0, 0
+        for i, r in enumerate(rows):
+            k, v = s.values(i, heads)
+            pos = np.arange(lens[i] - r, lens[i])
+            lo = np.maximum(pos - window + 1, 0) if window else np.zeros(r, np.int64)
+            hi = pos + 1 if causal else np.full(r, lens[i])
+            for e, h in enumerate(heads):
+                for j in range(h * ratio, (h + 1) * ratio):
+                    o, tol, va = R.attention(Q[at:at + r, j].double().cpu(), k[:, e], v[:, e], D ** -0.5, lo, hi, few)
+                    d = (O[at:at + r, j].double().cpu() - o).abs()
+                    assert bool((d <= tol).all()), (i, j)
+                    err2, var, count = err2 + float((d ** 2).sum()), var + float(va.sum()), count + d.numel()
+            at += r
+        assert err2 <= 1.21 * var or count < 4000, (err2 ** 0.5, var ** 0.5)
