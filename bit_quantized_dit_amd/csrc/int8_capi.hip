@@ -41,9 +41,9 @@ w4a4_int8_ws_layout ws_layout(int64_t T, const w4a4_int8_packed* d) {
     size_t off = 0;
     w.a_q = off;     off = align_up(off + (size_t)(round_up(T, 16) * d->k_pad));
     w.a_s = off;     off = align_up(off + (size_t)T * 4);
-    const Int8Plan plan = int8_plan(T, d->d_out, d->k_pad);
-    w.partial = off; off = align_up(off + plan.part_bytes);
-    w.count = off;   off = align_up(off + (plan.few && plan.split > 1 ? INT8_COUNTERS * 4 : 0));
+    const Int8Room room = int8_room(T, d->d_out, d->k_pad);
+    w.partial = off; off = align_up(off + room.part_bytes);
+    w.count = off;   off = align_up(off + (room.counters ? INT8_COUNTERS * 4 : 0));
     w.total = off;
     return w;
 }
@@ -59,8 +59,9 @@ int check_quantize(const void* X, int x_dtype, int64_t T, const w4a4_int8_packed
 }
 
 // The product's counters, which have to be zero when it starts; null where its plan has none.
-int32_t* counters(const w4a4_int8_ws_layout& w, void* ws) {
-    return w.total > w.count ? (int32_t*)((uint8_t*)ws + w.count) : nullptr;
+int32_t* counters(const w4a4_int8_ws_layout& w, void* ws, int64_t T, const w4a4_int8_packed* d) {
+    const Int8Plan plan = int8_plan(T, d->d_out, d->k_pad);
+    return plan.few && plan.split > 1 ? (int32_t*)((uint8_t*)ws + w.count) : nullptr;
 }
 int quantize(const void* X, int x_dtype, int64_t T, const w4a4_int8_packed* d, const w4a4_int8_ws_layout& w, void* ws, int32_t* count,
              hipStream_t stream) {
@@ -69,7 +70,8 @@ int quantize(const void* X, int x_dtype, int64_t T, const w4a4_int8_packed* d, c
 }
 int multiply(const w4a4_int8_ws_layout& w, void* ws, int64_t T, const w4a4_int8_packed* d, void* Y, int y_dtype, hipStream_t stream) {
     uint8_t* b = (uint8_t*)ws;
-    return dev_status(launch_int8_gemm(b + w.a_q, (const float*)(b + w.a_s), T, *d, Y, y_dtype, (int32_t*)(b + w.partial), counters(w, ws), stream));
+    return dev_status(launch_int8_gemm(b + w.a_q, (const float*)(b + w.a_s), T, *d, Y, y_dtype, (int32_t*)(b + w.partial),
+                                       counters(w, ws, T, d), stream));
 }
 
 int describe(int64_t d_in, int64_t d_out, void* blob, size_t blob_bytes, w4a4_int8_packed* out) {
@@ -157,7 +159,7 @@ int w4a4_int8_gemm_prequantized(void* ws, size_t ws_bytes, int64_t T, const w4a4
     if (ws_bytes < w.total) return W4A4_ERR_SHAPE;
     if (T == 0) return W4A4_OK;
     // the codes may come from a call for another layer, whose workspace has its counters elsewhere or none
-    if (int32_t* const count = counters(w, ws)) {
+    if (int32_t* const count = counters(w, ws, T, desc)) {
         const hipError_t e = launch_int8_clear(count, (hipStream_t)stream);
         if (e != hipSuccess) return dev_status(e);
     }
@@ -171,7 +173,7 @@ int w4a4_int8_linear(const void* X, int x_dtype, int64_t T, const w4a4_int8_pack
     w4a4_int8_ws_layout w;
     const int st = check_quantize(X, x_dtype, T, desc, ws, ws_bytes, &w);
     if (st || T == 0) return st;
-    const int q = quantize(X, x_dtype, T, desc, w, ws, counters(w, ws), (hipStream_t)stream);
+    const int q = quantize(X, x_dtype, T, desc, w, ws, counters(w, ws, T, desc), (hipStream_t)stream);
     return q ? q : multiply(w, ws, T, desc, Y, y_dtype, (hipStream_t)stream);
 }
 

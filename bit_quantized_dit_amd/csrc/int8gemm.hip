@@ -446,6 +446,33 @@ Int8Plan int8_plan(int64_t T, int64_t N, int64_t k_pad) {
     return p;
 }
 
+// Few tokens have a plan of their own for 16, 32 and every 64 tokens: looked at one by one.  Tiles have one for
+// every 128 or 256: of many tokens, what tails leave at most, s ranges of each of min(tiles, a round's) tiles.
+Int8Room int8_room(int64_t T, int64_t N, int64_t k_pad) {
+    Int8Room r = {0, false};
+    auto most = [&](int64_t n, const Int8Plan& p) {
+        if ((size_t)n > r.part_bytes) r.part_bytes = (size_t)n;
+        r.counters |= p.few && p.split > 1;
+    };
+    for (int64_t t : {16, 32}) {
+        const Int8Plan p = int8_plan(T < t ? T : t, N, k_pad);
+        most((int64_t)p.part_bytes, p);
+    }
+    for (int64_t t = 64; t - 64 < T && t <= 1024; t += 64) {
+        const Int8Plan p = int8_plan(T < t ? T : t, N, k_pad);
+        most((int64_t)p.part_bytes, p);
+    }
+    const int64_t s = k_pad / 128 / 4 < 16 ? k_pad / 128 / 4 : 16, nb = (N + 255) / 256;
+    if (T <= 1024 || s < 2) return r;
+    const int64_t big = (T + 255) / 256 * nb, small_T = 63 / nb * 256 < T ? 63 / nb * 256 : T;
+    if (small_T > 1024) {
+        const int64_t tiles = (small_T + 127) / 128 * ((N + 127) / 128);
+        most((tiles * s < 512 ? tiles * s : 512) * 128 * 128 * 4, Int8Plan{});
+    }
+    if (big >= 64) most((big * s < 256 ? big * s : 256) * 256 * 256 * 4, Int8Plan{});
+    return r;
+}
+
 hipError_t launch_int8_gemm(const uint8_t* aq, const float* as, int64_t T, const w4a4_int8_packed& d, void* out, int y_dtype, int32_t* part,
                             int32_t* count, hipStream_t st) {
     return y_dtype == W4A4_Y_F32 ? run_out<W4A4_Y_F32>(aq, as, T, d, out, part, count, st)

@@ -119,6 +119,12 @@ struct Int8Plan {
     size_t part_bytes;
 };
 Int8Plan int8_plan(int64_t T, int64_t N, int64_t k_pad);
+// What the plans of up to T tokens take at most, so that a workspace for T tokens serves fewer.
+struct Int8Room {
+    size_t part_bytes;
+    bool counters;
+};
+Int8Room int8_room(int64_t T, int64_t N, int64_t k_pad);
 hipError_t launch_int8_clear(int32_t* count, hipStream_t st);
 hipError_t launch_int8_gemm(const uint8_t* aq, const float* as, int64_t T, const w4a4_int8_packed& d, void* out, int y_dtype,
                             int32_t* part, int32_t* count, hipStream_t st);

@@ -1007,6 +1007,7 @@ def w4a4_int8_workspace_size(T: int, packed: PackedInt8) -> int:
 
 
 def alloc_workspace_int8(T: int, packed: PackedInt8, device="cuda") -> torch.Tensor:
+    """A workspace for calls of up to T tokens."""
     return torch.empty(max(w4a4_int8_workspace_size(T, packed), 256), dtype=torch.uint8, device=device)
 
 

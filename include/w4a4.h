@@ -537,10 +537,10 @@ typedef struct w4a4_int8_ws_layout {
                          rows past T unwritten                                              */
     size_t a_s;       /* fp32 [T] activation scales                                         */
     size_t partial;   /* int32 partial sums of ranges of the inputs (written and read back
-                         within a call; empty when the plan does not split)                 */
-    size_t count;     /* int32 ranges done (of a few tokens' plan that splits; cleared by
+                         within a call; empty when no plan of up to T tokens splits)        */
+    size_t count;     /* int32 ranges done (of few tokens' plans that split; cleared by
                          every call that multiplies)                                        */
-    size_t total;
+    size_t total;     /* does not fall with T: a workspace for T tokens serves fewer too    */
 } w4a4_int8_ws_layout;
 int w4a4_int8_workspace_layout(int64_t T, const w4a4_int8_packed* desc, w4a4_int8_ws_layout* out);
 int w4a4_int8_workspace_size(int64_t T, const w4a4_int8_packed* desc, size_t* bytes);
