@@ -1102,6 +1102,8 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
         p.groups = p.units * p.row_tiles * p.nsplit;
         p.slots = p.nsplit > 1 ? p.units * p.nsplit : 0;
     }
+    // At most W4A4_KV_ATTENTION_WS_MOST: slots * rows are up to 2048 tiles of 256 rows (few rows: 4096 slots of 16, or of up
+    // to 64 in 32 channels), 2^21 d_pad bytes and 2^22; joins and ranges of up to 4096 sequences below 2^18.
     p.o_bytes = up256((size_t)(p.slots * rows) * c.d_pad * 4);
     p.ml_bytes = up256((size_t)(p.slots * rows) * 8);
     p.join_bytes = p.target ? up256((size_t)b.n_seqs * 8) : 0;

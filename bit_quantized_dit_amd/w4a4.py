@@ -1160,6 +1160,12 @@ def w4a4_kv_attention_workspace_size(n_rows: int, batch: KvBatch, n_q_heads: int
     return n.value
 
 
+def w4a4_kv_attention_workspace_most(cache: KvCache) -> int:
+    """Bytes that no attention call over a cache of this head width needs more of (W4A4_KV_ATTENTION_WS_MOST): for one
+    buffer under calls of several shapes, as a call's own size may grow when its batch shrinks."""
+    return (cache.desc.d_pad << 21) + (1 << 23)
+
+
 def alloc_workspace_kv(n_rows: int, batch: KvBatch, n_q_heads: int, cache: KvCache, device="cuda") -> torch.Tensor:
     return torch.empty(max(w4a4_kv_attention_workspace_size(n_rows, batch, n_q_heads, cache), 256), dtype=torch.uint8, device=device)
 

@@ -648,7 +648,10 @@ int w4a4_kv_append(const w4a4_kv_rows* K, const w4a4_kv_rows* V, int64_t n_rows,
  * y_dtype (every code's value is a bf16 and an fp32 number).  Async. */
 int w4a4_kv_read(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache, void* K, void* V, int y_dtype,
                  void* stream);
-/* Bytes of an attention call's workspace: partial results of long sequences' ranges. */
+/* Bytes of an attention call's workspace: partial results of long sequences' ranges.  They follow the plan and may grow as
+ * a batch shrinks (many sequences fill the device whole, fewer are cut): a buffer for calls of several shapes holds the
+ * largest of their sizes, or W4A4_KV_ATTENTION_WS_MOST(cache.d_pad) bytes, which no call needs more of. */
+#define W4A4_KV_ATTENTION_WS_MOST(d_pad) (((size_t)(d_pad) << 21) + ((size_t)1 << 23))
 int w4a4_kv_attention_workspace_size(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache,
                                      int32_t n_q_heads, size_t* bytes);
 /* O device bf16 [n_rows][n_q_heads][head_dim]; scale > 0 (scale log2(e) finite); causal 0 or 1; window >= 0 (0: none;

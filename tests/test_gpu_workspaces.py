@@ -1,4 +1,4 @@
-"""One workspace, for the largest call of a loop, under calls of fewer tokens."""
+"""One workspace under all calls of a loop: fewer tokens, batches that shrink."""
 import pytest
 import torch
 
@@ -23,4 +23,33 @@ def test_int8_calls_of_fewer_tokens(d, n):
         Y.zero_()
         B.w4a4_int8_gemm_prequantized(ws[:size], T, layer, Y)
         assert torch.equal(Y, Z), T
+    assert bool((ws[size:] == 255).all())
+
+
+def test_attention_of_batches_that_shrink():
+    """Decoding with one buffer while sequences end: the results of calls with workspaces of their own."""
+    H, Hq, D, page, n = 8, 40, 128, 64, 300
+    most = 40
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cache = B.kv_cache(n * 2, page, H, D)
+    pages = torch.full((n, most), -1, dtype=torch.int32, device="cuda")
+    pages[:, :2] = torch.randperm(n * 2, device="cuda", generator=g).to(torch.int32).view(n, 2)
+    pages[:3, 2:] = pages[3:3 + 3 * 19, :2].reshape(3, 38)      # three long sequences share the others' pages
+    lens = torch.full((n,), 128, dtype=torch.int32, device="cuda")
+    K, V = (torch.randn(128 * n, H, D, device="cuda", generator=g).bfloat16() for _ in range(2))
+    q_all = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    B.w4a4_kv_append(K, V, B.kv_batch(q_all * 128, lens, pages, max_rows=128), cache)
+    lens[:3] = most * page - 5
+    size = B.w4a4_kv_attention_workspace_most(cache)
+    ws = torch.full((size + 512,), 255, dtype=torch.uint8, device="cuda")
+    Q = torch.randn(n, Hq, D, device="cuda", generator=g).bfloat16()
+    sizes = []
+    for m in (300, 200, 130, 64, 20, 3, 1):
+        b = B.kv_batch(q_all[:m + 1], lens[:m], pages[:m], max_rows=1)
+        O, P = torch.empty_like(Q[:m]), torch.empty_like(Q[:m])
+        sizes.append(B.w4a4_kv_attention_workspace_size(m, b, Hq, cache))
+        B.w4a4_kv_attention(Q[:m], b, cache, O, ws[:size])
+        B.w4a4_kv_attention(Q[:m], b, cache, P, B.alloc_workspace_kv(m, b, Hq, cache))
+        assert torch.equal(O, P) and not bool(torch.isnan(O).any()), m
+    assert any(x < y for x, y in zip(sizes, sizes[1:])), sizes
     assert bool((ws[size:] == 255).all())

@@ -1,6 +1,9 @@
 """Sizes of workspaces over the shapes that a serving loop meets: what a buffer for the largest call has to hold.  No
 call here reaches the GPU."""
 import ctypes
+import os
+import re
+from types import SimpleNamespace
 
 import pytest
 
@@ -11,7 +14,6 @@ FAKE = 0x100000     # an aligned address that host-side logic never reads
 
 @pytest.fixture(scope="module")
 def L():
-    import os
     if not os.path.exists(B.LIB_PATH):
         from bit_quantized_dit_amd import build
         build.build_library()
@@ -33,3 +35,34 @@ def test_int8_workspace_serves_fewer_tokens(L, d_in, d_out):
         before, at = out.total, T
         codes = -(-T // 16) * 16 * d.k_pad + 4 * T
         assert codes <= out.total <= codes + (65 << 20)
+
+
+def test_attention_workspaces_have_a_bound(L):
+    """Sizes grow as batches shrink, but never past what the header names."""
+    n = ctypes.c_size_t()
+
+    def size(seqs, rows, max_pages, c, heads):
+        b = B.W4A4KvBatch(seqs, rows, max_pages, FAKE, FAKE, FAKE)
+        st = L.w4a4_kv_attention_workspace_size(1, b, c, heads, n)
+        assert st in (0, 2)      # 2: more workgroups than a launch counts
+        return n.value if st == 0 else 0
+    with open(os.path.join(os.path.dirname(__file__), "..", "include", "w4a4.h")) as f:
+        macro = re.search(r"define W4A4_KV_ATTENTION_WS_MOST\(d_pad\) (.*)", f.read()).group(1)
+    assert macro == "(((size_t)(d_pad) << 21) + ((size_t)1 << 23))"
+    fell = False
+    for D in (32, 64, 96, 128, 192, 256):
+        for H in (1, 2, 8, 40):
+            c = B.W4A4KvCache()
+            assert L.w4a4_kv_cache_describe(1, 64, H, D, FAKE, B.w4a4_kv_cache_size(1, 64, H, D), c) == 0
+            most = B.w4a4_kv_attention_workspace_most(SimpleNamespace(desc=c))
+            assert most == (c.d_pad << 21) + (1 << 23)
+            for ratio in (1, 5, 16, 64):
+                for rows in (1, 2, 3, 4, 7, 16, 33, 64, 65, 200, 1000, 4096, 60000):
+                    before = 0
+                    for seqs in (1, 2, 3, 5, 13, 31, 64, 65, 100, 127, 128, 250, 500, 1000, 4095, 20000):
+                        for max_pages in (4, 40, 900, 40000):
+                            now = size(seqs, rows, max_pages, c, H * ratio)
+                            assert now <= most, (D, H, ratio, rows, seqs, max_pages)
+                        fell |= now < before
+                        before = now
+    assert fell
