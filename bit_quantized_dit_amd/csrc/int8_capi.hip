@@ -11,8 +11,9 @@ namespace {
 
 // 16 tokens a workgroup of up to 1024 work items, which a launch counts in 32 bits
 constexpr int64_t kMaxT = ((int64_t)1 << 26) - 16;
-// 256 x 256 tiles of outputs: a launch counts its work items, 512 a tile, in 32 bits
-constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 4096;
+// 256 x 256 tiles of outputs: a launch counts its work items, 512 a tile (and up to 512 ranges' besides), in 32 bits
+constexpr int64_t kMaxTiles = W4A4_INT8_MAX_TILES;
+static_assert((kMaxTiles + 512) * 512 < (int64_t)1 << 32, "work items of a launch");
 
 bool valid_x(int t) { return t == W4A4_X_F32 || t == W4A4_X_BF16; }
 bool valid_y(int t) { return t == W4A4_Y_F32 || t == W4A4_Y_BF16; }

@@ -506,10 +506,11 @@ int w4a4_moe_forward(const void* X, int x_dtype, int64_t T, const w4a4_moe* moe,
  *     included, within them).  An output is fl32(fl32(s_x s_w) fl32(sum)), rounded once more
  *     for bf16, so calls are bit-reproducible whatever the shape.
  *   - Limits: 1 <= d_in <= W4A4_INT8_MAX_D_IN, 1 <= d_out <= W4A4_INT8_MAX_D_OUT, up to 2^26 - 16
- *     tokens and 2^39 outputs (W4A4_ERR_SHAPE above).
+ *     tokens and W4A4_INT8_MAX_TILES tiles of 256 x 256 outputs, ceil(T / 256) * ceil(d_out / 256) (W4A4_ERR_SHAPE above).
  * The conventions at the top of this file hold. */
 #define W4A4_INT8_MAX_D_IN 131072
 #define W4A4_INT8_MAX_D_OUT 1048576
+#define W4A4_INT8_MAX_TILES 8384512 /* 2^23 - 4096 */
 
 typedef struct w4a4_int8_packed {
     int64_t d_in, d_out;

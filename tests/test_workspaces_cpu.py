@@ -1,5 +1,5 @@
-"""Sizes of workspaces over the shapes that a serving loop meets: what a buffer for the largest call has to hold.  No
-call here reaches the GPU."""
+"""Sizes of workspaces over the shapes that a serving loop meets: what a buffer for the largest call has to hold; limits
+as the header states them.  No call here reaches the GPU."""
 import ctypes
 import os
 import re
@@ -10,6 +10,11 @@ import pytest
 from bit_quantized_dit_amd import w4a4 as B
 
 FAKE = 0x100000     # an aligned address that host-side logic never reads
+
+
+def _header(name):
+    with open(os.path.join(os.path.dirname(__file__), "..", "include", "w4a4.h")) as f:
+        return re.search(rf"define {name} (.*)", f.read()).group(1)
 
 
 @pytest.fixture(scope="module")
@@ -46,9 +51,7 @@ def test_attention_workspaces_have_a_bound(L):
         st = L.w4a4_kv_attention_workspace_size(1, b, c, heads, n)
         assert st in (0, 2)      # 2: more workgroups than a launch counts
         return n.value if st == 0 else 0
-    with open(os.path.join(os.path.dirname(__file__), "..", "include", "w4a4.h")) as f:
-        macro = re.search(r"define W4A4_KV_ATTENTION_WS_MOST\(d_pad\) (.*)", f.read()).group(1)
-    assert macro == "(((size_t)(d_pad) << 21) + ((size_t)1 << 23))"
+    assert _header(r"W4A4_KV_ATTENTION_WS_MOST\(d_pad\)") == "(((size_t)(d_pad) << 21) + ((size_t)1 << 23))"
     fell = False
     for D in (32, 64, 96, 128, 192, 256):
         for H in (1, 2, 8, 40):
@@ -66,3 +69,17 @@ def test_attention_workspaces_have_a_bound(L):
                         fell |= now < before
                         before = now
     assert fell
+
+
+def test_int8_limits_are_the_headers(L):
+    """Both sides of the largest number of tiles, at the widest layer, the most tokens, and ragged last tiles."""
+    tiles = int(_header("W4A4_INT8_MAX_TILES").split()[0])
+    size = ctypes.c_size_t()
+
+    def status(T, d_out): return L.w4a4_int8_workspace_size(T, _int8(128, d_out), size)
+    for d_out in (1 << 20, (1 << 20) - 255, 7936, 7937, 65536, 65537):
+        nb = -(-d_out // 256)
+        T = min(tiles // nb * 256, (1 << 26) - 16)
+        assert status(T, d_out) == 0, (T, d_out)
+        assert status(T + 1, d_out) == 2, (T, d_out)
+    assert status((1 << 26) - 16, 7936) == 0 and status((1 << 26) - 16, 256 * (tiles >> 18) + 1) == 2
