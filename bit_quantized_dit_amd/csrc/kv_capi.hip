@@ -47,7 +47,7 @@ int check_batch(int64_t n_rows, const w4a4_kv_batch* b, const w4a4_kv_cache* c) 
     if (n_rows < 0 || !b || b->n_seqs < 0 || b->max_rows < 0 || b->max_pages <= 0) return W4A4_ERR_INVALID;
     const int st = check_cache(c);
     if (st) return st;
-    if (!b->q_start || !b->lens || !b->pages) return W4A4_ERR_INVALID;
+    if (b->n_seqs && (!b->q_start || !b->lens || !b->pages)) return W4A4_ERR_INVALID;      // (empty arrays may have no address)
     if (((uintptr_t)b->q_start | (uintptr_t)b->lens | (uintptr_t)b->pages) & 3u) return W4A4_ERR_ALIGN;
     if (n_rows > kMaxRows || b->max_rows > kMaxRows || b->n_seqs > kMaxSeqs || b->max_pages > kMaxTokens / c->page_tokens)
         return W4A4_ERR_SHAPE;

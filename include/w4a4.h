@@ -631,7 +631,7 @@ typedef struct w4a4_kv_batch {
     int64_t n_seqs, max_rows, max_pages;
     const int32_t* q_start;  /* device [n_seqs + 1], not decreasing                         */
     const int32_t* lens;     /* device [n_seqs]                                             */
-    const int32_t* pages;    /* device [n_seqs][max_pages]                                  */
+    const int32_t* pages;    /* device [n_seqs][max_pages]; all three may be null where n_seqs is 0 */
 } w4a4_kv_batch;
 
 /* A [n_rows][heads][head_dim] input with its strides in elements. */

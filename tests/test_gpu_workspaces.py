@@ -53,3 +53,18 @@ def test_attention_of_batches_that_shrink():
         assert torch.equal(O, P) and not bool(torch.isnan(O).any()), m
     assert any(x < y for x, y in zip(sizes, sizes[1:])), sizes
     assert bool((ws[size:] == 255).all())
+
+
+def test_a_batch_without_sequences():
+    """Through the binding, whose empty tensors have no address: nothing is read or written."""
+    cache = B.kv_cache(3, 16, 2, 64)
+    cache.data.fill_(9)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    b = B.kv_batch(torch.zeros(1, **i32), torch.zeros(0, **i32), torch.zeros(0, 4, **i32), max_rows=1)
+    K = torch.ones(5, 2, 64, device="cuda")
+    O, k = torch.full((5, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 2, 64), 7.0, device="cuda")
+    B.w4a4_kv_append(K, K, b, cache)
+    B.w4a4_kv_read(b, cache, k, k.clone())
+    B.w4a4_kv_attention(torch.ones(5, 4, 64, device="cuda"), b, cache, O, B.alloc_workspace_kv(5, b, 4, cache))
+    torch.cuda.synchronize()
+    assert bool((cache.data == 9).all()) and bool((O == 7).all()) and bool((k == 7).all())

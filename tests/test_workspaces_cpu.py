@@ -1,5 +1,5 @@
 """Sizes of workspaces over the shapes that a serving loop meets: what a buffer for the largest call has to hold; limits
-as the header states them.  No call here reaches the GPU."""
+as the header states them; batches without sequences.  No call here reaches the GPU."""
 import ctypes
 import os
 import re
@@ -83,3 +83,17 @@ def test_int8_limits_are_the_headers(L):
         assert status(T, d_out) == 0, (T, d_out)
         assert status(T + 1, d_out) == 2, (T, d_out)
     assert status((1 << 26) - 16, 7936) == 0 and status((1 << 26) - 16, 256 * (tiles >> 18) + 1) == 2
+
+
+def test_batches_without_sequences(L):
+    """Empty arrays have no address: such a batch is nothing to do, not an error."""
+    c, n = B.W4A4KvCache(), ctypes.c_size_t(7)
+    assert L.w4a4_kv_cache_describe(5, 16, 2, 72, FAKE, B.w4a4_kv_cache_size(5, 16, 2, 72), c) == 0
+    rows = B.W4A4KvRows(FAKE, 288, 72, 1, 0)
+    for at in ((None, None, None), (FAKE, None, None), (FAKE, FAKE, FAKE)):
+        b = B.W4A4KvBatch(0, 4, 5, *at)
+        assert L.w4a4_kv_attention_workspace_size(3, b, c, 4, n) == 0 and n.value == 0
+        assert L.w4a4_kv_append(rows, rows, 3, b, c, None) == 0 and L.w4a4_kv_read(3, b, c, FAKE, FAKE, 0, None) == 0
+        assert L.w4a4_kv_attention(rows, 3, b, c, 4, 0.1, 1, 0, FAKE, FAKE, 256, None) == 0
+    b = B.W4A4KvBatch(1, 4, 5, FAKE, None, FAKE)
+    assert L.w4a4_kv_append(rows, rows, 3, b, c, None) == 1
