@@ -932,6 +932,13 @@ def _matrix(t: torch.Tensor, cols: int, name: str) -> int:
     return dt
 
 
+def _int8_here(t: torch.Tensor, name: str, packed: "PackedInt8") -> int:
+    i = _here(t, name)
+    if packed.index != i:
+        raise ValueError(f"{name} is on cuda:{i}, the packed weights on {packed.blob.device}")
+    return i
+
+
 def _buffer(ws: torch.Tensor, device: int) -> None:
     if ws.dtype != torch.uint8:
         raise TypeError(f"ws must be a uint8 buffer, got {ws.dtype}")
@@ -943,7 +950,7 @@ class PackedInt8:
     """INT8 weights with a scale per output channel.  Keeps the device blob alive."""
 
     def __init__(self, blob: torch.Tensor, desc: W4A4Int8Packed):
-        self.blob, self.desc, self.ref = blob, desc, ctypes.byref(desc)
+        self.blob, self.desc, self.ref, self.index = blob, desc, ctypes.byref(desc), blob.get_device()
         self.d_in, self.d_out, self.k_pad, self.n_pad = desc.d_in, desc.d_out, desc.k_pad, desc.n_pad
 
     def views(self) -> dict:
@@ -1020,7 +1027,7 @@ def workspace_int8_views(ws: torch.Tensor, T: int, packed: PackedInt8) -> dict:
 
 
 def w4a4_int8_quantize_activations(X: torch.Tensor, packed: PackedInt8, ws: torch.Tensor, stream=None) -> None:
-    i = _here(X, "X")
+    i = _int8_here(X, "X", packed)
     dt = _matrix(X, packed.d_in, "X")
     _buffer(ws, i)
     T = X.shape[0]
@@ -1030,7 +1037,7 @@ def w4a4_int8_quantize_activations(X: torch.Tensor, packed: PackedInt8, ws: torc
 
 
 def w4a4_int8_gemm_prequantized(ws: torch.Tensor, T: int, packed: PackedInt8, Y: torch.Tensor, stream=None) -> None:
-    i = _here(Y, "Y")
+    i = _int8_here(Y, "Y", packed)
     dt = _matrix(Y, packed.d_out, "Y")
     _buffer(ws, i)
     if Y.shape[0] != T:
@@ -1041,7 +1048,7 @@ def w4a4_int8_gemm_prequantized(ws: torch.Tensor, T: int, packed: PackedInt8, Y:
 
 
 def w4a4_int8_linear(X: torch.Tensor, packed: PackedInt8, Y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
-    i = _here(X, "X")
+    i = _int8_here(X, "X", packed)
     dx, dy = _matrix(X, packed.d_in, "X"), _matrix(Y, packed.d_out, "Y")
     _buffer(ws, i)
     T = X.shape[0]
