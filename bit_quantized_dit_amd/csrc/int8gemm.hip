@@ -108,9 +108,9 @@ __device__ __forceinline__ void store_tiles(const v16i (&acc)[FT][FF], uint8_t* 
     }
 }
 
-// Bound by the board's power: 57600 x 5120 -> 5120 settles at 1316 us, 2.29 PO/s, with the clock at 1.72 GHz and the matrix
-// unit busy in 61% of the cycles (the library's product of the same size 1324).  Tiles of 128 x 128 a wavefront, four
-// wavefronts a workgroup, have fewer fragment reads and take 1484: one wavefront a SIMD does not cover its own waits.
+// Bound by the board's power: 57600 x 5120 -> 5120 settles at 1264 us, 2.39 PO/s, with the matrix unit busy in 65% of the
+// cycles (1316 on another card, where the library's product of the same size took 1324).  Tiles of 128 x 128 a wavefront, four
+// wavefronts a workgroup, have fewer fragment reads and took 1484 there: one wavefront a SIMD does not cover its own waits.
 //
 // A workgroup of WT x WF wavefronts owns (WT FT 32) tokens x (WF FF 32) features, a wavefront FT x FF
 // tiles of 32 x 32 whose sums stay in its accumulators.  The K loop walks blocks of 128 inputs
@@ -263,11 +263,12 @@ __global__ __launch_bounds__(64) void int8_reduce_kernel(const float* __restrict
 
 // ---------------------------------------------------------------- few tokens
 //
-// Bound by reading the weight codes once (one token, 5120 -> 13824: 71 MB in 13.0 us, 5.4 TB/s with the start), for
+// Bound by reading the weight codes once (one token, 5120 -> 13824: 71 MB in 13.8 us, 5.1 TB/s with the start), for
 // 65 to 1024 tokens of middling layers by the CUs' load path, as every 16 weight rows read all tokens' codes.  A workgroup owns RT tiles of 16 weight rows; its eight
 // wavefronts take every eighth block of 128 inputs and multiply codes straight from memory with
 // up to NT tiles of 16 tokens; the eight partial sums meet in LDS.  gridDim.z ranges of the inputs
-// keep the CUs filled where there are few row tiles; the last one done adds them.
+// keep the CUs filled where there are few row tiles; the last one done adds them.  (33 to 64 tokens by two row tiles: sums and
+// flag are 81924 bytes of LDS, so that a CU has one workgroup; 64 tokens 5120 -> 13824 25 us a call, 32 tokens 16.)
 __device__ __forceinline__ void put_int(int32_t* p, int32_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ int32_t get_int(const int32_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 

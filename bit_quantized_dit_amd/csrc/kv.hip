@@ -3,8 +3,8 @@
 //   c = max(floor(log2 amax) - 2 + 127, 0) of 32 channels (0xFF for a NaN or Inf), code =
 //   e2m1(x / 2^(c - 127)), nearest, ties to even, saturating at 6
 //
-// Bound by memory (a prompt of 57600 rows, 40 heads of 128, bf16: written in 273 us, read back in 258, 1.49 GB each, 5.5 and
-// 5.8 TB/s) or by the launch (64 rows of 8 heads: 4.2 and 3.5 us).  A wavefront owns a block of 16 tokens
+// Bound by memory (a prompt of 57600 rows, 40 heads of 128, bf16: written in 274 us, read back in 257, 1.49 GB each, 5.4 and
+// 5.8 TB/s) or by the launch (64 rows of 8 heads: 4.5 and 3.5 us).  A wavefront owns a block of 16 tokens
 // of one head, keys and values, and goes through its rows in items of 8 channels, neighbouring lanes on
 // neighbouring items, so that rows are read and written in whole lines.  The block's bytes, which lie in the
 // attention's order (value codes four tokens to a dword), pass through LDS.  Blocks that the call covers in

@@ -219,8 +219,8 @@ __device__ __forceinline__ void store_out4(uint16_t* row, int d, int D, v4f v) {
 
 // ---------------------------------------------------------------- few rows
 //
-// Up to 16 MT stacked rows: bound by reading the cache (64 ragged sequences of 8 heads and 1.16 GB: 205 us, 5.6 TB/s;
-// one row of 40 heads over 57600 tokens, 313 MB: 57 us, 5.5 TB/s; a kernel that only reads reaches 6.1), or, for a
+// Up to 16 MT stacked rows: bound by reading the cache (kernel times: 64 ragged sequences of 8 heads and 1.16 GB 201 us, 5.8 TB/s;
+// one row of 40 heads over 57600 tokens, 313 MB, 58 us, 5.4 TB/s; a kernel that only reads reaches 6.1), or, for a
 // few hundred tokens, by the latency of its dependent loads (9 us).  The tiles are those of the 16-row instruction,
 // as a sequence's one row and its ratio of heads seldom fill more.  The matrix unit has time to spare, so weights are
 // multiplied as two bf16 terms (16 bits) and their rounding does not show.  A wavefront takes every NW-th step of
@@ -230,7 +230,9 @@ __device__ __forceinline__ void store_out4(uint16_t* row, int d, int D, v4f v) {
 // are workgroups of 8 wavefronts.  The copies past the last step run with empty ranges, so that every wait counts the same number.  The wavefronts'
 // results meet in LDS.
 // (One wavefront a SIMD has its sums copied between register files at every use: 64 rows of 40 heads of 72 over 57600 tokens 170 us,
-// with two and 52 bytes in scratch 133; 20 rows of 192 channels 143 and 103.  Heads of 256 do not fit: 20 rows 326, with two 363.)
+// with two and 52 bytes in scratch 133; 20 rows of 192 channels 143 and 103.  Heads of 256 do not fit: 20 rows 326, with two 363,
+// and 140 bytes of 32 rows are in scratch.  Four wavefronts a SIMD put 152 bytes of 64 rows of up to 32 channels into scratch, and 16
+// of 32 rows of up to 64; not measured against fewer.)
 template <int G, int MT> struct Few {      // wavefronts of a workgroup, steps of a ring, wavefronts a SIMD (for the register budget)
     static constexpr int NW = 4, R = 2, OCC = G * MT <= 4 ? 4 : G * MT <= 12 ? 2 : 1;
     static constexpr int COPIES = (KvBlock<G>::BYTES + 1023) / 1024, STEP = 2 * KvBlock<G>::BYTES, LD = 32 * G + 4;
@@ -520,8 +522,8 @@ __global__ __launch_bounds__((Few<G, MT>::NW * 64), (Few<G, MT>::OCC)) void kv_f
 // ---------------------------------------------------------------- many rows
 //
 // Bound by the matrix unit, the vector unit's softmax and widening beside it, and the board's power: 4096 rows of 40
-// heads over 57600 tokens 4278 us, 1.13 PFLOP/s at 2.07 GHz, matrix unit 51% of the cycles (a large bf16 product
-// of the library: 1.24; without the widening 3860, without the exponentials 4040, without either 3290).  So weights are one
+// heads over 57600 tokens 4.27 to 4.33 ms, 1.12 PFLOP/s, matrix unit 52% of the cycles (a large bf16 product
+// of the library: 1.24; of 4.28, without the widening 3.86, without the exponentials 4.04, without either 3.29).  So weights are one
 // bf16 term here: two would double the second product.  TWO: of up to 64 stacked rows of heads of 97 to 128 channels, which
 // the few-row kernel has no registers for, they are two terms as there (64 rows of 40 heads over 57600 tokens 212 us, with one
 // 196; 64 sequences of 40 rows, 8 heads, 2048 tokens 94; error against 64 bits 0.0016 and 0.0023).
@@ -1081,8 +1083,8 @@ Plan plan_of(const w4a4_kv_batch& b, const w4a4_kv_cache& c, int32_t n_q_heads, 
         // (tokens that start and end inside a step: two steps more)
         const int64_t most = p.units * ((cap / 32 + 2 + FEW_LEAST - 1) / FEW_LEAST), round = few_round(c.d_pad / 32, p.mt);
         // One round of workgroups where few sequences leave most of it to full ranges (one row over 57600
-        // tokens, 40 heads: least of 90 calls 55 us, in two rounds 58); else about two, whose ranges are shorter, so that
-        // the last ones end closer together (64 ragged sequences: 194 us, in one round 213).  Sequences that fill the CUs by
+        // tokens, 40 heads: least kernel time of 90 calls 55 us, in two rounds 58); else about two, whose ranges are shorter, so that
+        // the last ones end closer together (64 ragged sequences: least 194 us, in one round 213).  Sequences that fill the CUs by
         // themselves stay whole.
         const int64_t target = p.units <= round / 4 ? round - p.units : p.units < round ? 2 * round - p.units : round;
         p.groups = p.units;

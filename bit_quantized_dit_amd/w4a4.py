@@ -1179,8 +1179,9 @@ def alloc_workspace_kv(n_rows: int, batch: KvBatch, n_q_heads: int, cache: KvCac
 
 def w4a4_kv_attention(Q: torch.Tensor, batch: KvBatch, cache: KvCache, O: torch.Tensor, ws: torch.Tensor, scale: float | None = None,
                       causal: bool = True, window: int = 0, stream=None) -> None:
-    """Q [rows, n_q_heads, head_dim] float32 or bfloat16; O bfloat16, contiguous, of Q's shape;
-    scale None: 1 / sqrt(head_dim)."""
+    """Q [rows, n_q_heads, head_dim] float32 (rounded to bfloat16) or bfloat16; O bfloat16, contiguous, of Q's shape;
+    scale None: 1 / sqrt(head_dim).  batch.max_rows chooses one kernel for all sequences: decoding rows and prompts
+    are two calls."""
     if Q.dim() != 3:
         raise ValueError(f"Q must be [rows, n_q_heads, {cache.head_dim}], got {tuple(Q.shape)}")
     n, heads, _ = shape = Q.shape

@@ -585,7 +585,7 @@ int w4a4_int8_linear(const void* X, int x_dtype, int64_t T, const w4a4_int8_pack
  *   - q_start is clamped to 0 .. n_rows; of a sequence with more than max_rows rows only the
  *     first max_rows are computed (all its rows count for the positions);
  *   - lens is clamped to 0 .. max_pages * page_tokens;
- *   - a position below zero is not stored, reads back as zero, and its row sees nothing;
+ *   - a position below zero is not stored, reads back as zero, and its row sees nothing if causal;
  *   - a page number outside 0 .. n_pages - 1 is a page that is not there: its tokens are not
  *     stored, read back as zero, and no row sees them.
  * No two rows of a call may name the same token of the cache.
@@ -603,6 +603,9 @@ int w4a4_int8_linear(const void* X, int x_dtype, int64_t T, const w4a4_int8_pack
  *     sums' p_t are up to 2^16, so that outputs are finite where |v| < 2^112 / (tokens).  The p_t are rounded to bf16 (for sequences of
  *     up to W4A4_KV_FEW_ROWS stacked rows, max_rows * (n_q_heads / n_heads), half as many where d_pad
  *     is above 128: to two bf16 terms, 16 bits) where they are multiplied with the values.
+ *   - max_rows chooses one kernel for the whole batch: sequences of few rows beside one of many run, and are rounded, as
+ *     those of many do, and are not cut into ranges of their own.  Decoding rows and prompts are therefore two calls.
+ *   - Queries given in binary32 are rounded to bf16, as the formula says; O is bf16.
  *   - Results depend on the sequences, not on where their pages are; the order of sums depends on
  *     shape and lengths only, so calls are bit-reproducible.
  *
@@ -651,7 +654,8 @@ int w4a4_kv_read(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache
                  void* stream);
 /* Bytes of an attention call's workspace: partial results of long sequences' ranges.  They follow the plan and may grow as
  * a batch shrinks (many sequences fill the device whole, fewer are cut): a buffer for calls of several shapes holds the
- * largest of their sizes, or W4A4_KV_ATTENTION_WS_MOST(cache.d_pad) bytes, which no call needs more of. */
+ * largest of their sizes, or W4A4_KV_ATTENTION_WS_MOST(cache.d_pad) bytes, which no call needs more of.  ws is an address
+ * also where the size is 0. */
 #define W4A4_KV_ATTENTION_WS_MOST(d_pad) (((size_t)(d_pad) << 21) + ((size_t)1 << 23))
 int w4a4_kv_attention_workspace_size(int64_t n_rows, const w4a4_kv_batch* batch, const w4a4_kv_cache* cache,
                                      int32_t n_q_heads, size_t* bytes);
